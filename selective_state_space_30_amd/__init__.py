@@ -26,6 +26,14 @@ Names follow the C ABI:
   the backward (which then skips its own checkpoint pass).
 * :func:`ssm_conv_scan_bwd` -- gradients of :func:`ssm_conv_scan_fwd`,
   through the conv prologue as well; :func:`ssm_conv_scan_bwd_workspace_size`.
+* :func:`ssm_linattn_fwd`, :func:`ssm_linattn_bwd`, :func:`ssm_linattn_step`
+  -- linear attention with a decay for each head (``include/ssm_linattn.h``):
+  whole or packed sequences, their gradients, and one token on states kept
+  in slots; :func:`ssm_linattn_plan`, :func:`ssm_linattn_workspace_size`,
+  :func:`ssm_linattn_bwd_workspace_size`.
+* :func:`ssm_block_norm_fwd`, :func:`ssm_block_norm_bwd` -- the norms after a
+  mixer and before the next block fused with gate, scale and residual, and
+  their gradients; :func:`ssm_block_norm_bwd_workspace_size`.
 * :func:`ssm_scan_plan`, :func:`ssm_scan_workspace_size`,
   :func:`ssm_last_error`, :func:`ssm_abi_version`.
 * :func:`ssm_roofline_hbm`, :func:`ssm_roofline_valu` -- microbenchmarks of
@@ -50,6 +58,7 @@ SSM_DTYPE_BF16 = 1
 SSM_FLAG_DELTA_SOFTPLUS = 1
 SSM_FLAG_ZOH_B = 2
 SSM_FLAG_BWD_SAVED = 4
+SSM_FLAG_HEAD_DECAY = 8
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_INVALID_ARG", 2: "SSM_ERR_UNSUPPORTED",
           3: "SSM_ERR_WORKSPACE", 4: "SSM_ERR_HIP"}
 EXPORTS = ("ssm_abi_version", "ssm_scan_plan", "ssm_scan_workspace_size",
@@ -59,7 +68,11 @@ EXPORTS = ("ssm_abi_version", "ssm_scan_plan", "ssm_scan_workspace_size",
            "ssm_scan_bwd",
            "ssm_ssd_workspace_size", "ssm_ssd_fwd", "ssm_last_error",
            "ssm_roofline_hbm", "ssm_roofline_valu", "ssm_scan_fwd_noalloc",
-           "ssm_conv_scan_bwd_workspace_size", "ssm_conv_scan_bwd")
+           "ssm_conv_scan_bwd_workspace_size", "ssm_conv_scan_bwd",
+           "ssm_linattn_plan", "ssm_linattn_workspace_size", "ssm_linattn_fwd",
+           "ssm_linattn_bwd_workspace_size", "ssm_linattn_bwd", "ssm_linattn_step",
+           "ssm_block_norm_fwd", "ssm_block_norm_bwd_workspace_size",
+           "ssm_block_norm_bwd")
 SCAN_SCRATCH_BYTES = 16 << 20  # the fixed scratch of ssm_scan_fwd_noalloc
 SSM_ROOFLINE_HBM_QUANTUM = 16384
 SSM_ROOFLINE_VALU_QUANTUM = 256
@@ -146,6 +159,35 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.ssm_roofline_hbm.restype = I
         lib.ssm_roofline_valu.argtypes = [I, P, I64, I, P]
         lib.ssm_roofline_valu.restype = I
+        SZ, F = ctypes.c_size_t, ctypes.c_float
+        side = [P, I64]
+        lib.ssm_linattn_plan.argtypes = [I64, I64, I, I64, I64, I64, I, I,
+                                         ctypes.POINTER(I64)]
+        lib.ssm_linattn_plan.restype = I
+        lib.ssm_linattn_workspace_size.argtypes = [I64, I64, I, I64, I64, I64,
+                                                   I, ctypes.POINTER(SZ)]
+        lib.ssm_linattn_workspace_size.restype = I
+        lib.ssm_linattn_fwd.argtypes = (side * 3 + [P, U, F, P, P, P, P] +
+                                        [I64] * 6 + [I, P, SZ, P])
+        lib.ssm_linattn_fwd.restype = I
+        lib.ssm_linattn_bwd_workspace_size.argtypes = [
+            I64, I64, I, I64, I64, I64, I64, I, I, ctypes.POINTER(SZ)]
+        lib.ssm_linattn_bwd_workspace_size.restype = I
+        lib.ssm_linattn_bwd.argtypes = (side * 3 + [P, U, F] + [P] * 9 +
+                                        [I64] * 6 + [I, P, SZ, P])
+        lib.ssm_linattn_bwd.restype = I
+        lib.ssm_linattn_step.argtypes = ([P] + side * 3 + [P, U, F, P, P] +
+                                         [I64] * 6 + [I, P])
+        lib.ssm_linattn_step.restype = I
+        norm = side + [P] + side + [P] + side + [P]
+        lib.ssm_block_norm_fwd.argtypes = norm + [P, P, I64, I64, I64, F, I, I, P]
+        lib.ssm_block_norm_fwd.restype = I
+        lib.ssm_block_norm_bwd_workspace_size.argtypes = [I64, I64,
+                                                          ctypes.POINTER(SZ)]
+        lib.ssm_block_norm_bwd_workspace_size.restype = I
+        lib.ssm_block_norm_bwd.argtypes = (norm + [P] * 8 +
+                                           [I64, I64, I64, F, I, I, P, SZ, P])
+        lib.ssm_block_norm_bwd.restype = I
         lib.ssm_last_error.argtypes = []
         lib.ssm_last_error.restype = ctypes.c_char_p
         if path is None:
@@ -723,3 +765,346 @@ def ssm_roofline_valu(kind, out, iters, stream=None):
     _check(load_library().ssm_roofline_valu(
         code, _ptr(out, "out", torch.float32), out.numel(), iters,
         _stream_handle(out.device, stream)))
+
+
+# ---------------------------------------------------------- linear attention
+def _on_device(fn):
+    """Runs the wrapper with its first argument's device as the current one
+    (kernels are launched on the current device), and with ``stream`` (when
+    given) as torch's current stream, as :func:`_on_stream` does."""
+    inner = _on_stream(fn)
+    first = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def wrapper(*args, **kwargs):
+        t = args[0] if args else kwargs.get(first)
+        call = fn if kwargs.get("stream") is None else inner
+        if (isinstance(t, torch.Tensor) and t.is_cuda
+                and t.device.index != torch.cuda.current_device()):
+            with torch.cuda.device(t.device):
+                return call(*args, **kwargs)
+        return call(*args, **kwargs)
+    return wrapper
+
+
+def _rows(t, name, dtype, lead, tail, dev):
+    """Address and row stride of a tensor of shape ``lead + tail`` whose rows
+    (the last dimensions, ``tail``) are dense and whose leading dimensions
+    step through rows at one stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != lead + tail:
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, lead + tail, tuple(t.shape)))
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if dev.type != "cuda":
+        raise ValueError("%s must be a device (HIP) tensor" % name)
+    row = 1
+    for n in tail:
+        row *= n
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    st, want = t.stride(), 1
+    for n, s in zip(reversed(tail), reversed(st[len(lead):])):
+        if n != 1 and s != want:
+            raise ValueError("%s: the elements of a row must be contiguous" % name)
+        want *= n
+    step = None
+    rows = 1
+    for n, s in zip(reversed(lead), reversed(st[:len(lead)])):
+        if n != 1:
+            if step is None:
+                step = s
+            elif s != step * rows:
+                raise ValueError("%s: rows must be one stride apart" % name)
+            rows *= n
+    step = row if step is None else step
+    if step < row:
+        raise ValueError("%s: rows overlap" % name)
+    return t.data_ptr(), step
+
+
+def _size(fn, *args):
+    out = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(out)))
+    return out.value
+
+
+def _scratch(workspace, need, dev):
+    """(tensor, address, bytes) of a workspace of ``need`` bytes: the given
+    one, or a new one."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on %s" % dev)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _code(dtype):
+    if dtype == torch.bfloat16:
+        return SSM_DTYPE_BF16
+    if dtype == torch.float32:
+        return SSM_DTYPE_F32
+    raise TypeError("activations must be float32 or bfloat16, got %s" % dtype)
+
+
+def ssm_linattn_plan(tokens, nseq, heads, qk_dim, v_dim, dtype=torch.bfloat16,
+                     packed=False, backward=False) -> dict:
+    """How :func:`ssm_linattn_fwd` (or the backward) cuts the sequences:
+    tokens per segment, segments, tokens per chunk, and whether a pass over
+    k and v forms the states between segments."""
+    out = (ctypes.c_int64 * 4)()
+    _check(load_library().ssm_linattn_plan(tokens, nseq, int(packed), heads,
+                                           qk_dim, v_dim, _code(dtype),
+                                           int(backward), out))
+    return {"segment": out[0], "segments": out[1], "chunk": out[2],
+            "state_pass": bool(out[3])}
+
+
+def ssm_linattn_workspace_size(tokens, nseq, heads, qk_dim, v_dim,
+                               dtype=torch.bfloat16, packed=False) -> int:
+    return _size(load_library().ssm_linattn_workspace_size, tokens, nseq,
+                 int(packed), heads, qk_dim, v_dim, _code(dtype))
+
+
+def ssm_linattn_bwd_workspace_size(tokens, nseq, heads, qk_heads, qk_dim, v_dim,
+                                   dtype=torch.bfloat16, packed=False,
+                                   want_dg=0) -> int:
+    """``want_dg``: 0 without dg, 1 for a decay a token, 2 for one a head."""
+    return _size(load_library().ssm_linattn_bwd_workspace_size, tokens, nseq,
+                 int(packed), heads, qk_heads, qk_dim, v_dim, _code(dtype),
+                 want_dg)
+
+
+class _Linattn:
+    """The checked arguments that the linear-attention calls share."""
+
+    __slots__ = ("dev", "act", "lead", "tokens", "nseq", "heads", "qk_heads",
+                 "dk", "dv", "code", "qkv", "g", "flags", "scale", "h0", "cu",
+                 "states")
+
+    def __init__(self, q, k, v, g, scale, h0, cu_seqlens, step=False):
+        if not (isinstance(q, torch.Tensor) and isinstance(v, torch.Tensor)):
+            raise TypeError("q and v must be torch.Tensors")
+        flat = step or cu_seqlens is not None
+        if q.dim() != (3 if flat else 4) or v.dim() != q.dim():
+            raise ValueError("q, k, v must be %s" % (
+                "(batch, heads, dim)" if step else "(tokens, heads, dim) with cu_seqlens"
+                if flat else "(batch, seqlen, heads, dim)"))
+        self.dev, self.act = q.device, q.dtype
+        self.code = _code(q.dtype)
+        lead = self.lead = tuple(v.shape[:-2])
+        self.heads, self.dv = v.shape[-2:]
+        self.qk_heads, self.dk = q.shape[-2:]
+        self.tokens = lead[0] if flat else lead[0] * lead[1]
+        dev, act = self.dev, self.act
+        qk = (self.qk_heads, self.dk)
+        self.qkv = (_rows(q, "q", act, lead, qk, dev) + _rows(k, "k", act, lead, qk, dev) +
+                    _rows(v, "v", act, lead, (self.heads, self.dv), dev))
+        self.flags = 0
+        if g is not None and g.dim() == 1:
+            self.flags = SSM_FLAG_HEAD_DECAY
+            self.g = _ptr(g, "g", torch.float32, (self.heads,), dev)
+        else:
+            self.g = _ptr(g, "g", torch.float32, lead + (self.heads,), dev)
+        self.scale = self.dk ** -0.5 if scale is None else float(scale)
+        self.cu = None
+        self.nseq = 0 if step else lead[0]
+        if not step and cu_seqlens is not None:
+            if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+                raise ValueError("cu_seqlens must be (sequences + 1,)")
+            self.nseq = cu_seqlens.shape[0] - 1
+            self.cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (self.nseq + 1,), dev)
+        self.states = (self.nseq, self.heads, self.dk, self.dv)
+        self.h0 = _ptr(h0, "h0", torch.float32, self.states, dev)
+
+
+@_on_device
+def ssm_linattn_fwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
+                    return_final_state=True, o=None, h_final=None,
+                    workspace=None, stream=None):
+    """Linear attention with a decay for each head, per sequence and head:
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale * S_t^T q_t.
+
+    q, k: (batch, seqlen, qk_heads, qk_dim); v: (batch, seqlen, heads, v_dim),
+    float32 or bfloat16; value head h uses query/key head
+    h // (heads // qk_heads).  g: log decay, fp32 (batch, seqlen, heads), or
+    (heads,) for a fixed one, or None.  scale: qk_dim ** -0.5 by default.
+    h0: (batch, heads, qk_dim, v_dim) fp32 or None.  With ``cu_seqlens``
+    (int32, device, sequences + 1 row offsets) the sequences are packed: q, k,
+    v (and g) have one leading dimension, tokens, and states one per
+    sequence; rows outside the sequences are left as they are.  q, k and v
+    may be slices of wider rows.  Returns ``(o, h_final)``."""
+    a = _Linattn(q, k, v, g, scale, h0, cu_seqlens)
+    lib = load_library()
+    if o is None:
+        o = torch.empty(a.lead + (a.heads, a.dv), dtype=a.act, device=a.dev)
+    if not return_final_state:
+        h_final = None
+    elif h_final is None:
+        h_final = torch.empty(a.states, dtype=torch.float32, device=a.dev)
+    need = _size(lib.ssm_linattn_workspace_size, a.tokens, a.nseq, a.cu is not None,
+                 a.heads, a.dk, a.dv, a.code)
+    keep, ws, ws_bytes = _scratch(workspace, need, a.dev)
+    _check(lib.ssm_linattn_fwd(
+        *a.qkv, a.g, a.flags, a.scale, a.h0, a.cu,
+        _ptr(o, "o", a.act, a.lead + (a.heads, a.dv), a.dev),
+        _ptr(h_final, "h_final", torch.float32, a.states, a.dev),
+        a.tokens, a.nseq, a.heads, a.qk_heads, a.dk, a.dv, a.code, ws, ws_bytes,
+        _stream_handle(a.dev, stream)))
+    return o, h_final
+
+
+@_on_device
+def ssm_linattn_bwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
+                    do=None, dh_final=None, want_dg=True, want_dh0=True,
+                    out=None, workspace=None, stream=None):
+    """Gradients of :func:`ssm_linattn_fwd` for a loss with gradient ``do``
+    (like o) and ``dh_final`` (like h_final, or None).  Returns a dict: dq,
+    dk, dv (activation dtype; dq and dk summed over the value heads that share
+    a query/key head), dg (fp32, like g; when g is given) and dh0 (fp32).
+    ``out`` may supply any of them."""
+    if do is None:
+        raise ValueError("do is required")
+    a = _Linattn(q, k, v, g, scale, h0, cu_seqlens)
+    lib = load_library()
+    f32 = torch.float32
+    shapes = {"dq": (a.lead + (a.qk_heads, a.dk), a.act),
+              "dk": (a.lead + (a.qk_heads, a.dk), a.act),
+              "dv": (a.lead + (a.heads, a.dv), a.act)}
+    if g is not None and want_dg:
+        shapes["dg"] = (tuple(g.shape), f32)
+    if want_dh0:
+        shapes["dh0"] = (a.states, f32)
+    out = dict(out or {})
+    p = {}
+    for name, (shape, dtype) in shapes.items():
+        if name not in out:
+            out[name] = torch.empty(shape, dtype=dtype, device=a.dev)
+        p[name] = _ptr(out[name], name, dtype, shape, a.dev)
+    kind = 0 if "dg" not in shapes else 2 if a.flags else 1
+    need = _size(lib.ssm_linattn_bwd_workspace_size, a.tokens, a.nseq, a.cu is not None,
+                 a.heads, a.qk_heads, a.dk, a.dv, a.code, kind)
+    keep, ws, ws_bytes = _scratch(workspace, need, a.dev)
+    _check(lib.ssm_linattn_bwd(
+        *a.qkv, a.g, a.flags, a.scale, a.h0, a.cu,
+        _ptr(do, "do", a.act, a.lead + (a.heads, a.dv), a.dev),
+        _ptr(dh_final, "dh_final", f32, a.states, a.dev),
+        p["dq"], p["dk"], p["dv"], p.get("dg"), p.get("dh0"),
+        a.tokens, a.nseq, a.heads, a.qk_heads, a.dk, a.dv, a.code, ws, ws_bytes,
+        _stream_handle(a.dev, stream)))
+    return {name: out[name] for name in shapes}
+
+
+@_on_device
+def ssm_linattn_step(state, q, k, v, g=None, scale=None, slots=None, o=None,
+                     stream=None):
+    """One token of a batch: advances ``state`` (nslots, heads, qk_dim,
+    v_dim) fp32 in place and returns o (batch, heads, v_dim).  q, k: (batch,
+    qk_heads, qk_dim); v: (batch, heads, v_dim); g: (batch, heads), (heads,)
+    or None.  ``slots``: int32 (batch,), the state of each row (row b's is b
+    without it); a row whose slot is negative, too large or already an
+    earlier row's changes nothing and gets o = 0."""
+    a = _Linattn(q, k, v, g, scale, None, None, step=True)
+    if state.dim() != 4:
+        raise ValueError("state must be (nslots, heads, qk_dim, v_dim)")
+    nslots = state.shape[0]
+    if o is None:
+        o = torch.empty(a.lead + (a.heads, a.dv), dtype=a.act, device=a.dev)
+    _check(load_library().ssm_linattn_step(
+        _ptr(state, "state", torch.float32, (nslots, a.heads, a.dk, a.dv), a.dev),
+        *a.qkv, a.g, a.flags, a.scale,
+        _ptr(slots, "slots", torch.int32, a.lead, a.dev),
+        _ptr(o, "o", a.act, a.lead + (a.heads, a.dv), a.dev),
+        a.tokens, nslots, a.heads, a.qk_heads, a.dk, a.dv, a.code,
+        _stream_handle(a.dev, stream)))
+    return o
+
+
+# ---------------------------------------------------------------- block norm
+def ssm_block_norm_bwd_workspace_size(rows, dim) -> int:
+    return _size(load_library().ssm_block_norm_bwd_workspace_size, rows, dim)
+
+
+def _norm_args(x, w_post, z, scale, residual, w_pre):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor (..., dim)")
+    dev, act, f32 = x.device, x.dtype, torch.float32
+    code = _code(act)
+    lead, dim = tuple(x.shape[:-1]), x.shape[-1]
+    rows = 1
+    for n in lead:
+        rows *= n
+    rdt = act if residual is None else residual.dtype
+    rcode = _code(rdt)
+
+    def side(t, name, dtype):
+        return (None, 0) if t is None else _rows(t, name, dtype, lead, (dim,), dev)
+
+    args = (side(x, "x", act) + (_ptr(w_post, "w_post", f32, (dim,), dev),) +
+            side(z, "z", act) + (_ptr(scale, "scale", f32, (dim,), dev),) +
+            side(residual, "residual", rdt) + (_ptr(w_pre, "w_pre", f32, (dim,), dev),))
+    return args, rows, dim, code, rcode, rdt
+
+
+@_on_device
+def ssm_block_norm_fwd(x, w_post=None, z=None, scale=None, residual=None,
+                       w_pre=None, groups=1, eps=1e-5, r=None, y=None,
+                       stream=None):
+    """The end of a block and the start of the next in one pass, per row:
+    n = rmsnorm of each of ``groups`` parts of x, times w_post (n = x without
+    w_post); r = residual + n * silu(z) * scale (each optional); y =
+    rmsnorm(r) * w_pre (None without w_pre).  x, z: (..., dim), float32 or
+    bfloat16; residual: the same or float32, and r with it; w_post, scale,
+    w_pre: (dim,) fp32.  x, z and residual may be slices of wider rows.
+    ``r`` may be the residual itself (in place).  Returns ``(r, y)``."""
+    args, rows, dim, code, rcode, rdt = _norm_args(x, w_post, z, scale, residual, w_pre)
+    if r is None:
+        r = torch.empty(x.shape, dtype=rdt, device=x.device)
+    if w_pre is None:
+        y = None
+    elif y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check(load_library().ssm_block_norm_fwd(
+        *args, _ptr(r, "r", rdt, x.shape, x.device), _ptr(y, "y", x.dtype, x.shape, x.device),
+        rows, dim, groups, eps, code, rcode, _stream_handle(x.device, stream)))
+    return r, y
+
+
+@_on_device
+def ssm_block_norm_bwd(x, w_post=None, z=None, scale=None, residual=None,
+                       w_pre=None, groups=1, eps=1e-5, dr=None, dy=None,
+                       out=None, workspace=None, stream=None):
+    """Gradients of :func:`ssm_block_norm_fwd`, from its inputs, for gradients
+    ``dr`` of r (or None) and ``dy`` of y (with w_pre).  Returns a dict: dx,
+    and for each input given dw_post, dz, dscale, dresidual, dw_pre.  ``out``
+    may supply any of them."""
+    args, rows, dim, code, rcode, rdt = _norm_args(x, w_post, z, scale, residual, w_pre)
+    dev, act, f32 = x.device, x.dtype, torch.float32
+    shapes = {"dx": (x.shape, act)}
+    for name, t, like in (("dw_post", w_post, ((dim,), f32)), ("dz", z, (x.shape, act)),
+                          ("dscale", scale, ((dim,), f32)),
+                          ("dresidual", residual, (x.shape, rdt)),
+                          ("dw_pre", w_pre, ((dim,), f32))):
+        if t is not None:
+            shapes[name] = like
+    out = dict(out or {})
+    p = {}
+    for name, (shape, dtype) in shapes.items():
+        if name not in out:
+            out[name] = torch.empty(shape, dtype=dtype, device=dev)
+        p[name] = _ptr(out[name], name, dtype, shape, dev)
+    lib = load_library()
+    keep, ws, ws_bytes = _scratch(
+        workspace, _size(lib.ssm_block_norm_bwd_workspace_size, rows, dim), dev)
+    _check(lib.ssm_block_norm_bwd(
+        *args, _ptr(dr, "dr", rdt, x.shape, dev), _ptr(dy, "dy", act, x.shape, dev),
+        p["dx"], p.get("dw_post"), p.get("dz"), p.get("dscale"), p.get("dresidual"),
+        p.get("dw_pre"), rows, dim, groups, eps, code, rcode, ws, ws_bytes,
+        _stream_handle(dev, stream)))
+    return {name: out[name] for name in shapes}

@@ -45,7 +45,9 @@ def _run(cmd):
 
 
 HIP_SOURCES = ["ssm_kernels.hip", "ssm_step.hip", "ssm_bwd.hip", "ssm_ssd.hip",
-               "ssm_roofline.hip", "ssm_conv_bwd.hip"]
+               "ssm_roofline.hip", "ssm_conv_bwd.hip", "ssm_linattn.hip",
+               "ssm_linattn_bf16.hip", "ssm_linattn_f32.hip", "ssm_block_norm.hip"]
+CPP_SOURCES = ["ssm_api.cpp", "ssm_linattn_api.cpp"]
 
 
 def build(verbose: bool = False) -> str:
@@ -58,11 +60,12 @@ def build(verbose: bool = False) -> str:
         objs.append(obj)
         jobs.append(_start([hipcc] + HIP_FLAGS + ["-I", INCLUDE, "-I", CSRC, "-c",
                                                   os.path.join(CSRC, src), "-o", obj]))
-    a_obj = os.path.join(BUILD_DIR, "ssm_api.o")
-    objs.append(a_obj)
-    jobs.append(_start(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra",
-                        "-I", INCLUDE, "-I", CSRC, "-c",
-                        os.path.join(CSRC, "ssm_api.cpp"), "-o", a_obj]))
+    for src in CPP_SOURCES:
+        obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
+        objs.append(obj)
+        jobs.append(_start(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra",
+                            "-I", INCLUDE, "-I", CSRC, "-c",
+                            os.path.join(CSRC, src), "-o", obj]))
     out = "".join(_finish(*j) for j in jobs)
     tmp = LIB + ".tmp%d" % os.getpid()
     out += _run([hipcc, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp]

@@ -160,6 +160,15 @@ int64_t bwd_slots(int64_t batch, int64_t dim, int64_t n_chunks) {
 }  // namespace
 
 namespace ssm {
+int set_error(int status, const char *message) noexcept {
+  try {
+    g_last_error = message;
+  } catch (...) {
+    g_last_error.clear();  // no memory for the message: the status says it all
+  }
+  return status;
+}
+
 BwdLayout bwd_layout(int64_t batch, int64_t dim, int64_t N, int64_t seqlen,
                      int64_t elem_bytes) {
   const size_t ns = static_cast<size_t>(N);

@@ -176,4 +176,8 @@ BwdLayout bwd_layout(int64_t batch, int64_t dim, int64_t N, int64_t seqlen,
                      int64_t elem_bytes);
 const char *hip_error_string(int err);
 
+// Sets the calling thread's error message (ssm_last_error) and returns the
+// status; never throws.
+int set_error(int status, const char *message) noexcept;
+
 }  // namespace ssm

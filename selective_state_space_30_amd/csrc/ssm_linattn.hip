@@ -1,0 +1,451 @@
+// ssm_linattn.hip -- linear attention with a decay for each head: the small
+// kernels around the chunk kernel (ssm_linattn_core.h) and the single-token
+// step.
+#include "ssm_linattn_core.h"
+
+namespace ssm {
+namespace {
+
+using namespace lin;
+
+// ------------------------------------------------------- segment states ---
+// Per (sequence, head): what each segment adds to the state -> the state
+// that enters it, one segment after another.  Each thread carries kPer
+// elements; the next segment's are requested before this one's are replaced.
+constexpr int kChainPer = 4;
+
+__global__ __launch_bounds__(256) void linattn_chain_kernel(LinChain p) {
+  const int h = blockIdx.x % p.plan.heads;
+  const int seq = blockIdx.x / p.plan.heads;
+  int64_t b, e;
+  sequence_rows(p.plan, seq, &b, &e);
+  int64_t segs = (e - b + p.plan.seg_len - 1) / p.plan.seg_len;
+  if (segs < 1) segs = 1;
+  const int64_t slot0 = first_slot(p.plan, seq);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.y) * 256 * kChainPer + threadIdx.x;
+  const int64_t by_seq = (static_cast<int64_t>(seq) * p.plan.heads + h) * p.size;
+  float acc[kChainPer], cur[kChainPer], next[kChainPer];
+  auto slot_at = [&](int64_t k) { return slot0 + (p.reverse ? segs - 1 - k : k); };
+  auto fetch = [&](int64_t k, float *v) {
+    const float *s = p.states + (slot_at(k) * p.plan.heads + h) * p.size;
+#pragma unroll
+    for (int i = 0; i < kChainPer; ++i) v[i] = i0 + 256 * i < p.size ? s[i0 + 256 * i] : 0.0f;
+  };
+#pragma unroll
+  for (int i = 0; i < kChainPer; ++i) {
+    acc[i] = p.first && i0 + 256 * i < p.size ? p.first[by_seq + i0 + 256 * i] : 0.0f;
+    cur[i] = next[i] = 0.0f;
+  }
+  // nothing reads what the last segment adds
+  if (segs > 1) fetch(0, cur);
+  for (int64_t k = 0; k < segs; ++k) {
+    if (k + 2 < segs) fetch(k + 1, next);
+    float *s = p.states + (slot_at(k) * p.plan.heads + h) * p.size;
+    const float d = k + 1 < segs ? p.decay[slot_at(k) * p.plan.heads + h] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChainPer; ++i) {
+      if (i0 + 256 * i < p.size) s[i0 + 256 * i] = acc[i];
+      acc[i] = fmaf(acc[i], d, cur[i]);
+      cur[i] = next[i];
+    }
+  }
+}
+
+// -------------------------------------------------- gradient of the decay ---
+// With W_ts = scale e^{a_t - a_s} (q_t . k_s) (do_t . v_s) over all pairs
+// s < t of a sequence, dL/dg_t is the sum of W over the pairs that straddle
+// t (s < t <= r).  From the end of a segment backwards,
+//   dg_t = dg_{t+1} + (what t's row adds) - (what t's column adds),
+// dg at a segment's end being the inner product of the state there with its
+// adjoint.  Row and column sums leave out the pair (t, t), and pairs inside a
+// chunk enter rows and columns with the same 32-bit value, so that what
+// cancels, cancels: only the sums' own rounding is left.  At a sequence's
+// end the adjoint (dh_final) also meets the last tokens' own terms, which no
+// dg holds and which may be far larger; so the last chunk is summed from the
+// state before it: dg_t = e^{a_T} <S, dh_final> + rows from t on + columns
+// before t.
+
+// Pairs inside each chunk: out_t = sum_{s<t} W_ts - sum_{r>t} W_rt.  One
+// workgroup per (chunk, head), wave w takes the rows of token tile w;
+// operands come from memory straight into fragments.
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_pairs_kernel(LinPairs p) {
+  typedef Traits<T> Tr;
+  typedef typename Tr::Frag Frag;
+  constexpr int C = Tr::kChunk, kNT = C / 16;
+  __shared__ double As[C];
+  __shared__ float Cols[4][C];
+  __shared__ float Rows[C];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int h = blockIdx.x % p.plan.heads;
+  const int64_t per_seg = p.plan.seg_len / C;
+  const int64_t cs = blockIdx.x / p.plan.heads;
+  const Segment sg = segment_of(p.plan, cs / per_seg);
+  const int64_t t0 = sg.begin + (cs % per_seg) * C;
+  if (!sg.real || t0 >= sg.end) return;
+  const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
+  if (wave == 0) {
+    const float g = lane < rows ? decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h) : 0.0f;
+    const double a = wave_sums<C>(lane < C ? log2_decay(g) : 0.0, lane);
+    if (lane < C) As[lane] = a;
+  }
+  auto frag = [&](const LinSide &x, int row, int c) __attribute__((always_inline)) {
+    const T *s = static_cast<const T *>(x.p) + (t0 + row) * x.stride + (h / x.div) * x.d + c;
+    Frag f;
+    if (row < rows && p.plan.vec && c + 8 <= x.d) {
+      __builtin_memcpy(&f, s, sizeof(f));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        f[e] = row < rows && c + e < x.d
+                   ? __builtin_bit_cast(typename Tr::Elem, s[e])
+                   : static_cast<typename Tr::Elem>(0.0f);
+    }
+    return f;
+  };
+  __syncthreads();
+  const int ti = wave;
+  float row_sum = 0.0f;
+  if (ti < kNT) {
+    f32x4 w[kNT];
+    for (int part = 0; part < 2; ++part) {
+      const LinSide &xr = part ? p.o : p.q, &xc = part ? p.v : p.k;
+      f32x4 acc[kNT];
+#pragma unroll
+      for (int si = 0; si < kNT; ++si) acc[si] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int c = 8 * lq; c - 8 * lq < xr.d; c += 32) {
+        const Frag b = frag(xr, 16 * ti + li, c);
+#pragma unroll
+        for (int si = 0; si < kNT; ++si)
+          if (si <= ti) acc[si] = mma(frag(xc, 16 * si + li, c), b, acc[si]);
+      }
+#pragma unroll
+      for (int si = 0; si < kNT; ++si) w[si] = part ? w[si] * acc[si] : acc[si];
+    }
+    // lane: token t = 16 ti + li against s = 16 si + 4 lq + e
+    const int t = 16 * ti + li;
+    const double at = As[t];
+#pragma unroll
+    for (int si = 0; si < kNT; ++si) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int s = 16 * si + 4 * lq + e;
+        float x = 0.0f;
+        if (si <= ti && s < t) x = w[si][e] * fast_exp2(static_cast<float>(at - As[s])) * p.scale;
+        row_sum += x;
+        float col = x;
+        col += __shfl_xor(col, 1);
+        col += __shfl_xor(col, 2);
+        col += __shfl_xor(col, 4);
+        col += __shfl_xor(col, 8);
+        if (li == 0) Cols[ti][s] = col;
+      }
+    }
+    row_sum += __shfl_xor(row_sum, 16);
+    row_sum += __shfl_xor(row_sum, 32);
+    if (lq == 0) Rows[t] = row_sum;
+  }
+  __syncthreads();
+  if (tid < rows) {
+    float c = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kNT; ++w) c += Cols[w][tid];
+    p.out[(t0 + tid) * p.plan.heads + h] = Rows[tid] - c;
+  }
+}
+
+// One workgroup per (segment, head): the inner product at the segment's end,
+// then the sums from there backwards, in 64 bits.
+__global__ __launch_bounds__(256) void linattn_decay_grad_kernel(LinDecayGrad p) {
+  __shared__ double Red[256];
+  __shared__ double Run[4][2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = blockIdx.x % p.plan.heads;
+  const int64_t slot = blockIdx.x / p.plan.heads;
+  const Segment sg = segment_of(p.plan, slot);
+  if (!sg.real || sg.begin >= sg.end) return;
+  const int64_t n = sg.end - sg.begin;
+  // tokens from here on are summed from the state before them
+  const int64_t tail = sg.last ? (n - 1) / p.chunk * p.chunk : n;
+  const float *state = nullptr, *adj = nullptr;
+  const int64_t by_seq = (static_cast<int64_t>(sg.seq) * p.plan.heads + h) * p.size;
+  double factor = 1.0;
+  if (sg.last) {
+    if (p.dlast) {
+      state = p.last + by_seq;
+      adj = p.dlast + by_seq;
+      double sum = 0.0;
+      for (int64_t t = sg.begin + tail; t < sg.end; ++t)
+        sum += log2_decay(decay_at(p.g, p.g_kind, t, p.plan.heads, h));
+      factor = fast_exp2(static_cast<float>(sum));
+    }
+  } else {
+    state = p.states + ((slot + 1) * p.plan.heads + h) * p.size;
+    adj = p.adjoints + (slot * p.plan.heads + h) * p.size;
+  }
+  double dot = 0.0;
+  if (state)
+    for (int64_t i = tid; i < p.size; i += 256)
+      dot += static_cast<double>(state[i]) * static_cast<double>(adj[i]);
+  Red[tid] = dot;
+  __syncthreads();
+  for (int d = 128; d > 0; d >>= 1) {
+    if (tid < d) Red[tid] += Red[tid + d];
+    __syncthreads();
+  }
+  double end = Red[0] * factor;
+  for (int64_t base = (n - 1) / 256 * 256; base >= 0; base -= 256) {
+    // thread i takes token base + 255 - i: sums from the end are prefix sums
+    const int64_t k = base + 255 - tid;
+    double v = 0.0, y = 0.0;
+    const int64_t at = (sg.begin + k) * p.plan.heads + h;
+    if (k < n) {
+      v = p.pairs[at];
+      for (int s = 0; s < p.xslices; ++s) v += p.xdots[s * p.plan.tokens * p.plan.heads + at];
+      for (int s = 0; s < p.yslices; ++s) y += p.ydots[s * p.plan.tokens * p.plan.heads + at];
+      if (k < tail) {
+        v -= y;
+        y = 0.0;
+      }
+    }
+    v = wave_sums<64>(v, lane);
+    y = wave_sums<64>(y, lane);
+    if (lane == 63) {
+      Run[wave][0] = v;
+      Run[wave][1] = y;
+    }
+    __syncthreads();
+    double before = end, from = 0.0;  // sums over the tokens behind this wave's
+    for (int w = 0; w < wave; ++w) {
+      before += Run[w][0];
+      from += Run[w][1];
+    }
+    const double all = end + Run[0][0] + Run[1][0] + Run[2][0] + Run[3][0];
+    const double ally = Run[0][1] + Run[1][1] + Run[2][1] + Run[3][1];
+    // columns of the tail's tokens before k (the others' are 0)
+    const double columns = k >= tail ? ally - (from + y) : 0.0;
+    if (k < n) p.dg[at] = static_cast<float>(before + v + columns);
+    __syncthreads();
+    end = all;
+  }
+}
+
+// ------------------------------------------------------------ reductions ---
+__device__ __forceinline__ void all_rows(const LinPlan &p, int64_t *begin, int64_t *end) {
+  int64_t b, e, unused;
+  sequence_rows(p, 0, begin, &unused);
+  sequence_rows(p, p.nseq - 1, &b, &e);
+  *end = e;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_head_sum_kernel(const float *in, T *out,
+                                                               LinPlan plan, int div, int d) {
+  int64_t begin, end;
+  all_rows(plan, &begin, &end);
+  const int64_t row = static_cast<int64_t>(plan.heads / div) * d;  // of out
+  const int64_t stop = end * row, step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = begin * row + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < stop;
+       i += step) {
+    const int64_t t = i / row, c = i % row;
+    const float *s = in + t * plan.heads * d + c / d * div * d + c % d;
+    float acc = 0.0f;
+    for (int k = 0; k < div; ++k) acc += s[static_cast<int64_t>(k) * d];
+    out[i] = from_f32<T>(acc);
+  }
+}
+
+__global__ __launch_bounds__(1024) void linattn_token_sum_kernel(const float *in, float *out,
+                                                                 LinPlan plan) {
+  __shared__ double Red[1024];
+  const int tid = threadIdx.x, h = blockIdx.x;
+  int64_t begin, end;
+  all_rows(plan, &begin, &end);
+  double acc = 0.0;
+  for (int64_t t = begin + tid; t < end; t += 1024) acc += in[t * plan.heads + h];
+  Red[tid] = acc;
+  __syncthreads();
+  for (int d = 512; d > 0; d >>= 1) {
+    if (tid < d) Red[tid] += Red[tid + d];
+    __syncthreads();
+  }
+  if (tid == 0) out[h] = static_cast<float>(Red[0]);
+}
+
+// ------------------------------------------------------------------ step ---
+// One token: a workgroup takes 64 columns of one row's head state, 16
+// threads with 4 neighbouring columns each in 16 groups over the state's
+// rows.  The state is read and written once; everything else is small.
+constexpr int kStepCols = 64, kStepGroups = 16;
+constexpr int kStepRows = kLinMaxDim / kStepGroups;  // state rows a thread may take
+
+template <typename T, bool kVec>
+__global__ __launch_bounds__(256) void linattn_step_kernel(LinStep p) {
+  __shared__ float Qs[kLinMaxDim], Ks[kLinMaxDim];
+  __shared__ __align__(16) float Part[kStepGroups][kStepCols];
+  const int tid = threadIdx.x;
+  const int slices = (p.dv + kStepCols - 1) / kStepCols;
+  const int slice = blockIdx.x % slices;
+  const int h = blockIdx.x / slices % p.heads;
+  const int64_t b = blockIdx.x / slices / p.heads;
+  const int hk = h / (p.heads / p.qk_heads);
+  const int64_t slot = p.slot_of ? p.slot_of[b] : b;
+  // a row without a slot of its own: out of range, or an earlier row's
+  int taken = slot < 0 || slot >= p.slots;
+  if (p.slot_of && !taken)
+    for (int64_t i = tid; i < b; i += 256) taken |= p.slot_of[i] == slot;
+  if (tid < p.dk) {
+    const int64_t at = static_cast<int64_t>(hk) * p.dk + tid;
+    Qs[tid] = to_f32<T>(static_cast<const T *>(p.q)[b * p.q_stride + at]);
+    Ks[tid] = to_f32<T>(static_cast<const T *>(p.k)[b * p.k_stride + at]);
+  }
+  taken = __syncthreads_or(taken);
+  const int cg = tid & 15, rg = tid >> 4;
+  const int c = slice * kStepCols + 4 * cg;   // this thread's first column
+  T *o = static_cast<T *>(p.o) + (b * p.heads + h) * p.dv;
+  if (taken) {
+    if (tid < kStepCols && slice * kStepCols + tid < p.dv)
+      o[slice * kStepCols + tid] = from_f32<T>(0.0f);
+    return;
+  }
+  const float decay =
+      p.g_kind == kLinDecayNone
+          ? 1.0f
+          : fast_exp2(static_cast<float>(log2_decay(
+                p.g_kind == kLinDecayHead ? p.g[h] : p.g[b * p.heads + h])));
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    v[e] = c + e < p.dv
+               ? to_f32<T>(static_cast<const T *>(
+                     p.v)[b * p.v_stride + static_cast<int64_t>(h) * p.dv + c + e])
+               : 0.0f;
+  float *s = p.state + (slot * p.heads + h) * p.dk * p.dv + c;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 x[kStepRows];
+#pragma unroll
+  for (int i = 0; i < kStepRows; ++i) {
+    const int r = rg + kStepGroups * i;
+    x[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (r < p.dk && c < p.dv) {
+      if (kVec) {
+        x[i] = *reinterpret_cast<const f32x4 *>(s + r * p.dv);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.dv) x[i][e] = s[r * p.dv + e];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kStepRows; ++i) {
+    const int r = rg + kStepGroups * i;
+    if (r < p.dk && c < p.dv) {
+      const float k = Ks[r], q = Qs[r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[i][e] = fmaf(x[i][e], decay, k * v[e]);
+        acc[e] = fmaf(q, x[i][e], acc[e]);
+      }
+      if (kVec) {
+        *reinterpret_cast<f32x4 *>(s + r * p.dv) = x[i];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.dv) s[r * p.dv + e] = x[i][e];
+      }
+    }
+  }
+  *reinterpret_cast<f32x4 *>(&Part[rg][4 * cg]) = acc;
+  __syncthreads();
+  if (tid < kStepCols && slice * kStepCols + tid < p.dv) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kStepGroups; ++i) sum += Part[i][tid];
+    o[slice * kStepCols + tid] = from_f32<T>(sum * p.scale);
+  }
+}
+
+}  // namespace
+
+int linattn_chunk(bool bf16) { return bf16 ? kLinChunkBf16 : kLinChunkF32; }
+
+// Output columns of a workgroup.  128 halve what the waves read of q and k
+// per output; 64 where there are no more, where the state's registers do
+// not allow more (q and k heads over 128 wide), and in 32 bits.
+int linattn_slice(bool bf16, int dk, int dv) { return bf16 && dk <= 128 && dv > 64 ? 128 : 64; }
+
+int launch_linattn_core(const LinCore &a, int mode, bool reverse, bool bf16, void *stream) {
+  return bf16 ? launch_linattn_core_bf16(a, mode, reverse, stream)
+              : launch_linattn_core_f32(a, mode, reverse, stream);
+}
+
+int launch_linattn_chain(const LinChain &a, void *stream) {
+  const int64_t parts = (a.size + 256 * kChainPer - 1) / (256 * kChainPer);
+  hipLaunchKernelGGL(linattn_chain_kernel,
+                     dim3(static_cast<unsigned>(a.plan.nseq * static_cast<int64_t>(a.plan.heads)),
+                          static_cast<unsigned>(parts)),
+                     dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_linattn_pairs(const LinPairs &a, bool bf16, void *stream) {
+  const dim3 grid(
+      static_cast<unsigned>(a.plan.slots * (a.plan.seg_len / a.chunk) * a.plan.heads));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (bf16)
+    hipLaunchKernelGGL(linattn_pairs_kernel<uint16_t>, grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(linattn_pairs_kernel<float>, grid, dim3(256), 0, s, a);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_linattn_decay_grad(const LinDecayGrad &a, void *stream) {
+  hipLaunchKernelGGL(linattn_decay_grad_kernel,
+                     dim3(static_cast<unsigned>(a.plan.slots * a.plan.heads)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), a);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_linattn_head_sum(const float *in, void *out, const LinPlan &plan, int div, int d,
+                            bool bf16, void *stream) {
+  const int64_t n = plan.tokens * (plan.heads / div) * d, most = 1 << 16;
+  const dim3 grid(static_cast<unsigned>((n + 255) / 256 < most ? (n + 255) / 256 : most));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (bf16)
+    hipLaunchKernelGGL(linattn_head_sum_kernel<uint16_t>, grid, dim3(256), 0, s, in,
+                       static_cast<uint16_t *>(out), plan, div, d);
+  else
+    hipLaunchKernelGGL(linattn_head_sum_kernel<float>, grid, dim3(256), 0, s, in,
+                       static_cast<float *>(out), plan, div, d);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_linattn_token_sum(const float *in, float *out, const LinPlan &plan, void *stream) {
+  hipLaunchKernelGGL(linattn_token_sum_kernel, dim3(static_cast<unsigned>(plan.heads)), dim3(1024),
+                     0, static_cast<hipStream_t>(stream), in, out, plan);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_linattn_step(const LinStep &a, bool bf16, void *stream) {
+  const int64_t slices = (a.dv + kStepCols - 1) / kStepCols;
+  const dim3 grid(static_cast<unsigned>(a.batch * a.heads * slices));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool vec = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+  if (bf16) {
+    if (vec)
+      hipLaunchKernelGGL((linattn_step_kernel<uint16_t, true>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((linattn_step_kernel<uint16_t, false>), grid, dim3(256), 0, s, a);
+  } else {
+    if (vec)
+      hipLaunchKernelGGL((linattn_step_kernel<float, true>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((linattn_step_kernel<float, false>), grid, dim3(256), 0, s, a);
+  }
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace ssm

@@ -1,0 +1,578 @@
+// ssm_linattn_core.h -- the chunk kernel of linear attention with a decay for
+// each head on gfx950's matrix cores.  Included by the .hip files that
+// instantiate it.
+//
+// With the recurrence S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = S_t^T q_t and
+// a_t the sum of g from the chunk's start to t, a chunk of T tokens is
+//   o_t = e^{a_t} S_in^T q_t + sum_{s<=t} e^{a_t - a_s} (q_t . k_s) v_s
+//   S_out = e^{a_T} S_in + sum_s e^{a_T - a_s} k_s v_s^T.
+// Its gradients are the same products with other operands.  With M the
+// adjoint of the state that leaves the chunk:
+//   dq: in token order, (q, k, v) := (do, v, k), state S^T
+//   dv: against it,     (q, k, v) := (k, q, do), state M
+//   dk: against it,     (q, k, v) := (v, do, q), state M^T
+// where against token order s runs over s >= t, the weights are e^{a_s - a_t}
+// inside the chunk, e^{a_T - a_t} on the state and e^{a_s} into it.  So one
+// kernel serves the forward pass, the three gradients and the pass that
+// forms only the states of the segments.
+//
+// The decay sums run in 64 bits and every weight is the exponential of a
+// difference, so that a strong decay (even -inf, a reset) neither
+// overflows nor cancels.
+#pragma once
+
+#include "ssm_device.h"
+#include "ssm_linattn_internal.h"
+
+namespace ssm {
+namespace lin {
+
+using namespace dev;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A fragment: 8 elements of the contracted index a lane holds for one row
+// (or column) of a 16 x 16 product over 32: lane l, element e belong to
+// row l % 16 and contracted position 8 * (l / 16) + e.  In 32 bits the
+// product is 8 steps of 4, step e taking element e of every lane.
+template <typename T> struct Traits;
+template <> struct Traits<uint16_t> {
+  typedef bf16x8 Frag;
+  typedef bf16x4 Half;
+  typedef __bf16 Elem;
+  static constexpr int kChunk = kLinChunkBf16;
+  static constexpr bool kBf16 = true;
+};
+template <> struct Traits<float> {
+  typedef f32x8 Frag;
+  typedef f32x4 Half;
+  typedef float Elem;
+  static constexpr int kChunk = kLinChunkF32;
+  static constexpr bool kBf16 = false;
+};
+
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(f32x8 a, f32x8 b, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+
+// Elements p[0..3] and p[16..19]: the fragment whose contracted positions
+// are the rows a lane holds of two stacked 16-row accumulator tiles.
+__device__ __forceinline__ bf16x8 two_halves(const __bf16 *p) {
+  const bf16x4 a = *reinterpret_cast<const bf16x4 *>(p);
+  const bf16x4 b = *reinterpret_cast<const bf16x4 *>(p + 16);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ f32x8 two_halves(const float *p) {
+  const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
+  const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 16);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Fragment of a row-major [position][column] LDS tile contracted over its
+// rows: lane l gets column col + l % 16, positions row + 8 * (l / 16) + e.
+// In bf16 the transposing LDS read hands every lane of 16 one column of the
+// 4 x 16 block that the 16 lanes address.
+template <int kStride>
+__device__ __forceinline__ bf16x8 frag_by_column(const __bf16 *tile, int row, int col, int lane) {
+  const int li = lane & 15, lq = lane >> 4;
+  const __bf16 *p = tile + (row + 8 * lq + (li >> 2)) * kStride + col + 4 * (li & 3);
+  typedef __attribute__((address_space(3))) s16x4 *Lds;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 4 * kStride));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int kStride>
+__device__ __forceinline__ f32x8 frag_by_column(const float *tile, int row, int col, int lane) {
+  const float *p = tile + (row + 8 * (lane >> 4)) * kStride + col + (lane & 15);
+  f32x8 r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = p[e * kStride];
+  return r;
+}
+
+__device__ __forceinline__ bf16x8 to_frag(f32x8 v, bf16x8) {
+  return __builtin_convertvector(v, bf16x8);
+}
+__device__ __forceinline__ f32x8 to_frag(f32x8 v, f32x8) { return v; }
+
+// Where a segment lies.
+struct Segment {
+  int64_t begin, end;  // token rows
+  int seq;
+  int seg;             // its number in the sequence
+  bool last;           // of its sequence
+  bool real;           // the slot is in use
+};
+
+__device__ __forceinline__ int64_t cu_at(const LinPlan &p, int i) {
+  const int64_t c = p.cu[i];
+  return c < 0 ? 0 : c > p.tokens ? p.tokens : c;
+}
+
+// Rows of a sequence; offsets outside [0, tokens], or that fall, are brought
+// into range, so that no offset reaches memory outside the arrays.
+__device__ __forceinline__ void sequence_rows(const LinPlan &p, int seq, int64_t *begin,
+                                              int64_t *end) {
+  if (!p.cu) {
+    *begin = seq * p.seqlen;
+    *end = *begin + p.seqlen;
+    return;
+  }
+  const int64_t b = cu_at(p, seq), e = cu_at(p, seq + 1);
+  *begin = b;
+  *end = e < b ? b : e;
+}
+
+__device__ __forceinline__ int64_t first_slot(const LinPlan &p, int seq) {
+  return p.cu ? cu_at(p, seq) / p.seg_len + seq : seq * p.segs;
+}
+
+__device__ __forceinline__ Segment segment_of(const LinPlan &p, int64_t slot) {
+  Segment s;
+  if (!p.cu) {
+    s.seq = static_cast<int>(slot / p.segs);
+  } else {
+    int lo = 0, hi = p.nseq - 1;  // the last sequence whose first slot is <= slot
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_slot(p, mid) <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    s.seq = lo;
+  }
+  s.seg = static_cast<int>(slot - first_slot(p, s.seq));
+  int64_t b, e;
+  sequence_rows(p, s.seq, &b, &e);
+  s.begin = b + s.seg * p.seg_len;
+  // an empty sequence has one (empty) segment, which hands its state on
+  s.real = s.seg >= 0 && (s.begin < e || s.seg == 0);
+  s.end = s.begin + p.seg_len < e ? s.begin + p.seg_len : e;
+  s.last = s.end == e;
+  return s;
+}
+
+// log2 of a token's decay factor: g / ln 2, no less than -2^14 (whose
+// exponential is 0 in 32 bits: -inf must not meet itself in a difference).
+__device__ __forceinline__ double log2_decay(float g) {
+  const double x = static_cast<double>(g) * 1.4426950408889634;
+  return x < -16384.0 ? -16384.0 : x;
+}
+
+__device__ __forceinline__ float decay_at(const float *g, int kind, int64_t t, int heads, int h) {
+  return kind == kLinDecayNone ? 0.0f : kind == kLinDecayHead ? g[h] : g[t * heads + h];
+}
+
+// Inclusive sums over the first kWidth lanes of a wave.
+template <int kWidth>
+__device__ __forceinline__ double wave_sums(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < kWidth; d *= 2) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// 16-byte pieces of kRows token rows of one head, `cols` elements wide in
+// LDS (the head's d, zeros behind), from memory to registers.  Rows behind
+// `rows` are zeros and are not read.
+template <typename T, int kRows, int kCols>
+struct Tile {
+  static constexpr int kPer = 16 / sizeof(T);           // elements of a piece
+  static constexpr int kRowPieces = kCols / kPer;
+  static constexpr int kPieces = kRows * kRowPieces / 256;
+  static_assert(kRows * kRowPieces % 256 == 0, "whole pieces per thread");
+  u32x4 r[kPieces];
+
+  __device__ __forceinline__ void load(const T *base, int64_t stride, int rows, int d, bool vec,
+                                       int tid) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int q = tid + 256 * i, row = q / kRowPieces, c = (q % kRowPieces) * kPer;
+      r[i] = u32x4{0u, 0u, 0u, 0u};
+      if (row < rows && c < d) {
+        const T *p = base + row * stride + c;
+        if (vec) {
+          r[i] = *reinterpret_cast<const u32x4 *>(p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            if (c + e < d) {
+              if constexpr (sizeof(T) == 2)
+                r[i][e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e % 2));
+              else
+                r[i][e] = __builtin_bit_cast(uint32_t, p[e]);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  template <int kStride>
+  __device__ __forceinline__ void store(typename Traits<T>::Elem *tile, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int q = tid + 256 * i, row = q / kRowPieces, c = (q % kRowPieces) * kPer;
+      *reinterpret_cast<u32x4 *>(tile + row * kStride + c) = r[i];
+    }
+  }
+};
+
+__device__ __forceinline__ void store4(uint16_t *p, f32x4 v, int n, bool vec) {
+  if (vec && n >= 4) {
+    uint2 w;
+    w.x = pack_bf16x2(v[0], v[1]);
+    w.y = pack_bf16x2(v[2], v[3]);
+    *reinterpret_cast<uint2 *>(p) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = from_f32<uint16_t>(v[e]);
+  }
+}
+__device__ __forceinline__ void store4(float *p, f32x4 v, int n, bool vec) {
+  if (vec && n >= 4) {
+    *reinterpret_cast<f32x4 *>(p) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+
+// One workgroup: 4 waves, one segment of one head, kNJ * 64 output columns.
+// Wave w owns columns 16 kNJ w .. of the output and of the state, whose
+// kDK x 16 kNJ part stays in its accumulator registers from chunk to chunk
+// (the state tiles are the second operand of the next product as they
+// stand: the first operand is read with its columns in the order the
+// accumulators hold the rows).  The products are set up so that a lane
+// holds 4 neighbouring output columns of one token.  Per chunk: the tiles go
+// from registers (loaded during the chunk before) to LDS; the waves share
+// out the token pairs' products, each then takes all of them for its
+// columns.  bf16 roundings: the weighted pair products and the state where
+// it is an operand, once each (2^-8 of each term, as the output's own
+// rounding); what goes into the state enters as a pair of bf16 values
+// (2^-16), since the state is returned in 32 bits and is carried over the
+// sequence; likewise the state itself where dot products in 32 bits are
+// wanted (kLinOutDot).
+template <typename T, int kDK, int kNJ, int kMode, bool kRev>
+__global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
+  typedef Traits<T> Tr;
+  typedef typename Tr::Frag Frag;
+  typedef typename Tr::Elem Elem;
+  constexpr int C = Tr::kChunk, kNT = C / 16, kTS = C / 32;
+  constexpr int kKS = kDK / 32, kIT = kDK / 16, kDV = 64 * kNJ;
+  constexpr bool kBf16 = Tr::kBf16;
+  constexpr bool kOut = kMode != kLinState, kDot = kMode == kLinOutDot;
+  // row strides: rows 4 banks apart where rows are read side by side, 8
+  // where a read takes 4 rows of 8 banks at once (transposing reads)
+  constexpr int kRowQ = kDK + (kBf16 ? 8 : 4), kRowK = kDK + (kBf16 ? 16 : 4);
+  constexpr int kRowV = kDV + (kBf16 ? 16 : 4), kRowP = C + (kBf16 ? 8 : 4);
+  __shared__ __align__(16) Elem Qs[kOut ? C * kRowQ : 8];
+  __shared__ __align__(16) Elem Ks[C * kRowK];
+  __shared__ __align__(16) Elem Vs[C * kRowV];
+  __shared__ __align__(16) Elem Ps[kOut ? C * kRowP : 8];
+  __shared__ double As[C];                       // sums of decays (log2)
+  __shared__ __align__(16) float Wo[C], Wi[C];   // weights out of, into the state
+  __shared__ float Wd[1];                        // the chunk's decay
+  __shared__ float Dots[kDot ? 4 * C : 1];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int slices = (p.v.d + kDV - 1) / kDV;
+  const int slice = blockIdx.x % slices;
+  const int h = blockIdx.x / slices % p.plan.heads;
+  const int64_t slot = blockIdx.x / slices / p.plan.heads;
+  const Segment sg = segment_of(p.plan, slot);
+  if (!sg.real) return;
+  const bool ends = kRev ? sg.seg == 0 : sg.last;  // nothing comes after it
+  if (kMode == kLinState && ends) return;
+
+  const int j0 = slice * kDV;
+  const int dk = p.k.d, dv = p.v.d - j0;     // columns from this slice's first
+  const int64_t n = sg.end - sg.begin;
+  const int chunks = static_cast<int>((n + C - 1) / C);
+  const bool vec = p.plan.vec;
+  const T *qh = static_cast<const T *>(p.q.p) + (h / p.q.div) * p.q.d;
+  const T *kh = static_cast<const T *>(p.k.p) + (h / p.k.div) * p.k.d;
+  const T *vh = static_cast<const T *>(p.v.p) + (h / p.v.div) * p.v.d + j0;
+
+  // the state: tile (it, nj), element e is S[16 it + 4 lq + e][jw + 16 nj + li]
+  const int jw = 16 * kNJ * wave;
+  f32x4 S[kIT][kNJ];
+  const int64_t size = static_cast<int64_t>(p.k.d) * p.v.d;
+  const int64_t by_slot = (slot * p.plan.heads + h) * size;
+  const int64_t by_seq = (static_cast<int64_t>(sg.seq) * p.plan.heads + h) * size;
+  {
+    const float *in = nullptr;
+    if (kMode != kLinState)
+      in = p.in_slots ? p.in_slots + by_slot : p.in_seqs ? p.in_seqs + by_seq : nullptr;
+#pragma unroll
+    for (int it = 0; it < kIT; ++it)
+#pragma unroll
+      for (int nj = 0; nj < kNJ; ++nj)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int a = 16 * it + 4 * lq + e, b = jw + 16 * nj + li;
+          S[it][nj][e] = in && a < dk && b < dv ? in[a * p.sa + (j0 + b) * p.sb] : 0.0f;
+        }
+  }
+  auto save = [&](float *out) __attribute__((always_inline)) {
+#pragma unroll
+    for (int it = 0; it < kIT; ++it)
+#pragma unroll
+      for (int nj = 0; nj < kNJ; ++nj)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int a = 16 * it + 4 * lq + e, b = jw + 16 * nj + li;
+          if (a < dk && b < dv) out[a * p.sa + (j0 + b) * p.sb] = S[it][nj][e];
+        }
+  };
+  // the decay's gradient needs the state before a sequence's last chunk
+  constexpr bool kBeforeLast = kDot && !kRev;
+  double total = 0.0;  // state pass: the segment's sum of decays (wave 0)
+
+  Tile<T, C, kDK> tq, tk;
+  Tile<T, C, kDV> tv;
+  float gt = 0.0f;
+  auto load = [&](int c) __attribute__((always_inline)) {
+    const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
+    const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
+    if (kOut) tq.load(qh + t0 * p.q.stride, p.q.stride, rows, p.q.d, vec, tid);
+    tk.load(kh + t0 * p.k.stride, p.k.stride, rows, dk, vec, tid);
+    tv.load(vh + t0 * p.v.stride, p.v.stride, rows, dv, vec, tid);
+    gt = 0.0f;
+    if (wave == 0 && lane < rows) gt = decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h);
+  };
+  auto stage = [&]() __attribute__((always_inline)) {
+    if (kOut) tq.template store<kRowQ>(Qs, tid);
+    tk.template store<kRowK>(Ks, tid);
+    tv.template store<kRowV>(Vs, tid);
+    if (wave == 0) {
+      const double a = wave_sums<C>(lane < C ? log2_decay(gt) : 0.0, lane);
+      const double end = __shfl(a, C - 1);
+      const float from = fast_exp2(static_cast<float>(a));
+      const float to = fast_exp2(static_cast<float>(end - a));
+      if (lane < C) {
+        As[lane] = a;
+        Wo[lane] = (kRev ? to : from) * p.inter;
+        Wi[lane] = (kRev ? from : to) * p.into;
+      }
+      if (lane == 0) Wd[0] = fast_exp2(static_cast<float>(end));
+      if (kMode == kLinState) total += end;
+    }
+  };
+
+  const int first = kRev ? chunks - 1 : 0, step = kRev ? -1 : 1;
+  if (chunks > 0) {
+    load(first);
+    stage();
+  }
+  for (int i = 0; i < chunks; ++i) {
+    const int c = first + i * step;
+    const bool more = i + 1 < chunks;
+    __syncthreads();  // the chunk is staged
+    if (more) load(c + step);
+
+    if (kOut) {
+      // token pairs: wave w takes the tokens t of tile w (32-bit chunks have
+      // 2 tiles: two waves a tile, each half of the s)
+      const int ti = kNT == 4 ? wave : wave >> 1;
+      const int s_lo = kNT == 4 ? 0 : wave & 1, s_hi = kNT == 4 ? kNT : (wave & 1) + 1;
+      const double at = As[16 * ti + li];
+#pragma unroll
+      for (int si = 0; si < kNT; ++si) {
+        if (si < s_lo || si >= s_hi) continue;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        const bool some = kRev ? si >= ti : si <= ti;
+        if (some) {
+#pragma unroll
+          for (int ks = 0; ks < kKS; ++ks) {
+            const Frag a = *reinterpret_cast<const Frag *>(&Ks[(16 * si + li) * kRowK + 32 * ks + 8 * lq]);
+            const Frag b = *reinterpret_cast<const Frag *>(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 8 * lq]);
+            acc = mma(a, b, acc);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int s = 16 * si + 4 * lq + e, t = 16 * ti + li;
+            const double as = As[s];
+            const float w = fast_exp2(static_cast<float>(kRev ? as - at : at - as));
+            acc[e] = (kRev ? s >= t : s <= t) ? acc[e] * w * p.inside : 0.0f;
+          }
+        }
+        Elem *d = &Ps[(16 * ti + li) * kRowP + 16 * si + 4 * lq];
+        if constexpr (kBf16)
+          *reinterpret_cast<bf16x4 *>(d) = __builtin_convertvector(acc, bf16x4);
+        else
+          *reinterpret_cast<f32x4 *>(d) = acc;
+      }
+    }
+
+    f32x4 O[kNT][kNJ];
+    if (kOut) {
+#pragma unroll
+      for (int ti = 0; ti < kNT; ++ti)
+#pragma unroll
+        for (int nj = 0; nj < kNJ; ++nj) O[ti][nj] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // the state's part
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        Frag hi[kNJ], lo[kNJ];
+#pragma unroll
+        for (int nj = 0; nj < kNJ; ++nj) {
+          const f32x8 s = __builtin_shufflevector(S[2 * ks][nj], S[2 * ks + 1][nj], 0, 1, 2, 3, 4, 5, 6, 7);
+          hi[nj] = to_frag(s, Frag{});
+          if constexpr (kDot && kBf16)
+            lo[nj] = to_frag(s - __builtin_convertvector(hi[nj], f32x8), Frag{});
+        }
+#pragma unroll
+        for (int ti = 0; ti < kNT; ++ti) {
+          const Frag b = two_halves(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 4 * lq]);
+#pragma unroll
+          for (int nj = 0; nj < kNJ; ++nj) {
+            O[ti][nj] = mma(hi[nj], b, O[ti][nj]);
+            if constexpr (kDot && kBf16) O[ti][nj] = mma(lo[nj], b, O[ti][nj]);
+          }
+        }
+      }
+#pragma unroll
+      for (int ti = 0; ti < kNT; ++ti) {
+        const float w = Wo[16 * ti + li];
+#pragma unroll
+        for (int nj = 0; nj < kNJ; ++nj) O[ti][nj] *= w;
+      }
+      if constexpr (kDot) {
+        // dot products of the state's part with x's rows, this wave's columns
+        const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
+        const T *xh = static_cast<const T *>(p.x.p) + (h / p.x.div) * p.x.d + j0;
+#pragma unroll
+        for (int ti = 0; ti < kNT; ++ti) {
+          const int64_t t = t0 + 16 * ti + li;
+          float d = 0.0f;
+          if (t < sg.end) {
+#pragma unroll
+            for (int nj = 0; nj < kNJ; ++nj)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int b = jw + 16 * nj + 4 * lq + e;
+                if (b < dv) d = fmaf(O[ti][nj][e], to_f32<T>(xh[t * p.x.stride + b]), d);
+              }
+          }
+          d += __shfl_xor(d, 16);
+          d += __shfl_xor(d, 32);
+          if (lq == 0) Dots[wave * C + 16 * ti + li] = d;
+        }
+      }
+    }
+
+    if (kBeforeLast && !more && ends && p.out_seqs) save(p.out_seqs + by_seq);
+
+    // into the state
+    const float wd = Wd[0];
+#pragma unroll
+    for (int it = 0; it < kIT; ++it)
+#pragma unroll
+      for (int nj = 0; nj < kNJ; ++nj) S[it][nj] *= wd;
+    Frag vf[kTS][kNJ];
+#pragma unroll
+    for (int ts = 0; ts < kTS; ++ts) {
+      const f32x8 w = *reinterpret_cast<const f32x8 *>(&Wi[32 * ts + 8 * lq]);
+      Frag hi[kNJ], lo[kNJ];
+#pragma unroll
+      for (int nj = 0; nj < kNJ; ++nj) {
+        vf[ts][nj] = frag_by_column<kRowV>(Vs, 32 * ts, jw + 16 * nj, lane);
+        const f32x8 x = __builtin_convertvector(vf[ts][nj], f32x8) * w;
+        hi[nj] = to_frag(x, Frag{});
+        if constexpr (kBf16) lo[nj] = to_frag(x - __builtin_convertvector(hi[nj], f32x8), Frag{});
+      }
+#pragma unroll
+      for (int it = 0; it < kIT; ++it) {
+        const Frag a = frag_by_column<kRowK>(Ks, 32 * ts, 16 * it, lane);
+#pragma unroll
+        for (int nj = 0; nj < kNJ; ++nj) {
+          S[it][nj] = mma(a, hi[nj], S[it][nj]);
+          if constexpr (kBf16) S[it][nj] = mma(a, lo[nj], S[it][nj]);
+        }
+      }
+    }
+
+    __syncthreads();  // the pairs' products are in LDS; all else there is read
+    if (more) stage();
+    if (kOut) {
+#pragma unroll
+      for (int ti = 0; ti < kNT; ++ti)
+#pragma unroll
+        for (int ts = 0; ts < kTS; ++ts) {
+          if (kRev ? 2 * ts + 1 < ti : 2 * ts > ti) continue;  // no pair left
+          const Frag b = *reinterpret_cast<const Frag *>(&Ps[(16 * ti + li) * kRowP + 32 * ts + 8 * lq]);
+#pragma unroll
+          for (int nj = 0; nj < kNJ; ++nj) O[ti][nj] = mma(vf[ts][nj], b, O[ti][nj]);
+        }
+      const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
+      const int64_t out_stride = static_cast<int64_t>(p.plan.heads) * p.v.d;
+#pragma unroll
+      for (int ti = 0; ti < kNT; ++ti) {
+        const int64_t t = t0 + 16 * ti + li;
+        if (t < sg.end) {
+          const int64_t at = t * out_stride + h * p.v.d + j0;
+#pragma unroll
+          for (int nj = 0; nj < kNJ; ++nj) {
+            const int b = jw + 16 * nj + 4 * lq;
+            if (p.out_f32)
+              store4(static_cast<float *>(p.out) + at + b, O[ti][nj], dv - b, p.out_vec);
+            else
+              store4(static_cast<T *>(p.out) + at + b, O[ti][nj], dv - b, p.out_vec);
+          }
+        }
+      }
+      if constexpr (kDot) {
+        if (tid < C && t0 + tid < sg.end)
+          p.dots[(slice * p.plan.tokens + t0 + tid) * p.plan.heads + h] =
+              Dots[tid] + Dots[C + tid] + Dots[2 * C + tid] + Dots[3 * C + tid];
+      }
+    }
+  }
+
+  if (kMode == kLinState)
+    save(p.out_slots + by_slot);
+  else if (!kBeforeLast && p.out_seqs && ends)
+    save(p.out_seqs + by_seq);
+  if (kMode == kLinState && tid == 0 && slice == 0)
+    p.out_decay[slot * p.plan.heads + h] = fast_exp2(static_cast<float>(total));
+}
+
+template <typename T, int kDK, int kNJ, int kMode, bool kRev>
+int launch_core_t(const LinCore &a, hipStream_t s) {
+  const int64_t slices = (a.v.d + 64 * kNJ - 1) / (64 * kNJ);
+  hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kNJ, kMode, kRev>),
+                     dim3(static_cast<unsigned>(a.plan.slots * a.plan.heads * slices)), dim3(256),
+                     0, s, a);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename T, int kDK, int kNJ>
+int launch_core_m(const LinCore &a, int mode, bool reverse, hipStream_t s) {
+  if (mode == kLinState)
+    return reverse ? launch_core_t<T, kDK, kNJ, kLinState, true>(a, s)
+                   : launch_core_t<T, kDK, kNJ, kLinState, false>(a, s);
+  if (mode == kLinOut)
+    return reverse ? launch_core_t<T, kDK, kNJ, kLinOut, true>(a, s)
+                   : launch_core_t<T, kDK, kNJ, kLinOut, false>(a, s);
+  return reverse ? launch_core_t<T, kDK, kNJ, kLinOutDot, true>(a, s)
+                 : launch_core_t<T, kDK, kNJ, kLinOutDot, false>(a, s);
+}
+
+}  // namespace lin
+}  // namespace ssm
