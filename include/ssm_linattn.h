@@ -21,8 +21,8 @@
  *   states      (sequences, heads, qk_dim, v_dim) fp32 dense
  * Value head h uses query/key head h / (heads / qk_heads).  A row stride
  * larger than the row lets q, k and v be parts of one projection's output.
- * Sizes: qk_dim and v_dim 1..256; heads a multiple of qk_heads; activations
- * fp32 or bf16 (ssm_dtype).  bf16 rows whose starts, strides and head sizes
+ * Sizes: qk_dim and v_dim 1..256; heads a multiple of qk_heads; row strides
+ * up to 2^22; activations fp32 or bf16 (ssm_dtype).  bf16 rows whose starts, strides and head sizes
  * are multiples of 16 bytes are read 16 bytes at a time; others element by
  * element.
  *

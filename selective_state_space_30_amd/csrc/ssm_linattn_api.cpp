@@ -69,6 +69,9 @@ int check_workspace(const void *workspace, size_t have, size_t need) {
   return SSM_OK;
 }
 
+// Row strides: a chunk of rows is addressed by 32-bit byte offsets.
+constexpr int64_t kMaxStride = int64_t(1) << 22;
+
 // Workgroups of 256 threads a launch may have (2^32 threads).
 constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
 
@@ -146,6 +149,8 @@ bool many_segments(const Sizes &z, const ssm::LinPlan &p) {
 }
 
 int check_plan(const Sizes &z, const ssm::LinPlan &p) {
+  if (z.heads * z.dk > kMaxStride || z.heads * z.dv > kMaxStride)
+    return fail(SSM_ERR_UNSUPPORTED, "heads=%lld: rows too long", (long long)z.heads);
   // the widest grids: slices of 64 columns, and chunks of token pairs
   if (p.slots * z.heads * 4 > kMaxGroups ||
       p.slots * (p.seg_len / ssm::linattn_chunk(z.bf16())) * z.heads > kMaxGroups)
@@ -210,9 +215,12 @@ BwdLayout bwd_layout(const Sizes &z, const ssm::LinPlan &p, int want_dg) {
 }
 
 int check_stride(const char *name, int64_t stride, int64_t row) {
-  if (stride < row || stride >= (int64_t(1) << 31))
+  if (stride < row)
     return fail(SSM_ERR_INVALID_ARG, "%s_stride=%lld: rows have %lld elements", name,
                 (long long)stride, (long long)row);
+  if (stride > kMaxStride)
+    return fail(SSM_ERR_UNSUPPORTED, "%s_stride=%lld: this build supports up to %lld", name,
+                (long long)stride, (long long)kMaxStride);
   return SSM_OK;
 }
 
@@ -268,10 +276,6 @@ bool rows16(const void *p, int64_t stride, int64_t d, int64_t es) {
 
 ssm::LinSide side(const void *p, int64_t stride, int64_t d, int64_t div) {
   return ssm::LinSide{p, stride, static_cast<int>(d), static_cast<int>(div)};
-}
-
-bool out_rows(const void *p, int64_t d, int64_t es) {
-  return d % 4 == 0 && aligned(p, 4 * es);
 }
 
 }  // namespace
@@ -339,7 +343,7 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
 
   plan.cu = cu_seqlens;
   plan.vec = rows16(q, q_stride, qk_dim, es) && rows16(k, k_stride, qk_dim, es) &&
-             rows16(v, v_stride, v_dim, es);
+             rows16(v, v_stride, v_dim, es) && aligned(o, 16);
   const int64_t div = heads / qk_heads;
   ssm::LinCore a{};
   a.plan = plan;
@@ -351,7 +355,7 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   a.inter = a.inside = scale;
   a.into = 1.0f;
   a.in_seqs = h0;
-  a.sa = v_dim;
+  a.sa = static_cast<int>(v_dim);
   a.sb = 1;
   int err;
   if (l.total) {
@@ -366,7 +370,6 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   }
   a.out_seqs = h_final;
   a.out = o;
-  a.out_vec = out_rows(o, v_dim, es);
   if ((err = ssm::launch_linattn_core(a, ssm::kLinOut, false, z.bf16(), stream)) != 0)
     return hip_failed(err);
   return ok();
@@ -434,7 +437,8 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   plan.cu = cu_seqlens;
   const int64_t o_stride = heads * v_dim;
   plan.vec = rows16(q, q_stride, qk_dim, es) && rows16(k, k_stride, qk_dim, es) &&
-             rows16(v, v_stride, v_dim, es) && rows16(d_o, o_stride, v_dim, es);
+             rows16(v, v_stride, v_dim, es) && rows16(d_o, o_stride, v_dim, es) &&
+             aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16);
   const int64_t div = heads / qk_heads;
   const bool bf16 = z.bf16(), many = many_segments(z, plan);
   char *w = static_cast<char *>(workspace);
@@ -454,7 +458,7 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     a.k = K;
     a.v = V;
     a.into = 1.0f;
-    a.sa = v_dim;
+    a.sa = static_cast<int>(v_dim);
     a.sb = 1;
     a.out_slots = f32(l.states);
     a.out_decay = f32(l.decay);
@@ -485,10 +489,9 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     a.in_slots = many ? f32(l.states) : nullptr;
     a.in_seqs = h0;
     a.sa = 1;
-    a.sb = v_dim;
+    a.sb = static_cast<int>(v_dim);
     a.out = shared ? static_cast<void *>(f32(l.dq)) : dq;
     a.out_f32 = shared;
-    a.out_vec = shared ? qk_dim % 4 == 0 : out_rows(dq, qk_dim, es);
     if (want_dg) {
       a.x = Q;
       a.dots = f32(l.xdots);
@@ -506,10 +509,9 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     a.in_slots = many ? f32(l.adjoints) : nullptr;
     a.in_seqs = dh_final;
     a.sa = 1;
-    a.sb = v_dim;
+    a.sb = static_cast<int>(v_dim);
     a.out = shared ? static_cast<void *>(f32(l.dk)) : dk;
     a.out_f32 = shared;
-    a.out_vec = shared ? qk_dim % 4 == 0 : out_rows(dk, qk_dim, es);
     if (want_dg) {
       a.x = K;
       a.dots = f32(l.ydots);
@@ -525,10 +527,9 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     a.inside = a.into = scale;
     a.in_slots = many ? f32(l.adjoints) : nullptr;
     a.in_seqs = dh_final;
-    a.sa = v_dim;
+    a.sa = static_cast<int>(v_dim);
     a.sb = 1;
     a.out = dv;
-    a.out_vec = out_rows(dv, v_dim, es);
     a.out_seqs = dh0;
     if ((err = ssm::launch_linattn_core(a, ssm::kLinOut, true, bf16, stream)) != 0)
       return hip_failed(err);

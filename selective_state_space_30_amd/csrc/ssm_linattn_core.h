@@ -21,6 +21,8 @@
 // overflows nor cancels.
 #pragma once
 
+#include <type_traits>
+
 #include "ssm_device.h"
 #include "ssm_linattn_internal.h"
 
@@ -105,6 +107,13 @@ __device__ __forceinline__ bf16x8 to_frag(f32x8 v, bf16x8) {
 }
 __device__ __forceinline__ f32x8 to_frag(f32x8 v, f32x8) { return v; }
 
+// The value, known to be the same in every lane, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // Where a segment lies.
 struct Segment {
   int64_t begin, end;  // token rows
@@ -150,9 +159,12 @@ __device__ __forceinline__ Segment segment_of(const LinPlan &p, int64_t slot) {
     }
     s.seq = lo;
   }
-  s.seg = static_cast<int>(slot - first_slot(p, s.seq));
+  s.seq = __builtin_amdgcn_readfirstlane(s.seq);
+  s.seg = __builtin_amdgcn_readfirstlane(static_cast<int>(slot - first_slot(p, s.seq)));
   int64_t b, e;
   sequence_rows(p, s.seq, &b, &e);
+  b = uniform(b);
+  e = uniform(e);
   s.begin = b + s.seg * p.seg_len;
   // an empty sequence has one (empty) segment, which hands its state on
   s.real = s.seg >= 0 && (s.begin < e || s.seg == 0);
@@ -183,37 +195,57 @@ __device__ __forceinline__ double wave_sums(double v, int lane) {
   return v;
 }
 
-// 16-byte pieces of kRows token rows of one head, `cols` elements wide in
-// LDS (the head's d, zeros behind), from memory to registers.  Rows behind
-// `rows` are zeros and are not read.
-template <typename T, int kRows, int kCols>
+// Byte view of `rows` token rows (wave-uniform) for buffer loads: what lies
+// behind the last row's end reads as 0.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const T *base, int64_t stride,
+                                                            int rows, int d) {
+  const int bytes = rows > 0 ? static_cast<int>(((rows - 1) * stride + d) * sizeof(T)) : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(base), 0, bytes, kBufferWord3);
+}
+
+constexpr int kNowhere = 0x7ffffff0;  // behind the end of every view
+
+// kRows token rows of one head, kCols elements wide in LDS (the head's d,
+// zeros behind), from memory to registers in pieces of 16 bytes.  Byte
+// offsets are the same for every chunk; rows behind the sequence's end lie
+// behind the view.  Without kVec the pieces are put together from elements.
+template <typename T, int kRows, int kCols, bool kVec>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(T);           // elements of a piece
   static constexpr int kRowPieces = kCols / kPer;
   static constexpr int kPieces = kRows * kRowPieces / 256;
   static_assert(kRows * kRowPieces % 256 == 0, "whole pieces per thread");
+  static_assert(256 % kRowPieces == 0, "a thread's pieces are in one column");
   u32x4 r[kPieces];
 
-  __device__ __forceinline__ void load(const T *base, int64_t stride, int rows, int d, bool vec,
-                                       int tid) {
+  __device__ __forceinline__ void load(const T *base, int64_t stride, int rows, int d, int tid) {
+    const __amdgpu_buffer_rsrc_t v = rows_view(base, stride, rows, d);
+    const int c = tid % kRowPieces * kPer;
+    const int row_bytes = static_cast<int>(stride * sizeof(T));
+    // (past kNowhere the offsets stay, unsigned, behind every view)
+    unsigned off0 = c < d ? tid / kRowPieces * row_bytes + c * sizeof(T) : kNowhere;
+    asm volatile("" : "+v"(off0));  // one register from chunk to chunk, not one a piece
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int q = tid + 256 * i, row = q / kRowPieces, c = (q % kRowPieces) * kPer;
-      r[i] = u32x4{0u, 0u, 0u, 0u};
-      if (row < rows && c < d) {
-        const T *p = base + row * stride + c;
-        if (vec) {
-          r[i] = *reinterpret_cast<const u32x4 *>(p);
+      const int off = static_cast<int>(off0 + static_cast<unsigned>(i * (256 / kRowPieces)) * row_bytes);
+      if constexpr (kVec) {
+        r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(v, off, 0, 0));
+      } else {
+        const int left = d - c;  // elements of the row from here
+        if constexpr (sizeof(T) == 2) {
+          uint32_t e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            e[k] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
+                v, k < left ? off + 2 * k : kNowhere, 0, 0));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[i][k] = e[2 * k] | (e[2 * k + 1] << 16);
         } else {
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            if (c + e < d) {
-              if constexpr (sizeof(T) == 2)
-                r[i][e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e % 2));
-              else
-                r[i][e] = __builtin_bit_cast(uint32_t, p[e]);
-            }
-          }
+          for (int k = 0; k < 4; ++k)
+            r[i][k] = __builtin_amdgcn_raw_buffer_load_b32(
+                v, k < left ? off + 4 * k : kNowhere, 0, 0);
         }
       }
     }
@@ -229,25 +261,68 @@ struct Tile {
   }
 };
 
-__device__ __forceinline__ void store4(uint16_t *p, f32x4 v, int n, bool vec) {
-  if (vec && n >= 4) {
-    uint2 w;
-    w.x = pack_bf16x2(v[0], v[1]);
-    w.y = pack_bf16x2(v[2], v[3]);
-    *reinterpret_cast<uint2 *>(p) = w;
+// 4 neighbouring elements at a byte offset of a view, n of them in the row,
+// as they are in memory.
+template <typename T, bool kVec>
+struct Four {
+  uint32_t w[sizeof(T)];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t v, int off, int n) {
+    if constexpr (kVec && sizeof(T) == 2) {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(v, n > 0 ? off : kNowhere, 0, 0);
+      w[0] = x[0];
+      w[1] = x[1];
+    } else if constexpr (kVec) {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b128(v, n > 0 ? off : kNowhere, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = x[e];
+    } else if constexpr (sizeof(T) == 2) {
+      uint32_t x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = static_cast<uint16_t>(
+            __builtin_amdgcn_raw_buffer_load_b16(v, e < n ? off + 2 * e : kNowhere, 0, 0));
+      w[0] = x[0] | (x[1] << 16);
+      w[1] = x[2] | (x[3] << 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = __builtin_amdgcn_raw_buffer_load_b32(v, e < n ? off + 4 * e : kNowhere, 0, 0);
+    }
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 2)
+      return e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    else
+      return __builtin_bit_cast(float, w[e]);
+  }
+};
+
+// Stores 4 neighbouring elements at a byte offset of a view, n of them in
+// the row.  (A store behind the view is dropped.)
+template <bool kVec>
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t v, int off, f32x4 x, int n,
+                                       uint16_t) {
+  if constexpr (kVec) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(
+        u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, v, n > 0 ? off : kNowhere, 0, 0);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (e < n) p[e] = from_f32<uint16_t>(v[e]);
+      __builtin_amdgcn_raw_buffer_store_b16(from_f32<uint16_t>(x[e]), v,
+                                            e < n ? off + 2 * e : kNowhere, 0, 0);
   }
 }
-__device__ __forceinline__ void store4(float *p, f32x4 v, int n, bool vec) {
-  if (vec && n >= 4) {
-    *reinterpret_cast<f32x4 *>(p) = v;
+template <bool kVec>
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t v, int off, f32x4 x, int n, float) {
+  if constexpr (kVec) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), v,
+                                           n > 0 ? off : kNowhere, 0, 0);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (e < n) p[e] = v[e];
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[e]), v,
+                                            e < n ? off + 4 * e : kNowhere, 0, 0);
   }
 }
 
@@ -266,8 +341,8 @@ __device__ __forceinline__ void store4(float *p, f32x4 v, int n, bool vec) {
 // (2^-16), since the state is returned in 32 bits and is carried over the
 // sequence; likewise the state itself where dot products in 32 bits are
 // wanted (kLinOutDot).
-template <typename T, int kDK, int kNJ, int kMode, bool kRev>
-__global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
+template <typename T, int kDK, int kNJ, int kMode, bool kRev, bool kVec>
+__global__ __launch_bounds__(256, 2) void linattn_core_kernel(LinCore p) {
   typedef Traits<T> Tr;
   typedef typename Tr::Frag Frag;
   typedef typename Tr::Elem Elem;
@@ -292,9 +367,9 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int slices = (p.v.d + kDV - 1) / kDV;
-  const int slice = blockIdx.x % slices;
-  const int h = blockIdx.x / slices % p.plan.heads;
-  const int64_t slot = blockIdx.x / slices / p.plan.heads;
+  const int slice = blockIdx.x % static_cast<unsigned>(slices);
+  const int h = blockIdx.x / static_cast<unsigned>(slices) % static_cast<unsigned>(p.plan.heads);
+  const int64_t slot = blockIdx.x / (static_cast<unsigned>(slices) * p.plan.heads);
   const Segment sg = segment_of(p.plan, slot);
   if (!sg.real) return;
   const bool ends = kRev ? sg.seg == 0 : sg.last;  // nothing comes after it
@@ -304,7 +379,6 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
   const int dk = p.k.d, dv = p.v.d - j0;     // columns from this slice's first
   const int64_t n = sg.end - sg.begin;
   const int chunks = static_cast<int>((n + C - 1) / C);
-  const bool vec = p.plan.vec;
   const T *qh = static_cast<const T *>(p.q.p) + (h / p.q.div) * p.q.d;
   const T *kh = static_cast<const T *>(p.k.p) + (h / p.k.div) * p.k.d;
   const T *vh = static_cast<const T *>(p.v.p) + (h / p.v.div) * p.v.d + j0;
@@ -315,6 +389,16 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
   const int64_t size = static_cast<int64_t>(p.k.d) * p.v.d;
   const int64_t by_slot = (slot * p.plan.heads + h) * size;
   const int64_t by_seq = (static_cast<int64_t>(sg.seq) * p.plan.heads + h) * size;
+  auto state_view = [&](const float *at) __attribute__((always_inline)) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(at), 0,
+                                             static_cast<int>(size * sizeof(float)), kBufferWord3);
+  };
+  const int state0 = 4 * (4 * lq * p.sa + (j0 + jw + li) * p.sb);
+  auto state_off = [&](int it, int nj, int e) __attribute__((always_inline)) {
+    const int off = state0 + 4 * ((16 * it + e) * p.sa + 16 * nj * p.sb);
+    const bool in = 16 * it + 4 * lq + e < dk && jw + 16 * nj + li < dv;
+    return in ? off : kNowhere;
+  };
   {
     const float *in = nullptr;
     if (kMode != kLinState)
@@ -322,37 +406,43 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
 #pragma unroll
     for (int it = 0; it < kIT; ++it)
 #pragma unroll
-      for (int nj = 0; nj < kNJ; ++nj)
+      for (int nj = 0; nj < kNJ; ++nj) S[it][nj] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (in) {
+      const __amdgpu_buffer_rsrc_t v = state_view(in);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int a = 16 * it + 4 * lq + e, b = jw + 16 * nj + li;
-          S[it][nj][e] = in && a < dk && b < dv ? in[a * p.sa + (j0 + b) * p.sb] : 0.0f;
-        }
+      for (int it = 0; it < kIT; ++it)
+#pragma unroll
+        for (int nj = 0; nj < kNJ; ++nj)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            S[it][nj][e] = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(v, state_off(it, nj, e), 0, 0));
+    }
   }
   auto save = [&](float *out) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t v = state_view(out);
 #pragma unroll
     for (int it = 0; it < kIT; ++it)
 #pragma unroll
       for (int nj = 0; nj < kNJ; ++nj)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int a = 16 * it + 4 * lq + e, b = jw + 16 * nj + li;
-          if (a < dk && b < dv) out[a * p.sa + (j0 + b) * p.sb] = S[it][nj][e];
-        }
+        for (int e = 0; e < 4; ++e)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[it][nj][e]), v,
+                                                state_off(it, nj, e), 0, 0);
   };
   // the decay's gradient needs the state before a sequence's last chunk
   constexpr bool kBeforeLast = kDot && !kRev;
   double total = 0.0;  // state pass: the segment's sum of decays (wave 0)
 
-  Tile<T, C, kDK> tq, tk;
-  Tile<T, C, kDV> tv;
+  Tile<T, C, kDK, kVec> tq, tk;
+  Tile<T, C, kDV, kVec> tv;
   float gt = 0.0f;
   auto load = [&](int c) __attribute__((always_inline)) {
     const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
     const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
-    if (kOut) tq.load(qh + t0 * p.q.stride, p.q.stride, rows, p.q.d, vec, tid);
-    tk.load(kh + t0 * p.k.stride, p.k.stride, rows, dk, vec, tid);
-    tv.load(vh + t0 * p.v.stride, p.v.stride, rows, dv, vec, tid);
+    if (kOut) tq.load(qh + t0 * p.q.stride, p.q.stride, rows, p.q.d, tid);
+    tk.load(kh + t0 * p.k.stride, p.k.stride, rows, dk, tid);
+    tv.load(vh + t0 * p.v.stride, p.v.stride, rows, dv, tid);
     gt = 0.0f;
     if (wave == 0 && lane < rows) gt = decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h);
   };
@@ -385,38 +475,58 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
     const bool more = i + 1 < chunks;
     __syncthreads();  // the chunk is staged
     if (more) load(c + step);
+    Four<T, kVec> xr[kDot ? kNT : 1][kNJ];  // x's rows where this lane has outputs
+    if constexpr (kDot) {
+      const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
+      const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
+      const T *xh = static_cast<const T *>(p.x.p) + t0 * p.x.stride + (h / p.x.div) * p.x.d + j0;
+      const __amdgpu_buffer_rsrc_t v = rows_view(xh, p.x.stride, rows, dv);
+      const int b = jw + 4 * lq, row = static_cast<int>(p.x.stride * sizeof(T));
+      int off = li * row + b * static_cast<int>(sizeof(T));
+      asm volatile("" : "+v"(off));
+#pragma unroll
+      for (int ti = 0; ti < kNT; ++ti)
+#pragma unroll
+        for (int nj = 0; nj < kNJ; ++nj)
+          xr[ti][nj].load(v, off + 16 * ti * row + 16 * nj * static_cast<int>(sizeof(T)),
+                          dv - b - 16 * nj);
+    }
 
     if (kOut) {
       // token pairs: wave w takes the tokens t of tile w (32-bit chunks have
       // 2 tiles: two waves a tile, each half of the s)
+      constexpr int kSub = kNT == 4 ? 4 : 1;
       const int ti = kNT == 4 ? wave : wave >> 1;
-      const int s_lo = kNT == 4 ? 0 : wave & 1, s_hi = kNT == 4 ? kNT : (wave & 1) + 1;
+      const int s0 = kNT == 4 ? 0 : wave & 1;
       const double at = As[16 * ti + li];
+      f32x4 acc[kSub];
 #pragma unroll
-      for (int si = 0; si < kNT; ++si) {
-        if (si < s_lo || si >= s_hi) continue;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        const bool some = kRev ? si >= ti : si <= ti;
-        if (some) {
+      for (int si = 0; si < kSub; ++si) acc[si] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int ks = 0; ks < kKS; ++ks) {
-            const Frag a = *reinterpret_cast<const Frag *>(&Ks[(16 * si + li) * kRowK + 32 * ks + 8 * lq]);
-            const Frag b = *reinterpret_cast<const Frag *>(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 8 * lq]);
-            acc = mma(a, b, acc);
-          }
+      for (int ks = 0; ks < kKS; ++ks) {
+        const Frag b = *reinterpret_cast<const Frag *>(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 8 * lq]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int s = 16 * si + 4 * lq + e, t = 16 * ti + li;
-            const double as = As[s];
-            const float w = fast_exp2(static_cast<float>(kRev ? as - at : at - as));
-            acc[e] = (kRev ? s >= t : s <= t) ? acc[e] * w * p.inside : 0.0f;
-          }
+        for (int si = 0; si < kSub; ++si) {
+          const Frag a = *reinterpret_cast<const Frag *>(
+              &Ks[(16 * (s0 + si) + li) * kRowK + 32 * ks + 8 * lq]);
+          acc[si] = mma(a, b, acc[si]);
         }
-        Elem *d = &Ps[(16 * ti + li) * kRowP + 16 * si + 4 * lq];
+      }
+#pragma unroll
+      for (int si = 0; si < kSub; ++si) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = 16 * (s0 + si) + 4 * lq + e, t = 16 * ti + li;
+          const double as = As[s];
+          float w = fast_exp2(static_cast<float>(kRev ? as - at : at - as));
+          asm volatile("" : "+v"(w));  // all lanes compute it: no branch for it
+          acc[si][e] = (kRev ? s >= t : s <= t) ? acc[si][e] * w * p.inside : 0.0f;
+        }
+        Elem *d = &Ps[(16 * ti + li) * kRowP + 16 * (s0 + si) + 4 * lq];
         if constexpr (kBf16)
-          *reinterpret_cast<bf16x4 *>(d) = __builtin_convertvector(acc, bf16x4);
+          *reinterpret_cast<bf16x4 *>(d) = __builtin_convertvector(acc[si], bf16x4);
         else
-          *reinterpret_cast<f32x4 *>(d) = acc;
+          *reinterpret_cast<f32x4 *>(d) = acc[si];
       }
     }
 
@@ -455,21 +565,13 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
       }
       if constexpr (kDot) {
         // dot products of the state's part with x's rows, this wave's columns
-        const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
-        const T *xh = static_cast<const T *>(p.x.p) + (h / p.x.div) * p.x.d + j0;
 #pragma unroll
         for (int ti = 0; ti < kNT; ++ti) {
-          const int64_t t = t0 + 16 * ti + li;
           float d = 0.0f;
-          if (t < sg.end) {
 #pragma unroll
-            for (int nj = 0; nj < kNJ; ++nj)
+          for (int nj = 0; nj < kNJ; ++nj)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int b = jw + 16 * nj + 4 * lq + e;
-                if (b < dv) d = fmaf(O[ti][nj][e], to_f32<T>(xh[t * p.x.stride + b]), d);
-              }
-          }
+            for (int e = 0; e < 4; ++e) d = fmaf(O[ti][nj][e], xr[ti][nj][e], d);
           d += __shfl_xor(d, 16);
           d += __shfl_xor(d, 32);
           if (lq == 0) Dots[wave * C + 16 * ti + li] = d;
@@ -521,22 +623,27 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
           for (int nj = 0; nj < kNJ; ++nj) O[ti][nj] = mma(vf[ts][nj], b, O[ti][nj]);
         }
       const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
+      const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
       const int64_t out_stride = static_cast<int64_t>(p.plan.heads) * p.v.d;
+      const int64_t at = t0 * out_stride + h * p.v.d + j0;
+      auto write = [&](auto *out) __attribute__((always_inline)) {
+        typedef std::remove_reference_t<decltype(*out)> E;
+        constexpr int kSize = sizeof(E);
+        const __amdgpu_buffer_rsrc_t v = rows_view(out + at, out_stride, rows, dv);
+        const int b = jw + 4 * lq, row = static_cast<int>(out_stride) * kSize;
+        int off = li * row + b * kSize;
+        asm volatile("" : "+v"(off));
 #pragma unroll
-      for (int ti = 0; ti < kNT; ++ti) {
-        const int64_t t = t0 + 16 * ti + li;
-        if (t < sg.end) {
-          const int64_t at = t * out_stride + h * p.v.d + j0;
+        for (int ti = 0; ti < kNT; ++ti)
 #pragma unroll
-          for (int nj = 0; nj < kNJ; ++nj) {
-            const int b = jw + 16 * nj + 4 * lq;
-            if (p.out_f32)
-              store4(static_cast<float *>(p.out) + at + b, O[ti][nj], dv - b, p.out_vec);
-            else
-              store4(static_cast<T *>(p.out) + at + b, O[ti][nj], dv - b, p.out_vec);
-          }
-        }
-      }
+          for (int nj = 0; nj < kNJ; ++nj)
+            store4<kVec>(v, off + 16 * ti * row + 16 * nj * kSize, O[ti][nj], dv - b - 16 * nj,
+                         E(0));
+      };
+      if (p.out_f32)
+        write(static_cast<float *>(p.out));
+      else
+        write(static_cast<T *>(p.out));
       if constexpr (kDot) {
         if (tid < C && t0 + tid < sg.end)
           p.dots[(slice * p.plan.tokens + t0 + tid) * p.plan.heads + h] =
@@ -556,9 +663,13 @@ __global__ __launch_bounds__(256) void linattn_core_kernel(LinCore p) {
 template <typename T, int kDK, int kNJ, int kMode, bool kRev>
 int launch_core_t(const LinCore &a, hipStream_t s) {
   const int64_t slices = (a.v.d + 64 * kNJ - 1) / (64 * kNJ);
-  hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kNJ, kMode, kRev>),
-                     dim3(static_cast<unsigned>(a.plan.slots * a.plan.heads * slices)), dim3(256),
-                     0, s, a);
+  const dim3 grid(static_cast<unsigned>(a.plan.slots * a.plan.heads * slices));
+  if (a.plan.vec)
+    hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kNJ, kMode, kRev, true>), grid, dim3(256), 0, s,
+                       a);
+  else
+    hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kNJ, kMode, kRev, false>), grid, dim3(256), 0,
+                       s, a);
   return static_cast<int>(hipGetLastError());
 }
 

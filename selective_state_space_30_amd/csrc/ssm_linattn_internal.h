@@ -25,7 +25,7 @@ struct LinPlan {
   int64_t segs;         // equal sequences: segments of each
   int64_t slots;        // segments over all sequences (upper bound if packed)
   int nseq, heads;
-  int vec;              // every row piece of 16 bytes may be loaded whole
+  int vec;              // every row piece of 16 bytes may be moved whole
 };
 
 // One (tokens, heads, d) operand.
@@ -54,10 +54,9 @@ struct LinCore {
   // token order: instead the state before each sequence's last chunk
   float *out_slots, *out_seqs;
   float *out_decay;     // state pass: exp of each segment's sum of decays (slot, head)
-  int64_t sa, sb;
+  int sa, sb;
   void *out;            // (tokens, heads, v.d), or null (state pass)
   int out_f32;          // out in fp32 whatever the activations
-  int out_vec;          // out rows start on 4-element boundaries
   // the inter part's dot products with the rows of x: dots (slice, tokens, heads)
   LinSide x;
   float *dots;

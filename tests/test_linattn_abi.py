@@ -45,9 +45,9 @@ SHARED = [
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(heads=0), 1), (dict(qk_heads=0), 1), (dict(qk_heads=3), 1), (dict(dk=0), 1),
     (dict(dv=0), 1), (dict(dk=257, qs=600, ks=600), 2), (dict(dv=257, vs=2000), 2),
-    (dict(qs=127), 1), (dict(ks=0), 1), (dict(vs=255), 1), (dict(vs=1 << 31), 1),
+    (dict(qs=127), 1), (dict(ks=0), 1), (dict(vs=255), 1), (dict(vs=(1 << 22) + 1), 2),
     (dict(q=at(1, 1)), 1), (dict(v=at(3, 1)), 1), (dict(g=at(4, 2)), 1),
-    (dict(heads=1 << 17, qk_heads=1 << 17, qs=1 << 23, ks=1 << 23, vs=1 << 23), 2),
+    (dict(heads=1 << 17, qk_heads=1 << 17), 2),
 ]
 SEQS = SHARED + [
     (dict(tokens=-1), 1), (dict(nseq=0), 1), (dict(tokens=127), 1), (dict(tokens=1 << 31), 2),
