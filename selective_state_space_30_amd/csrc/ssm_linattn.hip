@@ -10,44 +10,40 @@ using namespace lin;
 
 // ------------------------------------------------------- segment states ---
 // Per (sequence, head): what each segment adds to the state -> the state
-// that enters it, one segment after another.  Each thread carries kPer
-// elements; the next segment's are requested before this one's are replaced.
-constexpr int kChainPer = 4;
+// that enters it, one segment after another.  A thread carries one element;
+// kAhead segments are requested at once, so that the latency of memory is
+// paid once for all of them.
+constexpr int kAhead = 8;
 
 __global__ __launch_bounds__(256) void linattn_chain_kernel(LinChain p) {
-  const int h = blockIdx.x % p.plan.heads;
-  const int seq = blockIdx.x / p.plan.heads;
+  const int h = blockIdx.x % static_cast<unsigned>(p.plan.heads);
+  const int seq = blockIdx.x / static_cast<unsigned>(p.plan.heads);
   int64_t b, e;
   sequence_rows(p.plan, seq, &b, &e);
   int64_t segs = (e - b + p.plan.seg_len - 1) / p.plan.seg_len;
   if (segs < 1) segs = 1;
-  const int64_t slot0 = first_slot(p.plan, seq);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.y) * 256 * kChainPer + threadIdx.x;
-  const int64_t by_seq = (static_cast<int64_t>(seq) * p.plan.heads + h) * p.size;
-  float acc[kChainPer], cur[kChainPer], next[kChainPer];
-  auto slot_at = [&](int64_t k) { return slot0 + (p.reverse ? segs - 1 - k : k); };
-  auto fetch = [&](int64_t k, float *v) {
-    const float *s = p.states + (slot_at(k) * p.plan.heads + h) * p.size;
+  const int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
+  if (i >= p.size) return;
+  const int64_t slot0 = first_slot(p.plan, seq) + (p.reverse ? segs - 1 : 0);
+  const int64_t step = p.reverse ? -p.plan.heads : p.plan.heads;  // cells
+  const int64_t cell0 = slot0 * p.plan.heads + h;
+  float acc = p.first ? p.first[(static_cast<int64_t>(seq) * p.plan.heads + h) * p.size + i] : 0.0f;
+  for (int64_t k = 0; k < segs; k += kAhead) {
+    float add[kAhead], decay[kAhead];
 #pragma unroll
-    for (int i = 0; i < kChainPer; ++i) v[i] = i0 + 256 * i < p.size ? s[i0 + 256 * i] : 0.0f;
-  };
-#pragma unroll
-  for (int i = 0; i < kChainPer; ++i) {
-    acc[i] = p.first && i0 + 256 * i < p.size ? p.first[by_seq + i0 + 256 * i] : 0.0f;
-    cur[i] = next[i] = 0.0f;
-  }
-  // nothing reads what the last segment adds
-  if (segs > 1) fetch(0, cur);
-  for (int64_t k = 0; k < segs; ++k) {
-    if (k + 2 < segs) fetch(k + 1, next);
-    float *s = p.states + (slot_at(k) * p.plan.heads + h) * p.size;
-    const float d = k + 1 < segs ? p.decay[slot_at(k) * p.plan.heads + h] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kChainPer; ++i) {
-      if (i0 + 256 * i < p.size) s[i0 + 256 * i] = acc[i];
-      acc[i] = fmaf(acc[i], d, cur[i]);
-      cur[i] = next[i];
+    for (int j = 0; j < kAhead; ++j) {
+      // nothing reads what the last segment adds
+      const bool in = k + j + 1 < segs;
+      const int64_t cell = cell0 + (in ? k + j : 0) * step;
+      add[j] = in ? p.states[cell * p.size + i] : 0.0f;
+      decay[j] = in ? p.decay[cell] : 0.0f;
     }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (k + j < segs) {
+        p.states[(cell0 + (k + j) * step) * p.size + i] = acc;
+        acc = fmaf(acc, decay[j], add[j]);
+      }
   }
 }
 
@@ -372,10 +368,12 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(LinStep p) {
 
 int linattn_chunk(bool bf16) { return bf16 ? kLinChunkBf16 : kLinChunkF32; }
 
-// Output columns of a workgroup.  128 halve what the waves read of q and k
-// per output; 64 where there are no more, where the state's registers do
-// not allow more (q and k heads over 128 wide), and in 32 bits.
-int linattn_slice(bool bf16, int dk, int dv) { return bf16 && dk <= 128 && dv > 64 ? 128 : 64; }
+int linattn_slice(int dv) { return dv > 64 ? 128 : 64; }
+
+bool linattn_pairs_heads(const LinCore &a, int mode) {
+  return mode != kLinOutDot && a.v.d <= 64 && a.k.div % 2 == 0 &&
+         (mode == kLinState || a.q.div % 2 == 0);
+}
 
 int launch_linattn_core(const LinCore &a, int mode, bool reverse, bool bf16, void *stream) {
   return bf16 ? launch_linattn_core_bf16(a, mode, reverse, stream)
@@ -383,7 +381,7 @@ int launch_linattn_core(const LinCore &a, int mode, bool reverse, bool bf16, voi
 }
 
 int launch_linattn_chain(const LinChain &a, void *stream) {
-  const int64_t parts = (a.size + 256 * kChainPer - 1) / (256 * kChainPer);
+  const int64_t parts = (a.size + 255) / 256;
   hipLaunchKernelGGL(linattn_chain_kernel,
                      dim3(static_cast<unsigned>(a.plan.nseq * static_cast<int64_t>(a.plan.heads)),
                           static_cast<unsigned>(parts)),

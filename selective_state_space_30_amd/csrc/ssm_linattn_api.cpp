@@ -120,8 +120,7 @@ constexpr int64_t kMaxGradSegment = 1024;
 
 ssm::LinPlan make_plan(const Sizes &z, bool decay_grad) {
   const int64_t chunk = ssm::linattn_chunk(z.bf16());
-  const int64_t width = ssm::linattn_slice(z.bf16(), static_cast<int>(z.dk),
-                                           static_cast<int>(z.dv));
+  const int64_t width = ssm::linattn_slice(static_cast<int>(z.dv));
   const int64_t slices = (z.dv + width - 1) / width;
   const int64_t longest = z.packed ? z.tokens : z.tokens / z.nseq;
   const int64_t groups = z.nseq * z.heads * slices;
@@ -151,8 +150,8 @@ bool many_segments(const Sizes &z, const ssm::LinPlan &p) {
 int check_plan(const Sizes &z, const ssm::LinPlan &p) {
   if (z.heads * z.dk > kMaxStride || z.heads * z.dv > kMaxStride)
     return fail(SSM_ERR_UNSUPPORTED, "heads=%lld: rows too long", (long long)z.heads);
-  // the widest grids: slices of 64 columns, and chunks of token pairs
-  if (p.slots * z.heads * 4 > kMaxGroups ||
+  // the widest grids (of 512 threads): slices of 128 columns; chunks of token pairs
+  if (p.slots * z.heads * 4 > kMaxGroups || z.nseq * z.heads > kMaxGroups ||
       p.slots * (p.seg_len / ssm::linattn_chunk(z.bf16())) * z.heads > kMaxGroups)
     return fail(SSM_ERR_UNSUPPORTED, "tokens=%lld heads=%lld nseq=%lld: too many workgroups",
                 (long long)z.tokens, (long long)z.heads, (long long)z.nseq);
@@ -177,9 +176,9 @@ struct BwdLayout {
   int64_t states, adjoints, decay, adecay, last, dq, dk, pairs, xdots, ydots, dg, total;
 };
 
-int slices_of(const Sizes &z, int64_t contracted, int64_t out) {
-  const int w = ssm::linattn_slice(z.bf16(), static_cast<int>(contracted), static_cast<int>(out));
-  return static_cast<int>((out + w - 1) / w);
+int64_t slices_of(int64_t out) {
+  const int64_t w = ssm::linattn_slice(static_cast<int>(out));
+  return (out + w - 1) / w;
 }
 
 // want_dg: 0 no, 1 a token, 2 a head
@@ -206,8 +205,8 @@ BwdLayout bwd_layout(const Sizes &z, const ssm::LinPlan &p, int want_dg) {
     const int64_t one = z.tokens * z.heads * 4;
     l.last = take(z.nseq * z.heads * size);
     l.pairs = take(one);
-    l.xdots = take(one * slices_of(z, z.dv, z.dk));
-    l.ydots = take(one * slices_of(z, z.dv, z.dk));
+    l.xdots = take(one * slices_of(z.dk));
+    l.ydots = take(one * slices_of(z.dk));
     if (want_dg == 2) l.dg = take(one);
   }
   l.total = at;
@@ -544,7 +543,7 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     const ssm::LinPairs pr{plan, Q, K, V, O, g, base.g_kind, ssm::linattn_chunk(bf16), scale,
                            f32(l.pairs)};
     if ((err = ssm::launch_linattn_pairs(pr, bf16, stream)) != 0) return hip_failed(err);
-    const int slices = slices_of(z, v_dim, qk_dim);
+    const int slices = static_cast<int>(slices_of(qk_dim));
     ssm::LinDecayGrad a{};
     a.plan = plan;
     a.pairs = f32(l.pairs);

@@ -48,6 +48,7 @@ template <> struct Traits<uint16_t> {
   typedef bf16x4 Half;
   typedef __bf16 Elem;
   static constexpr int kChunk = kLinChunkBf16;
+  typedef float Sum;  // of decays, where two are subtracted: see As
   static constexpr bool kBf16 = true;
 };
 template <> struct Traits<float> {
@@ -55,6 +56,7 @@ template <> struct Traits<float> {
   typedef f32x4 Half;
   typedef float Elem;
   static constexpr int kChunk = kLinChunkF32;
+  typedef double Sum;
   static constexpr bool kBf16 = false;
 };
 
@@ -81,24 +83,27 @@ __device__ __forceinline__ f32x8 two_halves(const float *p) {
 }
 
 // Fragment of a row-major [position][column] LDS tile contracted over its
-// rows: lane l gets column col + l % 16, positions row + 8 * (l / 16) + e.
-// In bf16 the transposing LDS read hands every lane of 16 one column of the
-// 4 x 16 block that the 16 lanes address.
+// rows, `row` to `row` + 31: lane l gets column col + l % 16, and in elements
+// 0..3 the positions row + 4 * (l / 16) + e, in 4..7 those 16 further on (the
+// order of two_halves).  In bf16 the transposing LDS read hands every lane of
+// 16 one column of the 4 x 16 block that the 16 lanes address; 32 lanes read
+// 8 neighbouring rows at once, which lie 8 banks apart (measured: 2 cycles, as
+// without conflicts).
 template <int kStride>
 __device__ __forceinline__ bf16x8 frag_by_column(const __bf16 *tile, int row, int col, int lane) {
   const int li = lane & 15, lq = lane >> 4;
-  const __bf16 *p = tile + (row + 8 * lq + (li >> 2)) * kStride + col + 4 * (li & 3);
+  const __bf16 *p = tile + (row + 4 * lq + (li >> 2)) * kStride + col + 4 * (li & 3);
   typedef __attribute__((address_space(3))) s16x4 *Lds;
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 4 * kStride));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 16 * kStride));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 template <int kStride>
 __device__ __forceinline__ f32x8 frag_by_column(const float *tile, int row, int col, int lane) {
-  const float *p = tile + (row + 8 * (lane >> 4)) * kStride + col + (lane & 15);
+  const float *p = tile + (row + 4 * (lane >> 4)) * kStride + col + (lane & 15);
   f32x8 r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = p[e * kStride];
+  for (int e = 0; e < 8; ++e) r[e] = p[(e % 4 + e / 4 * 16) * kStride];
   return r;
 }
 
@@ -106,6 +111,13 @@ __device__ __forceinline__ bf16x8 to_frag(f32x8 v, bf16x8) {
   return __builtin_convertvector(v, bf16x8);
 }
 __device__ __forceinline__ f32x8 to_frag(f32x8 v, f32x8) { return v; }
+
+// The same value, unknown to the compiler: what is computed from it is made
+// anew where it is used, not kept in registers from chunk to chunk.
+__device__ __forceinline__ int anew(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 // The value, known to be the same in every lane, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t x) {
@@ -173,11 +185,11 @@ __device__ __forceinline__ Segment segment_of(const LinPlan &p, int64_t slot) {
   return s;
 }
 
-// log2 of a token's decay factor: g / ln 2, no less than -2^14 (whose
+// log2 of a token's decay factor: g / ln 2, no less than -256 (whose
 // exponential is 0 in 32 bits: -inf must not meet itself in a difference).
 __device__ __forceinline__ double log2_decay(float g) {
   const double x = static_cast<double>(g) * 1.4426950408889634;
-  return x < -16384.0 ? -16384.0 : x;
+  return x < -256.0 ? -256.0 : x;
 }
 
 __device__ __forceinline__ float decay_at(const float *g, int kind, int64_t t, int heads, int h) {
@@ -210,13 +222,13 @@ constexpr int kNowhere = 0x7ffffff0;  // behind the end of every view
 // zeros behind), from memory to registers in pieces of 16 bytes.  Byte
 // offsets are the same for every chunk; rows behind the sequence's end lie
 // behind the view.  Without kVec the pieces are put together from elements.
-template <typename T, int kRows, int kCols, bool kVec>
+template <typename T, int kRows, int kCols, int kThreads, bool kVec>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(T);           // elements of a piece
   static constexpr int kRowPieces = kCols / kPer;
-  static constexpr int kPieces = kRows * kRowPieces / 256;
-  static_assert(kRows * kRowPieces % 256 == 0, "whole pieces per thread");
-  static_assert(256 % kRowPieces == 0, "a thread's pieces are in one column");
+  static constexpr int kPieces = kRows * kRowPieces / kThreads;
+  static_assert(kRows * kRowPieces % kThreads == 0, "whole pieces per thread");
+  static_assert(kThreads % kRowPieces == 0, "a thread's pieces are in one column");
   u32x4 r[kPieces];
 
   __device__ __forceinline__ void load(const T *base, int64_t stride, int rows, int d, int tid) {
@@ -224,11 +236,10 @@ struct Tile {
     const int c = tid % kRowPieces * kPer;
     const int row_bytes = static_cast<int>(stride * sizeof(T));
     // (past kNowhere the offsets stay, unsigned, behind every view)
-    unsigned off0 = c < d ? tid / kRowPieces * row_bytes + c * sizeof(T) : kNowhere;
-    asm volatile("" : "+v"(off0));  // one register from chunk to chunk, not one a piece
+    const unsigned off0 = c < d ? tid / kRowPieces * row_bytes + c * sizeof(T) : kNowhere;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int off = static_cast<int>(off0 + static_cast<unsigned>(i * (256 / kRowPieces)) * row_bytes);
+      const int off = static_cast<int>(off0 + static_cast<unsigned>(i * (kThreads / kRowPieces)) * row_bytes);
       if constexpr (kVec) {
         r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(v, off, 0, 0));
       } else {
@@ -255,7 +266,7 @@ struct Tile {
   __device__ __forceinline__ void store(typename Traits<T>::Elem *tile, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int q = tid + 256 * i, row = q / kRowPieces, c = (q % kRowPieces) * kPer;
+      const int q = tid + kThreads * i, row = q / kRowPieces, c = (q % kRowPieces) * kPer;
       *reinterpret_cast<u32x4 *>(tile + row * kStride + c) = r[i];
     }
   }
@@ -326,66 +337,76 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t v, int off, f32x4 
   }
 }
 
-// One workgroup: 4 waves, one segment of one head, kNJ * 64 output columns.
-// Wave w owns columns 16 kNJ w .. of the output and of the state, whose
-// kDK x 16 kNJ part stays in its accumulator registers from chunk to chunk
-// (the state tiles are the second operand of the next product as they
-// stand: the first operand is read with its columns in the order the
-// accumulators hold the rows).  The products are set up so that a lane
-// holds 4 neighbouring output columns of one token.  Per chunk: the tiles go
-// from registers (loaded during the chunk before) to LDS; the waves share
-// out the token pairs' products, each then takes all of them for its
-// columns.  bf16 roundings: the weighted pair products and the state where
-// it is an operand, once each (2^-8 of each term, as the output's own
-// rounding); what goes into the state enters as a pair of bf16 values
-// (2^-16), since the state is returned in 32 bits and is carried over the
-// sequence; likewise the state itself where dot products in 32 bits are
-// wanted (kLinOutDot).
-template <typename T, int kDK, int kNJ, int kMode, bool kRev, bool kVec>
-__global__ __launch_bounds__(256, 2) void linattn_core_kernel(LinCore p) {
+// One workgroup: kWaves waves, one segment of kHeads heads that share k (and
+// q), kCols output columns of each.  A wave owns 16 columns of the output and
+// of the state of one head, and that kDK x 16 part of the state stays in its
+// accumulator registers from chunk to chunk (the state tiles are the second
+// operand of the next product as they stand: the first operand is read with
+// its columns in the order the accumulators hold the rows).  The products are
+// set up so that a lane holds 4 neighbouring output columns of one token.
+// Per chunk: the tiles go from registers (loaded during the chunk before) to
+// LDS; the waves share out the token pairs' products, each then takes all of
+// them for its columns.
+//
+// bf16 roundings: the weighted pair products and the state where it is an
+// operand, once each (2^-8 of each term, as the output's own rounding); what
+// goes into the state enters as a pair of bf16 values (2^-16), since the
+// state is returned in 32 bits and is carried over the sequence; likewise
+// the state itself where dot products in 32 bits are wanted (kLinOutDot).
+// The sums of decays, at most 2^14 in size, are subtracted in 32 bits for
+// the weights of the pairs in bf16 (2^-10 at the largest sizes, a quarter of
+// the rounding the product then has), else in 64.
+template <typename T, int kDK, int kWaves, int kHeads, int kMode, bool kRev, bool kVec>
+__global__ __launch_bounds__(64 * kWaves, kDK > 128 ? 2 : 4) void linattn_core_kernel(LinCore p) {
   typedef Traits<T> Tr;
   typedef typename Tr::Frag Frag;
   typedef typename Tr::Elem Elem;
+  typedef typename Tr::Sum Sum;
   constexpr int C = Tr::kChunk, kNT = C / 16, kTS = C / 32;
-  constexpr int kKS = kDK / 32, kIT = kDK / 16, kDV = 64 * kNJ;
+  constexpr int kKS = kDK / 32, kIT = kDK / 16;
+  constexpr int kThreads = 64 * kWaves, kCols = 16 * kWaves / kHeads;
   constexpr bool kBf16 = Tr::kBf16;
   constexpr bool kOut = kMode != kLinState, kDot = kMode == kLinOutDot;
-  // row strides: rows 4 banks apart where rows are read side by side, 8
-  // where a read takes 4 rows of 8 banks at once (transposing reads)
+  // row strides: 8 banks apart for the transposing reads and those of 16
+  // bytes, 4 for those of 8 bytes (cycles a read, measured: 2 and 4, with the
+  // other stride 4 and 8)
   constexpr int kRowQ = kDK + (kBf16 ? 8 : 4), kRowK = kDK + (kBf16 ? 16 : 4);
-  constexpr int kRowV = kDV + (kBf16 ? 16 : 4), kRowP = C + (kBf16 ? 8 : 4);
+  constexpr int kRowV = kCols + (kBf16 ? 16 : 4), kRowP = C + (kBf16 ? 8 : 4);
   __shared__ __align__(16) Elem Qs[kOut ? C * kRowQ : 8];
   __shared__ __align__(16) Elem Ks[C * kRowK];
-  __shared__ __align__(16) Elem Vs[C * kRowV];
-  __shared__ __align__(16) Elem Ps[kOut ? C * kRowP : 8];
-  __shared__ double As[C];                       // sums of decays (log2)
-  __shared__ __align__(16) float Wo[C], Wi[C];   // weights out of, into the state
-  __shared__ float Wd[1];                        // the chunk's decay
-  __shared__ float Dots[kDot ? 4 * C : 1];
+  __shared__ __align__(16) Elem Vs[kHeads][C * kRowV];
+  __shared__ __align__(16) Elem Ps[kHeads][kOut ? C * kRowP : 8];
+  __shared__ Sum As[kHeads][C];                  // sums of decays (log2)
+  __shared__ __align__(16) float Wi[kHeads][C];  // weights into,
+  __shared__ float Wo[kHeads][C];                // out of the state
+  __shared__ float Wd[kHeads];                   // the chunk's decay
+  __shared__ float Dots[kDot ? kWaves * C : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int slices = (p.v.d + kDV - 1) / kDV;
-  const int slice = blockIdx.x % static_cast<unsigned>(slices);
-  const int h = blockIdx.x / static_cast<unsigned>(slices) % static_cast<unsigned>(p.plan.heads);
-  const int64_t slot = blockIdx.x / (static_cast<unsigned>(slices) * p.plan.heads);
+  const unsigned slices = (p.v.d + kCols - 1) / kCols;
+  const unsigned teams = static_cast<unsigned>(p.plan.heads) / kHeads;
+  const int slice = blockIdx.x % slices;
+  const int h0 = blockIdx.x / slices % teams * kHeads;
+  const int64_t slot = blockIdx.x / (slices * teams);
   const Segment sg = segment_of(p.plan, slot);
   if (!sg.real) return;
   const bool ends = kRev ? sg.seg == 0 : sg.last;  // nothing comes after it
   if (kMode == kLinState && ends) return;
 
-  const int j0 = slice * kDV;
+  const int mine = kHeads == 1 ? 0 : wave / (kWaves / kHeads);  // this wave's head
+  const int h = h0 + mine;
+  const int j0 = slice * kCols;
   const int dk = p.k.d, dv = p.v.d - j0;     // columns from this slice's first
   const int64_t n = sg.end - sg.begin;
   const int chunks = static_cast<int>((n + C - 1) / C);
-  const T *qh = static_cast<const T *>(p.q.p) + (h / p.q.div) * p.q.d;
-  const T *kh = static_cast<const T *>(p.k.p) + (h / p.k.div) * p.k.d;
-  const T *vh = static_cast<const T *>(p.v.p) + (h / p.v.div) * p.v.d + j0;
+  const T *qh = static_cast<const T *>(p.q.p) + (h0 / p.q.div) * p.q.d;
+  const T *kh = static_cast<const T *>(p.k.p) + (h0 / p.k.div) * p.k.d;
 
-  // the state: tile (it, nj), element e is S[16 it + 4 lq + e][jw + 16 nj + li]
-  const int jw = 16 * kNJ * wave;
-  f32x4 S[kIT][kNJ];
+  // the state: tile it, element e is S[16 it + 4 lq + e][jw + li]
+  const int jw = 16 * (kHeads == 1 ? wave : wave % (kWaves / kHeads));
+  f32x4 S[kIT];
   const int64_t size = static_cast<int64_t>(p.k.d) * p.v.d;
   const int64_t by_slot = (slot * p.plan.heads + h) * size;
   const int64_t by_seq = (static_cast<int64_t>(sg.seq) * p.plan.heads + h) * size;
@@ -393,74 +414,78 @@ __global__ __launch_bounds__(256, 2) void linattn_core_kernel(LinCore p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(at), 0,
                                              static_cast<int>(size * sizeof(float)), kBufferWord3);
   };
-  const int state0 = 4 * (4 * lq * p.sa + (j0 + jw + li) * p.sb);
-  auto state_off = [&](int it, int nj, int e) __attribute__((always_inline)) {
-    const int off = state0 + 4 * ((16 * it + e) * p.sa + 16 * nj * p.sb);
-    const bool in = 16 * it + 4 * lq + e < dk && jw + 16 * nj + li < dv;
+  // byte offset of an element of this lane's, from that of its first one
+  auto state_off = [&](int first_off, int it, int e) __attribute__((always_inline)) {
+    const int off = first_off + 4 * (16 * it + e) * p.sa;
+    const bool in = 16 * it + 4 * lq + e < dk && jw + li < dv;
     return in ? off : kNowhere;
   };
+  const int state0 = 4 * (4 * lq * p.sa + (j0 + jw + li) * p.sb);
   {
     const float *in = nullptr;
     if (kMode != kLinState)
       in = p.in_slots ? p.in_slots + by_slot : p.in_seqs ? p.in_seqs + by_seq : nullptr;
 #pragma unroll
-    for (int it = 0; it < kIT; ++it)
-#pragma unroll
-      for (int nj = 0; nj < kNJ; ++nj) S[it][nj] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int it = 0; it < kIT; ++it) S[it] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (in) {
       const __amdgpu_buffer_rsrc_t v = state_view(in);
 #pragma unroll
       for (int it = 0; it < kIT; ++it)
 #pragma unroll
-        for (int nj = 0; nj < kNJ; ++nj)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            S[it][nj][e] = __builtin_bit_cast(
-                float, __builtin_amdgcn_raw_buffer_load_b32(v, state_off(it, nj, e), 0, 0));
+        for (int e = 0; e < 4; ++e)
+          S[it][e] = __uint_as_float(
+              __builtin_amdgcn_raw_buffer_load_b32(v, state_off(state0, it, e), 0, 0));
     }
   }
   auto save = [&](float *out) __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t v = state_view(out);
+    const int at = anew(state0);
 #pragma unroll
     for (int it = 0; it < kIT; ++it)
 #pragma unroll
-      for (int nj = 0; nj < kNJ; ++nj)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[it][nj][e]), v,
-                                                state_off(it, nj, e), 0, 0);
+      for (int e = 0; e < 4; ++e)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[it][e]), v, state_off(at, it, e), 0, 0);
   };
   // the decay's gradient needs the state before a sequence's last chunk
   constexpr bool kBeforeLast = kDot && !kRev;
-  double total = 0.0;  // state pass: the segment's sum of decays (wave 0)
+  // the first wave of each head forms its weights
+  const bool weighs = kHeads == 1 ? wave == 0 : wave % (kWaves / kHeads) == 0;
+  double total = 0.0;  // state pass: the segment's sum of decays (those waves)
 
-  Tile<T, C, kDK, kVec> tq, tk;
-  Tile<T, C, kDV, kVec> tv;
+  Tile<T, C, kDK, kThreads, kVec> tq, tk;
+  Tile<T, C, kCols, kThreads, kVec> tv[kHeads];
   float gt = 0.0f;
   auto load = [&](int c) __attribute__((always_inline)) {
     const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
     const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
-    if (kOut) tq.load(qh + t0 * p.q.stride, p.q.stride, rows, p.q.d, tid);
-    tk.load(kh + t0 * p.k.stride, p.k.stride, rows, dk, tid);
-    tv.load(vh + t0 * p.v.stride, p.v.stride, rows, dv, tid);
+    const int me = anew(tid);
+    if (kOut) tq.load(qh + t0 * p.q.stride, p.q.stride, rows, p.q.d, me);
+    tk.load(kh + t0 * p.k.stride, p.k.stride, rows, dk, me);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const T *vh = static_cast<const T *>(p.v.p) + ((h0 + i) / p.v.div) * p.v.d + j0;
+      tv[i].load(vh + t0 * p.v.stride, p.v.stride, rows, dv, me);
+    }
     gt = 0.0f;
-    if (wave == 0 && lane < rows) gt = decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h);
+    if (weighs && lane < rows) gt = decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h);
   };
   auto stage = [&]() __attribute__((always_inline)) {
-    if (kOut) tq.template store<kRowQ>(Qs, tid);
-    tk.template store<kRowK>(Ks, tid);
-    tv.template store<kRowV>(Vs, tid);
-    if (wave == 0) {
+    const int me = anew(tid);
+    if (kOut) tq.template store<kRowQ>(Qs, me);
+    tk.template store<kRowK>(Ks, me);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) tv[i].template store<kRowV>(Vs[i], me);
+    if (weighs) {
       const double a = wave_sums<C>(lane < C ? log2_decay(gt) : 0.0, lane);
       const double end = __shfl(a, C - 1);
       const float from = fast_exp2(static_cast<float>(a));
       const float to = fast_exp2(static_cast<float>(end - a));
       if (lane < C) {
-        As[lane] = a;
-        Wo[lane] = (kRev ? to : from) * p.inter;
-        Wi[lane] = (kRev ? from : to) * p.into;
+        As[mine][lane] = static_cast<Sum>(a);
+        Wo[mine][lane] = (kRev ? to : from) * p.inter;
+        Wi[mine][lane] = (kRev ? from : to) * p.into;
       }
-      if (lane == 0) Wd[0] = fast_exp2(static_cast<float>(end));
+      if (lane == 0) Wd[mine] = fast_exp2(static_cast<float>(end));
       if (kMode == kLinState) total += end;
     }
   };
@@ -475,103 +500,97 @@ __global__ __launch_bounds__(256, 2) void linattn_core_kernel(LinCore p) {
     const bool more = i + 1 < chunks;
     __syncthreads();  // the chunk is staged
     if (more) load(c + step);
-    Four<T, kVec> xr[kDot ? kNT : 1][kNJ];  // x's rows where this lane has outputs
+    Four<T, kVec> xr[kDot ? kNT : 1];  // x's rows where this lane has outputs
     if constexpr (kDot) {
       const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
       const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
+      const int lane = anew(tid) & 63, li = lane & 15, lq = lane >> 4;
       const T *xh = static_cast<const T *>(p.x.p) + t0 * p.x.stride + (h / p.x.div) * p.x.d + j0;
       const __amdgpu_buffer_rsrc_t v = rows_view(xh, p.x.stride, rows, dv);
       const int b = jw + 4 * lq, row = static_cast<int>(p.x.stride * sizeof(T));
-      int off = li * row + b * static_cast<int>(sizeof(T));
-      asm volatile("" : "+v"(off));
+      const int off = li * row + b * static_cast<int>(sizeof(T));
 #pragma unroll
-      for (int ti = 0; ti < kNT; ++ti)
-#pragma unroll
-        for (int nj = 0; nj < kNJ; ++nj)
-          xr[ti][nj].load(v, off + 16 * ti * row + 16 * nj * static_cast<int>(sizeof(T)),
-                          dv - b - 16 * nj);
+      for (int ti = 0; ti < kNT; ++ti) xr[ti].load(v, off + 16 * ti * row, dv - b);
     }
 
+    __builtin_amdgcn_sched_barrier(0);
     if (kOut) {
-      // token pairs: wave w takes the tokens t of tile w (32-bit chunks have
-      // 2 tiles: two waves a tile, each half of the s)
-      constexpr int kSub = kNT == 4 ? 4 : 1;
-      const int ti = kNT == 4 ? wave : wave >> 1;
-      const int s0 = kNT == 4 ? 0 : wave & 1;
-      const double at = As[16 * ti + li];
-      f32x4 acc[kSub];
+      // token pairs: kNT x kNT tiles of 16 x 16, kSub tiles a wave of one t
+      constexpr int kTiles = kNT * kNT, kBusy = kTiles < kWaves ? kTiles : kWaves;
+      constexpr int kSub = kTiles / kBusy, kPer = kNT / kSub;  // waves per tile row
+      const int ti = wave / kPer, s0 = wave % kPer * kSub;
+      const int lane = anew(tid) & 63, li = lane & 15, lq = lane >> 4;
+      if (kBusy == kWaves || wave < kBusy) {
+        f32x4 acc[kSub];
 #pragma unroll
-      for (int si = 0; si < kSub; ++si) acc[si] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int si = 0; si < kSub; ++si) acc[si] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        const Frag b = *reinterpret_cast<const Frag *>(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 8 * lq]);
+        for (int ks = 0; ks < kKS; ++ks) {
+          const Frag b = *reinterpret_cast<const Frag *>(
+              &Qs[(16 * ti + li) * kRowQ + 32 * ks + 8 * lq]);
 #pragma unroll
-        for (int si = 0; si < kSub; ++si) {
-          const Frag a = *reinterpret_cast<const Frag *>(
-              &Ks[(16 * (s0 + si) + li) * kRowK + 32 * ks + 8 * lq]);
-          acc[si] = mma(a, b, acc[si]);
+          for (int si = 0; si < kSub; ++si) {
+            const Frag a = *reinterpret_cast<const Frag *>(
+                &Ks[(16 * (s0 + si) + li) * kRowK + 32 * ks + 8 * lq]);
+            acc[si] = mma(a, b, acc[si]);
+          }
         }
-      }
+        const int t = 16 * ti + li;
 #pragma unroll
-      for (int si = 0; si < kSub; ++si) {
+        for (int hd = 0; hd < kHeads; ++hd) {
+          const Sum at = As[hd][t];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int s = 16 * (s0 + si) + 4 * lq + e, t = 16 * ti + li;
-          const double as = As[s];
-          float w = fast_exp2(static_cast<float>(kRev ? as - at : at - as));
-          asm volatile("" : "+v"(w));  // all lanes compute it: no branch for it
-          acc[si][e] = (kRev ? s >= t : s <= t) ? acc[si][e] * w * p.inside : 0.0f;
-        }
-        Elem *d = &Ps[(16 * ti + li) * kRowP + 16 * (s0 + si) + 4 * lq];
-        if constexpr (kBf16)
-          *reinterpret_cast<bf16x4 *>(d) = __builtin_convertvector(acc[si], bf16x4);
-        else
-          *reinterpret_cast<f32x4 *>(d) = acc[si];
-      }
-    }
-
-    f32x4 O[kNT][kNJ];
-    if (kOut) {
+          for (int si = 0; si < kSub; ++si) {
+            const int s = 16 * (s0 + si) + 4 * lq;
+            f32x4 x;
 #pragma unroll
-      for (int ti = 0; ti < kNT; ++ti)
-#pragma unroll
-        for (int nj = 0; nj < kNJ; ++nj) O[ti][nj] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // the state's part
-#pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        Frag hi[kNJ], lo[kNJ];
-#pragma unroll
-        for (int nj = 0; nj < kNJ; ++nj) {
-          const f32x8 s = __builtin_shufflevector(S[2 * ks][nj], S[2 * ks + 1][nj], 0, 1, 2, 3, 4, 5, 6, 7);
-          hi[nj] = to_frag(s, Frag{});
-          if constexpr (kDot && kBf16)
-            lo[nj] = to_frag(s - __builtin_convertvector(hi[nj], f32x8), Frag{});
-        }
-#pragma unroll
-        for (int ti = 0; ti < kNT; ++ti) {
-          const Frag b = two_halves(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 4 * lq]);
-#pragma unroll
-          for (int nj = 0; nj < kNJ; ++nj) {
-            O[ti][nj] = mma(hi[nj], b, O[ti][nj]);
-            if constexpr (kDot && kBf16) O[ti][nj] = mma(lo[nj], b, O[ti][nj]);
+            for (int e = 0; e < 4; ++e) {
+              const Sum as = As[hd][s + e];
+              float w = fast_exp2(static_cast<float>(kRev ? as - at : at - as));
+              asm volatile("" : "+v"(w));  // all lanes compute it: no branch for it
+              x[e] = (kRev ? s + e >= t : s + e <= t) ? acc[si][e] * w * p.inside : 0.0f;
+            }
+            Elem *d = &Ps[hd][t * kRowP + s];
+            if constexpr (kBf16)
+              *reinterpret_cast<bf16x4 *>(d) = __builtin_convertvector(x, bf16x4);
+            else
+              *reinterpret_cast<f32x4 *>(d) = x;
           }
         }
       }
+    }
+
+    __builtin_amdgcn_sched_barrier(0);  // phases apart: their operands share registers
+    f32x4 O[kNT];
+    if (kOut) {
 #pragma unroll
-      for (int ti = 0; ti < kNT; ++ti) {
-        const float w = Wo[16 * ti + li];
+      for (int ti = 0; ti < kNT; ++ti) O[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // the state's part
+      const int lane = anew(tid) & 63, li = lane & 15, lq = lane >> 4;
 #pragma unroll
-        for (int nj = 0; nj < kNJ; ++nj) O[ti][nj] *= w;
+      for (int ks = 0; ks < kKS; ++ks) {
+        __builtin_amdgcn_sched_barrier(0);
+        const f32x8 s = __builtin_shufflevector(S[2 * ks], S[2 * ks + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const Frag hi = to_frag(s, Frag{});
+        Frag lo;
+        if constexpr (kDot && kBf16)
+          lo = to_frag(s - __builtin_convertvector(hi, f32x8), Frag{});
+#pragma unroll
+        for (int ti = 0; ti < kNT; ++ti) {
+          const Frag b = two_halves(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 4 * lq]);
+          O[ti] = mma(hi, b, O[ti]);
+          if constexpr (kDot && kBf16) O[ti] = mma(lo, b, O[ti]);
+        }
       }
+#pragma unroll
+      for (int ti = 0; ti < kNT; ++ti) O[ti] *= Wo[mine][16 * ti + li];
       if constexpr (kDot) {
         // dot products of the state's part with x's rows, this wave's columns
 #pragma unroll
         for (int ti = 0; ti < kNT; ++ti) {
           float d = 0.0f;
 #pragma unroll
-          for (int nj = 0; nj < kNJ; ++nj)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d = fmaf(O[ti][nj][e], xr[ti][nj][e], d);
+          for (int e = 0; e < 4; ++e) d = fmaf(O[ti][e], xr[ti][e], d);
           d += __shfl_xor(d, 16);
           d += __shfl_xor(d, 32);
           if (lq == 0) Dots[wave * C + 16 * ti + li] = d;
@@ -581,46 +600,42 @@ __global__ __launch_bounds__(256, 2) void linattn_core_kernel(LinCore p) {
 
     if (kBeforeLast && !more && ends && p.out_seqs) save(p.out_seqs + by_seq);
 
+    __builtin_amdgcn_sched_barrier(0);
     // into the state
-    const float wd = Wd[0];
+    const float wd = Wd[mine];
+    const int fresh = anew(tid) & 63;
 #pragma unroll
-    for (int it = 0; it < kIT; ++it)
-#pragma unroll
-      for (int nj = 0; nj < kNJ; ++nj) S[it][nj] *= wd;
-    Frag vf[kTS][kNJ];
+    for (int it = 0; it < kIT; ++it) S[it] *= wd;
+    Frag vf[kTS];
 #pragma unroll
     for (int ts = 0; ts < kTS; ++ts) {
-      const f32x8 w = *reinterpret_cast<const f32x8 *>(&Wi[32 * ts + 8 * lq]);
-      Frag hi[kNJ], lo[kNJ];
-#pragma unroll
-      for (int nj = 0; nj < kNJ; ++nj) {
-        vf[ts][nj] = frag_by_column<kRowV>(Vs, 32 * ts, jw + 16 * nj, lane);
-        const f32x8 x = __builtin_convertvector(vf[ts][nj], f32x8) * w;
-        hi[nj] = to_frag(x, Frag{});
-        if constexpr (kBf16) lo[nj] = to_frag(x - __builtin_convertvector(hi[nj], f32x8), Frag{});
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      const f32x8 w = two_halves(&Wi[mine][32 * ts + 4 * (fresh >> 4)]);
+      vf[ts] = frag_by_column<kRowV>(Vs[mine], 32 * ts, jw, fresh);
+      const f32x8 x = __builtin_convertvector(vf[ts], f32x8) * w;
+      const Frag hi = to_frag(x, Frag{});
+      Frag lo;
+      if constexpr (kBf16) lo = to_frag(x - __builtin_convertvector(hi, f32x8), Frag{});
 #pragma unroll
       for (int it = 0; it < kIT; ++it) {
-        const Frag a = frag_by_column<kRowK>(Ks, 32 * ts, 16 * it, lane);
-#pragma unroll
-        for (int nj = 0; nj < kNJ; ++nj) {
-          S[it][nj] = mma(a, hi[nj], S[it][nj]);
-          if constexpr (kBf16) S[it][nj] = mma(a, lo[nj], S[it][nj]);
-        }
+        if (it % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+        const Frag a = frag_by_column<kRowK>(Ks, 32 * ts, 16 * it, fresh);
+        S[it] = mma(a, hi, S[it]);
+        if constexpr (kBf16) S[it] = mma(a, lo, S[it]);
       }
     }
 
     __syncthreads();  // the pairs' products are in LDS; all else there is read
     if (more) stage();
     if (kOut) {
+      const int lane = anew(tid) & 63, li = lane & 15, lq = lane >> 4;
 #pragma unroll
       for (int ti = 0; ti < kNT; ++ti)
 #pragma unroll
         for (int ts = 0; ts < kTS; ++ts) {
           if (kRev ? 2 * ts + 1 < ti : 2 * ts > ti) continue;  // no pair left
-          const Frag b = *reinterpret_cast<const Frag *>(&Ps[(16 * ti + li) * kRowP + 32 * ts + 8 * lq]);
-#pragma unroll
-          for (int nj = 0; nj < kNJ; ++nj) O[ti][nj] = mma(vf[ts][nj], b, O[ti][nj]);
+          const Frag b = two_halves(&Ps[mine][(16 * ti + li) * kRowP + 32 * ts + 4 * lq]);
+          O[ti] = mma(vf[ts], b, O[ti]);
         }
       const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
       const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
@@ -631,23 +646,22 @@ __global__ __launch_bounds__(256, 2) void linattn_core_kernel(LinCore p) {
         constexpr int kSize = sizeof(E);
         const __amdgpu_buffer_rsrc_t v = rows_view(out + at, out_stride, rows, dv);
         const int b = jw + 4 * lq, row = static_cast<int>(out_stride) * kSize;
-        int off = li * row + b * kSize;
-        asm volatile("" : "+v"(off));
+        const int off = li * row + b * kSize;
 #pragma unroll
         for (int ti = 0; ti < kNT; ++ti)
-#pragma unroll
-          for (int nj = 0; nj < kNJ; ++nj)
-            store4<kVec>(v, off + 16 * ti * row + 16 * nj * kSize, O[ti][nj], dv - b - 16 * nj,
-                         E(0));
+          store4<kVec>(v, off + 16 * ti * row, O[ti], dv - b, E(0));
       };
       if (p.out_f32)
         write(static_cast<float *>(p.out));
       else
         write(static_cast<T *>(p.out));
       if constexpr (kDot) {
-        if (tid < C && t0 + tid < sg.end)
-          p.dots[(slice * p.plan.tokens + t0 + tid) * p.plan.heads + h] =
-              Dots[tid] + Dots[C + tid] + Dots[2 * C + tid] + Dots[3 * C + tid];
+        if (tid < C && t0 + tid < sg.end) {
+          float d = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) d += Dots[w * C + tid];
+          p.dots[(slice * p.plan.tokens + t0 + tid) * p.plan.heads + h] = d;
+        }
       }
     }
   }
@@ -656,33 +670,55 @@ __global__ __launch_bounds__(256, 2) void linattn_core_kernel(LinCore p) {
     save(p.out_slots + by_slot);
   else if (!kBeforeLast && p.out_seqs && ends)
     save(p.out_seqs + by_seq);
-  if (kMode == kLinState && tid == 0 && slice == 0)
+  if (kMode == kLinState && weighs && lane == 0 && slice == 0)
     p.out_decay[slot * p.plan.heads + h] = fast_exp2(static_cast<float>(total));
 }
 
-template <typename T, int kDK, int kNJ, int kMode, bool kRev>
+template <typename T, int kDK, int kWaves, int kHeads, int kMode, bool kRev>
 int launch_core_t(const LinCore &a, hipStream_t s) {
-  const int64_t slices = (a.v.d + 64 * kNJ - 1) / (64 * kNJ);
-  const dim3 grid(static_cast<unsigned>(a.plan.slots * a.plan.heads * slices));
+  constexpr int kCols = 16 * kWaves / kHeads;
+  const int64_t slices = (a.v.d + kCols - 1) / kCols;
+  const dim3 grid(static_cast<unsigned>(a.plan.slots * (a.plan.heads / kHeads) * slices));
   if (a.plan.vec)
-    hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kNJ, kMode, kRev, true>), grid, dim3(256), 0, s,
-                       a);
+    hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kWaves, kHeads, kMode, kRev, true>), grid,
+                       dim3(64 * kWaves), 0, s, a);
   else
-    hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kNJ, kMode, kRev, false>), grid, dim3(256), 0,
-                       s, a);
+    hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kWaves, kHeads, kMode, kRev, false>), grid,
+                       dim3(64 * kWaves), 0, s, a);
   return static_cast<int>(hipGetLastError());
 }
 
-template <typename T, int kDK, int kNJ>
+// kHeads = 2 has no kLinOutDot: there the first two operands are those of one
+// value head.
+template <typename T, int kDK, int kWaves, int kHeads>
 int launch_core_m(const LinCore &a, int mode, bool reverse, hipStream_t s) {
   if (mode == kLinState)
-    return reverse ? launch_core_t<T, kDK, kNJ, kLinState, true>(a, s)
-                   : launch_core_t<T, kDK, kNJ, kLinState, false>(a, s);
-  if (mode == kLinOut)
-    return reverse ? launch_core_t<T, kDK, kNJ, kLinOut, true>(a, s)
-                   : launch_core_t<T, kDK, kNJ, kLinOut, false>(a, s);
-  return reverse ? launch_core_t<T, kDK, kNJ, kLinOutDot, true>(a, s)
-                 : launch_core_t<T, kDK, kNJ, kLinOutDot, false>(a, s);
+    return reverse ? launch_core_t<T, kDK, kWaves, kHeads, kLinState, true>(a, s)
+                   : launch_core_t<T, kDK, kWaves, kHeads, kLinState, false>(a, s);
+  if constexpr (kHeads == 1)
+    if (mode == kLinOutDot)
+      return reverse ? launch_core_t<T, kDK, kWaves, kHeads, kLinOutDot, true>(a, s)
+                     : launch_core_t<T, kDK, kWaves, kHeads, kLinOutDot, false>(a, s);
+  return reverse ? launch_core_t<T, kDK, kWaves, kHeads, kLinOut, true>(a, s)
+                 : launch_core_t<T, kDK, kWaves, kHeads, kLinOut, false>(a, s);
+}
+
+// Workgroups: 8 waves on 128 columns of a head; where heads have at most 64,
+// on two heads that share the first two operands (which are then read, and
+// multiplied, once for both); else 4 waves on 64 columns.
+template <typename T, int kDK>
+int launch_core_k(const LinCore &a, int mode, bool reverse, hipStream_t s) {
+  if (a.v.d > 64) return launch_core_m<T, kDK, 8, 1>(a, mode, reverse, s);
+  if (linattn_pairs_heads(a, mode)) return launch_core_m<T, kDK, 8, 2>(a, mode, reverse, s);
+  return launch_core_m<T, kDK, 4, 1>(a, mode, reverse, s);
+}
+
+template <typename T>
+int launch_core(const LinCore &a, int mode, bool reverse, void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a.k.d <= 64) return launch_core_k<T, 64>(a, mode, reverse, s);
+  if (a.k.d <= 128) return launch_core_k<T, 128>(a, mode, reverse, s);
+  return launch_core_k<T, 256>(a, mode, reverse, s);
 }
 
 }  // namespace lin

@@ -4,10 +4,7 @@
 namespace ssm {
 
 int launch_linattn_core_f32(const LinCore &a, int mode, bool reverse, void *stream) {
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a.k.d <= 64) return lin::launch_core_m<float, 64, 1>(a, mode, reverse, s);
-  if (a.k.d <= 128) return lin::launch_core_m<float, 128, 1>(a, mode, reverse, s);
-  return lin::launch_core_m<float, 256, 1>(a, mode, reverse, s);
+  return lin::launch_core<float>(a, mode, reverse, stream);
 }
 
 }  // namespace ssm

@@ -110,7 +110,9 @@ struct LinStep {
 
 // tokens of a chunk, output columns of one workgroup
 int linattn_chunk(bool bf16);
-int linattn_slice(bool bf16, int dk, int dv);
+int linattn_slice(int dv);
+// whether one workgroup takes two value heads
+bool linattn_pairs_heads(const LinCore &a, int mode);
 int launch_linattn_core(const LinCore &a, int mode, bool reverse, bool bf16, void *stream);
 int launch_linattn_core_bf16(const LinCore &a, int mode, bool reverse, void *stream);
 int launch_linattn_core_f32(const LinCore &a, int mode, bool reverse, void *stream);
