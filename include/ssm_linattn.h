@@ -47,21 +47,22 @@ extern "C" {
 /* g holds one log decay a head, for every token: (heads) */
 #define SSM_FLAG_HEAD_DECAY 8u
 
-/* How ssm_linattn_fwd (backward = 0) or ssm_linattn_bwd (backward = 1) cuts
- * the sequences, in plan_out[4] (no HIP call):
+/* How ssm_linattn_fwd (backward = 0) or ssm_linattn_bwd (backward = 1, or 2
+ * with dg) cuts the sequences, in plan_out[4] (no HIP call):
  *  [0] tokens per segment: segments are taken in parallel, each from the
  *      state that a pass over the segments before it formed
  *  [1] segments (an upper bound with cu_seqlens)
  *  [2] tokens per chunk of the matrix products
  *  [3] 1 if that pass is made, 0 if every sequence is one segment
  * packed: nonzero with cu_seqlens. */
-int ssm_linattn_plan(int64_t tokens, int64_t nseq, int packed, int64_t heads, int64_t qk_dim,
-                     int64_t v_dim, int dtype, int backward, int64_t *plan_out);
+int ssm_linattn_plan(int64_t tokens, int64_t nseq, int packed, int64_t heads, int64_t qk_heads,
+                     int64_t qk_dim, int64_t v_dim, int dtype, int backward, int64_t *plan_out);
 
 /* Bytes of device workspace for ssm_linattn_fwd (0 where every sequence is
  * one segment). */
 int ssm_linattn_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t heads,
-                               int64_t qk_dim, int64_t v_dim, int dtype, size_t *bytes);
+                               int64_t qk_heads, int64_t qk_dim, int64_t v_dim, int dtype,
+                               size_t *bytes);
 
 /* Linear attention over whole sequences (prompts, training).
  *  q, k, v     required, activation dtype; may overlap each other

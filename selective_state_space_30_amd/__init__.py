@@ -161,11 +161,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.ssm_roofline_valu.restype = I
         SZ, F = ctypes.c_size_t, ctypes.c_float
         side = [P, I64]
-        lib.ssm_linattn_plan.argtypes = [I64, I64, I, I64, I64, I64, I, I,
+        lib.ssm_linattn_plan.argtypes = [I64, I64, I, I64, I64, I64, I64, I, I,
                                          ctypes.POINTER(I64)]
         lib.ssm_linattn_plan.restype = I
         lib.ssm_linattn_workspace_size.argtypes = [I64, I64, I, I64, I64, I64,
-                                                   I, ctypes.POINTER(SZ)]
+                                                   I64, I, ctypes.POINTER(SZ)]
         lib.ssm_linattn_workspace_size.restype = I
         lib.ssm_linattn_fwd.argtypes = (side * 3 + [P, U, F, P, P, P, P] +
                                         [I64] * 6 + [I, P, SZ, P])
@@ -853,23 +853,24 @@ def _code(dtype):
     raise TypeError("activations must be float32 or bfloat16, got %s" % dtype)
 
 
-def ssm_linattn_plan(tokens, nseq, heads, qk_dim, v_dim, dtype=torch.bfloat16,
-                     packed=False, backward=False) -> dict:
-    """How :func:`ssm_linattn_fwd` (or the backward) cuts the sequences:
-    tokens per segment, segments, tokens per chunk, and whether a pass over
-    k and v forms the states between segments."""
+def ssm_linattn_plan(tokens, nseq, heads, qk_heads, qk_dim, v_dim,
+                     dtype=torch.bfloat16, packed=False, backward=0) -> dict:
+    """How :func:`ssm_linattn_fwd` (``backward``: 1, or 2 with dg, for
+    :func:`ssm_linattn_bwd`) cuts the sequences: tokens per segment, segments,
+    tokens per chunk, and whether a pass over the tokens forms the states
+    between segments."""
     out = (ctypes.c_int64 * 4)()
-    _check(load_library().ssm_linattn_plan(tokens, nseq, int(packed), heads,
+    _check(load_library().ssm_linattn_plan(tokens, nseq, int(packed), heads, qk_heads,
                                            qk_dim, v_dim, _code(dtype),
                                            int(backward), out))
     return {"segment": out[0], "segments": out[1], "chunk": out[2],
             "state_pass": bool(out[3])}
 
 
-def ssm_linattn_workspace_size(tokens, nseq, heads, qk_dim, v_dim,
+def ssm_linattn_workspace_size(tokens, nseq, heads, qk_heads, qk_dim, v_dim,
                                dtype=torch.bfloat16, packed=False) -> int:
     return _size(load_library().ssm_linattn_workspace_size, tokens, nseq,
-                 int(packed), heads, qk_dim, v_dim, _code(dtype))
+                 int(packed), heads, qk_heads, qk_dim, v_dim, _code(dtype))
 
 
 def ssm_linattn_bwd_workspace_size(tokens, nseq, heads, qk_heads, qk_dim, v_dim,
@@ -949,7 +950,7 @@ def ssm_linattn_fwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     elif h_final is None:
         h_final = torch.empty(a.states, dtype=torch.float32, device=a.dev)
     need = _size(lib.ssm_linattn_workspace_size, a.tokens, a.nseq, a.cu is not None,
-                 a.heads, a.dk, a.dv, a.code)
+                 a.heads, a.qk_heads, a.dk, a.dv, a.code)
     keep, ws, ws_bytes = _scratch(workspace, need, a.dev)
     _check(lib.ssm_linattn_fwd(
         *a.qkv, a.g, a.flags, a.scale, a.h0, a.cu,

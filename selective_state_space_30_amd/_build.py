@@ -46,7 +46,9 @@ def _run(cmd):
 
 HIP_SOURCES = ["ssm_kernels.hip", "ssm_step.hip", "ssm_bwd.hip", "ssm_ssd.hip",
                "ssm_roofline.hip", "ssm_conv_bwd.hip", "ssm_linattn.hip",
-               "ssm_linattn_bf16.hip", "ssm_linattn_f32.hip", "ssm_block_norm.hip"]
+               "ssm_linattn_out_bf16.hip", "ssm_linattn_out_f32.hip",
+               "ssm_linattn_grads_bf16.hip", "ssm_linattn_grads_f32.hip",
+               "ssm_block_norm.hip"]
 CPP_SOURCES = ["ssm_api.cpp", "ssm_linattn_api.cpp"]
 
 

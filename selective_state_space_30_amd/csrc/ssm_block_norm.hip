@@ -383,25 +383,31 @@ __global__ __launch_bounds__(kBound) void norm_bwd_kernel(NormArgs p) {
   }
 }
 
-// Sum of the workgroups' partial rows, 32 columns and 8 row groups a
+// Sum of the workgroups' partial rows, 32 columns and 32 row groups a
 // workgroup, in a fixed order.
-__global__ __launch_bounds__(256) void norm_parts_kernel(NormArgs p) {
-  __shared__ float Sums[8][33];
+__global__ __launch_bounds__(1024) void norm_parts_kernel(NormArgs p) {
+  __shared__ float Sums[32][33];
   const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
   const int which = blockIdx.y;
   float *out = which == 0 ? p.dw_post : which == 1 ? p.dscale : p.dw_pre;
   if (!out) return;
   const int c = blockIdx.x * 32 + lane;
-  float acc = 0.0f;
-  if (c < p.dim)
-    for (int w = grp; w < p.nparts; w += 8)
-      acc += p.parts[(static_cast<int64_t>(w) * 3 + which) * p.dim + c];
-  Sums[grp][lane] = acc;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < p.dim) {
+    const float *s = p.parts + static_cast<int64_t>(which) * p.dim + c;
+    const int64_t row = 3 * static_cast<int64_t>(p.dim);
+    int w = grp;
+    for (; w + 96 < p.nparts; w += 128)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] += s[(w + 32 * k) * row];
+    for (; w < p.nparts; w += 32) acc[0] += s[w * row];
+  }
+  Sums[grp][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
   __syncthreads();
   if (grp == 0 && c < p.dim) {
     float s = 0.0f;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) s += Sums[g][lane];
+    for (int g = 0; g < 32; ++g) s += Sums[g][lane];
     out[c] = s;
   }
 }
@@ -491,7 +497,7 @@ int launch_block_norm_bwd(const NormArgs &a, bool bf16, void *stream) {
   const int err = a.rows > 0 ? launch_norm(a, true, bf16, s) : 0;
   if (err != 0 || (!a.dw_post && !a.dscale && !a.dw_pre)) return err;
   hipLaunchKernelGGL(norm_parts_kernel, dim3(static_cast<unsigned>((a.dim + 31) / 32), 3),
-                     dim3(256), 0, s, a);
+                     dim3(1024), 0, s, a);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -15,7 +15,8 @@ using namespace lin;
 // paid once for all of them.
 constexpr int kAhead = 8;
 
-__global__ __launch_bounds__(256) void linattn_chain_kernel(LinChain p) {
+__global__ __launch_bounds__(256) void linattn_chain_kernel(LinChain a, LinChain other) {
+  const LinChain &p = blockIdx.z ? other : a;
   const int h = blockIdx.x % static_cast<unsigned>(p.plan.heads);
   const int seq = blockIdx.x / static_cast<unsigned>(p.plan.heads);
   int64_t b, e;
@@ -62,100 +63,146 @@ __global__ __launch_bounds__(256) void linattn_chain_kernel(LinChain p) {
 // before t.
 
 // Pairs inside each chunk: out_t = sum_{s<t} W_ts - sum_{r>t} W_rt.  One
-// workgroup per (chunk, head), wave w takes the rows of token tile w;
-// operands come from memory straight into fragments.
-template <typename T>
-__global__ __launch_bounds__(256) void linattn_pairs_kernel(LinPairs p) {
+// workgroup per (chunk, head); a wave takes 16 tokens t and half of the tokens
+// s (bf16) or all (fp32).  Operands come from memory straight into fragments,
+// 128 columns of all of them at once (latency bounds it: every row is read
+// by few waves and used in 8 products).
+template <typename T, bool kVec>
+__device__ __forceinline__ typename Traits<T>::Frag view_frag(__amdgpu_buffer_rsrc_t v, int off,
+                                                              int left) {
+  typedef typename Traits<T>::Frag Frag;
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (kVec) {
+      return __builtin_bit_cast(
+          Frag, __builtin_amdgcn_raw_buffer_load_b128(v, left > 0 ? off : kNowhere, 0, 0));
+    } else {
+      typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+      u16x8 x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = __builtin_amdgcn_raw_buffer_load_b16(v, e < left ? off + 2 * e : kNowhere, 0, 0);
+      return __builtin_bit_cast(Frag, x);
+    }
+  } else {
+    Frag f;
+    if constexpr (kVec) {
+      const f32x4 a = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, left > 0 ? off : kNowhere, 0, 0));
+      const f32x4 b = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, left > 4 ? off + 16 : kNowhere, 0, 0));
+      f = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        f[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            v, e < left ? off + 4 * e : kNowhere, 0, 0));
+    }
+    return f;
+  }
+}
+
+template <typename T, bool kVec>
+__global__ __launch_bounds__(512) void linattn_pairs_kernel(LinPairs p) {
   typedef Traits<T> Tr;
   typedef typename Tr::Frag Frag;
   constexpr int C = Tr::kChunk, kNT = C / 16;
+  constexpr int kSub = Tr::kBf16 ? 2 : 1, kPer = kNT / kSub;  // tiles a wave, waves a tile row
+  constexpr int kKS = 4;                                      // steps of 32 columns in flight
   __shared__ double As[C];
-  __shared__ float Cols[4][C];
-  __shared__ float Rows[C];
+  __shared__ float Cols[kNT][C];
+  __shared__ float Rows[kPer][C];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int h = blockIdx.x % p.plan.heads;
-  const int64_t per_seg = p.plan.seg_len / C;
-  const int64_t cs = blockIdx.x / p.plan.heads;
+  const int h = blockIdx.x % static_cast<unsigned>(p.plan.heads);
+  const unsigned per_seg = static_cast<unsigned>(p.plan.seg_len) / C;
+  const unsigned cs = blockIdx.x / static_cast<unsigned>(p.plan.heads);
   const Segment sg = segment_of(p.plan, cs / per_seg);
-  const int64_t t0 = sg.begin + (cs % per_seg) * C;
+  const int64_t t0 = sg.begin + static_cast<int64_t>(cs % per_seg) * C;
   if (!sg.real || t0 >= sg.end) return;
   const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
+  const int ti = wave / kPer, s0 = wave % kPer * kSub;
+  const bool some = s0 <= ti;  // else every pair of this wave's is empty
+  f32x4 w[kSub];
+#pragma unroll
+  for (int si = 0; si < kSub; ++si) w[si] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (some) {
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const LinSide &xr = part ? p.o : p.q, &xc = part ? p.v : p.k;
+      const __amdgpu_buffer_rsrc_t vr = rows_view(
+          static_cast<const T *>(xr.p) + t0 * xr.stride + (h / xr.div) * xr.d, xr.stride, rows, xr.d);
+      const __amdgpu_buffer_rsrc_t vc = rows_view(
+          static_cast<const T *>(xc.p) + t0 * xc.stride + (h / xc.div) * xc.d, xc.stride, rows, xc.d);
+      f32x4 acc[kSub];
+#pragma unroll
+      for (int si = 0; si < kSub; ++si) acc[si] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int c0 = 0; c0 < xr.d; c0 += 32 * kKS) {
+        Frag b[kKS], a[kKS][kSub];
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks) {
+          const int c = c0 + 32 * ks + 8 * lq;
+          b[ks] = view_frag<T, kVec>(
+              vr, static_cast<int>(((16 * ti + li) * xr.stride + c) * sizeof(T)), xr.d - c);
+#pragma unroll
+          for (int si = 0; si < kSub; ++si)
+            a[ks][si] = view_frag<T, kVec>(
+                vc, static_cast<int>(((16 * (s0 + si) + li) * xc.stride + c) * sizeof(T)),
+                xc.d - c);
+        }
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+          for (int si = 0; si < kSub; ++si) acc[si] = mma(a[ks][si], b[ks], acc[si]);
+      }
+#pragma unroll
+      for (int si = 0; si < kSub; ++si) w[si] = part ? w[si] * acc[si] : acc[si];
+    }
+  }
   if (wave == 0) {
     const float g = lane < rows ? decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h) : 0.0f;
     const double a = wave_sums<C>(lane < C ? log2_decay(g) : 0.0, lane);
     if (lane < C) As[lane] = a;
   }
-  auto frag = [&](const LinSide &x, int row, int c) __attribute__((always_inline)) {
-    const T *s = static_cast<const T *>(x.p) + (t0 + row) * x.stride + (h / x.div) * x.d + c;
-    Frag f;
-    if (row < rows && p.plan.vec && c + 8 <= x.d) {
-      __builtin_memcpy(&f, s, sizeof(f));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        f[e] = row < rows && c + e < x.d
-                   ? __builtin_bit_cast(typename Tr::Elem, s[e])
-                   : static_cast<typename Tr::Elem>(0.0f);
-    }
-    return f;
-  };
   __syncthreads();
-  const int ti = wave;
+  // lane: token t = 16 ti + li against s = 16 (s0 + si) + 4 lq + e
+  const int t = 16 * ti + li;
+  const double at = As[t];
   float row_sum = 0.0f;
-  if (ti < kNT) {
-    f32x4 w[kNT];
-    for (int part = 0; part < 2; ++part) {
-      const LinSide &xr = part ? p.o : p.q, &xc = part ? p.v : p.k;
-      f32x4 acc[kNT];
 #pragma unroll
-      for (int si = 0; si < kNT; ++si) acc[si] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int c = 8 * lq; c - 8 * lq < xr.d; c += 32) {
-        const Frag b = frag(xr, 16 * ti + li, c);
+  for (int si = 0; si < kSub; ++si) {
 #pragma unroll
-        for (int si = 0; si < kNT; ++si)
-          if (si <= ti) acc[si] = mma(frag(xc, 16 * si + li, c), b, acc[si]);
-      }
-#pragma unroll
-      for (int si = 0; si < kNT; ++si) w[si] = part ? w[si] * acc[si] : acc[si];
+    for (int e = 0; e < 4; ++e) {
+      const int s = 16 * (s0 + si) + 4 * lq + e;
+      const float f = fast_exp2(static_cast<float>(at - As[s])) * p.scale;
+      const float x = s < t ? w[si][e] * f : 0.0f;
+      row_sum += x;
+      float col = x;
+      col += __shfl_xor(col, 1);
+      col += __shfl_xor(col, 2);
+      col += __shfl_xor(col, 4);
+      col += __shfl_xor(col, 8);
+      if (li == 0) Cols[ti][s] = col;
     }
-    // lane: token t = 16 ti + li against s = 16 si + 4 lq + e
-    const int t = 16 * ti + li;
-    const double at = As[t];
-#pragma unroll
-    for (int si = 0; si < kNT; ++si) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int s = 16 * si + 4 * lq + e;
-        float x = 0.0f;
-        if (si <= ti && s < t) x = w[si][e] * fast_exp2(static_cast<float>(at - As[s])) * p.scale;
-        row_sum += x;
-        float col = x;
-        col += __shfl_xor(col, 1);
-        col += __shfl_xor(col, 2);
-        col += __shfl_xor(col, 4);
-        col += __shfl_xor(col, 8);
-        if (li == 0) Cols[ti][s] = col;
-      }
-    }
-    row_sum += __shfl_xor(row_sum, 16);
-    row_sum += __shfl_xor(row_sum, 32);
-    if (lq == 0) Rows[t] = row_sum;
   }
+  row_sum += __shfl_xor(row_sum, 16);
+  row_sum += __shfl_xor(row_sum, 32);
+  if (lq == 0) Rows[wave % kPer][t] = row_sum;
   __syncthreads();
   if (tid < rows) {
-    float c = 0.0f;
+    float c = 0.0f, r = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kNT; ++w) c += Cols[w][tid];
-    p.out[(t0 + tid) * p.plan.heads + h] = Rows[tid] - c;
+    for (int i = 0; i < kNT; ++i) c += Cols[i][tid];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r += Rows[i][tid];
+    p.out[(t0 + tid) * p.plan.heads + h] = r - c;
   }
 }
 
 // One workgroup per (segment, head): the inner product at the segment's end,
 // then the sums from there backwards, in 64 bits.
 __global__ __launch_bounds__(256) void linattn_decay_grad_kernel(LinDecayGrad p) {
-  __shared__ double Red[256];
+  __shared__ double Red[4];
   __shared__ double Run[4][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int h = blockIdx.x % p.plan.heads;
@@ -172,9 +219,10 @@ __global__ __launch_bounds__(256) void linattn_decay_grad_kernel(LinDecayGrad p)
     if (p.dlast) {
       state = p.last + by_seq;
       adj = p.dlast + by_seq;
-      double sum = 0.0;
-      for (int64_t t = sg.begin + tail; t < sg.end; ++t)
-        sum += log2_decay(decay_at(p.g, p.g_kind, t, p.plan.heads, h));
+      const int64_t t = sg.begin + tail + lane;  // (a chunk has at most 64 tokens)
+      double sum = t < sg.end ? log2_decay(decay_at(p.g, p.g_kind, t, p.plan.heads, h)) : 0.0;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
       factor = fast_exp2(static_cast<float>(sum));
     }
   } else {
@@ -182,16 +230,26 @@ __global__ __launch_bounds__(256) void linattn_decay_grad_kernel(LinDecayGrad p)
     adj = p.adjoints + (slot * p.plan.heads + h) * p.size;
   }
   double dot = 0.0;
-  if (state)
-    for (int64_t i = tid; i < p.size; i += 256)
-      dot += static_cast<double>(state[i]) * static_cast<double>(adj[i]);
-  Red[tid] = dot;
-  __syncthreads();
-  for (int d = 128; d > 0; d >>= 1) {
-    if (tid < d) Red[tid] += Red[tid + d];
-    __syncthreads();
+  if (state) {
+    // 16 elements of both in flight a thread (latency, not bytes)
+    constexpr int kFly = 16;
+    for (int64_t i0 = tid; i0 < p.size; i0 += 256 * kFly) {
+      float x[kFly], y[kFly];
+#pragma unroll
+      for (int j = 0; j < kFly; ++j) {
+        const int64_t i = i0 + 256 * j;
+        x[j] = i < p.size ? state[i] : 0.0f;
+        y[j] = i < p.size ? adj[i] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kFly; ++j) dot += static_cast<double>(x[j]) * static_cast<double>(y[j]);
+    }
   }
-  double end = Red[0] * factor;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
+  if (lane == 0) Red[wave] = dot;
+  __syncthreads();
+  double end = (Red[0] + Red[1] + Red[2] + Red[3]) * factor;
   for (int64_t base = (n - 1) / 256 * 256; base >= 0; base -= 256) {
     // thread i takes token base + 255 - i: sums from the end are prefix sums
     const int64_t k = base + 255 - tid;
@@ -370,22 +428,14 @@ int linattn_chunk(bool bf16) { return bf16 ? kLinChunkBf16 : kLinChunkF32; }
 
 int linattn_slice(int dv) { return dv > 64 ? 128 : 64; }
 
-bool linattn_pairs_heads(const LinCore &a, int mode) {
-  return mode != kLinOutDot && a.v.d <= 64 && a.k.div % 2 == 0 &&
-         (mode == kLinState || a.q.div % 2 == 0);
-}
+bool linattn_pairs_heads(int div, int dv) { return dv <= 64 && div % 2 == 0; }
 
-int launch_linattn_core(const LinCore &a, int mode, bool reverse, bool bf16, void *stream) {
-  return bf16 ? launch_linattn_core_bf16(a, mode, reverse, stream)
-              : launch_linattn_core_f32(a, mode, reverse, stream);
-}
-
-int launch_linattn_chain(const LinChain &a, void *stream) {
+int launch_linattn_chain(const LinChain &a, const LinChain *b, void *stream) {
   const int64_t parts = (a.size + 255) / 256;
   hipLaunchKernelGGL(linattn_chain_kernel,
                      dim3(static_cast<unsigned>(a.plan.nseq * static_cast<int64_t>(a.plan.heads)),
-                          static_cast<unsigned>(parts)),
-                     dim3(256), 0, static_cast<hipStream_t>(stream), a);
+                          static_cast<unsigned>(parts), b ? 2 : 1),
+                     dim3(256), 0, static_cast<hipStream_t>(stream), a, b ? *b : a);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -393,10 +443,18 @@ int launch_linattn_pairs(const LinPairs &a, bool bf16, void *stream) {
   const dim3 grid(
       static_cast<unsigned>(a.plan.slots * (a.plan.seg_len / a.chunk) * a.plan.heads));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (bf16)
-    hipLaunchKernelGGL(linattn_pairs_kernel<uint16_t>, grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL(linattn_pairs_kernel<float>, grid, dim3(256), 0, s, a);
+  // 16 tiles in pairs, or 4: a wave each
+  if (bf16) {
+    if (a.plan.vec)
+      hipLaunchKernelGGL((linattn_pairs_kernel<uint16_t, true>), grid, dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((linattn_pairs_kernel<uint16_t, false>), grid, dim3(512), 0, s, a);
+  } else {
+    if (a.plan.vec)
+      hipLaunchKernelGGL((linattn_pairs_kernel<float, true>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((linattn_pairs_kernel<float, false>), grid, dim3(256), 0, s, a);
+  }
   return static_cast<int>(hipGetLastError());
 }
 

@@ -108,28 +108,46 @@ int check_sizes(const Sizes &z) {
   return SSM_OK;
 }
 
-// Segments.  A sequence's chunks follow one another, so one segment a
-// sequence leaves nseq * heads * slices workgroups; with fewer than
-// kFewGroups of them, segments of at least kMinSegment tokens are cut until
-// there are about kManyGroups, for the price of a pass over k and v that
-// forms the states between them.  The gradient of the decay is summed over
-// one segment in 64 bits from an inner product at its end, so with it
-// segments have at most kMaxGradSegment tokens.
-constexpr int64_t kFewGroups = 384, kManyGroups = 768, kMinSegment = 256;
-constexpr int64_t kMaxGradSegment = 1024;
+// Segments.  A sequence's chunks follow one another, so that one segment a
+// sequence leaves as many workgroups as there are heads (or pairs of them)
+// and column slices.  Where they fill the GPU's places for workgroups less
+// than half, the sequences are cut into as many segments of at least
+// kMinSegment tokens as fill them once, for the price of a pass over k and v
+// (and q and do) that forms the states between them: that pass and the chain
+// cost about half of the output pass (measured, 8192 tokens, 80 heads of 64
+// on states of 128: 50 + 14 of 175 us; uncut 290 us).  A CU holds two
+// workgroups, or one of heads over 128 wide.  The gradient of the decay is
+// summed over one segment in 64 bits from an inner product at its end, so
+// with it segments have at most kMaxGradSegment tokens.
+constexpr int64_t kPlaces = 512, kMinSegment = 256, kMaxGradSegment = 1024;
 
-ssm::LinPlan make_plan(const Sizes &z, bool decay_grad) {
+// workgroups that a sequence's chunk pass has
+int64_t groups_of(const Sizes &z, bool backward) {
+  const int64_t div = z.heads / z.qk_heads;
+  auto slices = [](int64_t d) {
+    const int64_t w = ssm::linattn_slice(static_cast<int>(d));
+    return (d + w - 1) / w;
+  };
+  const int64_t pair = ssm::linattn_pairs_heads(static_cast<int>(div), static_cast<int>(z.dv)) ? 2 : 1;
+  const int64_t one = z.heads / pair * slices(z.dv);
+  return backward ? one + 2 * z.heads * slices(z.dk) : one;
+}
+
+ssm::LinPlan make_plan(const Sizes &z, bool backward, bool decay_grad) {
   const int64_t chunk = ssm::linattn_chunk(z.bf16());
-  const int64_t width = ssm::linattn_slice(static_cast<int>(z.dv));
-  const int64_t slices = (z.dv + width - 1) / width;
   const int64_t longest = z.packed ? z.tokens : z.tokens / z.nseq;
-  const int64_t groups = z.nseq * z.heads * slices;
+  const int64_t groups = groups_of(z, backward);
+  const int64_t places = z.dk > 128 || (backward && z.dv > 128) ? kPlaces / 2 : kPlaces;
   int64_t seg = up(longest > 0 ? longest : 1, chunk);
-  // packed sequences may differ in length: their tokens count, not their number
-  if (groups < kFewGroups || z.packed) {
-    const int64_t even = up((z.tokens * z.heads * slices + kManyGroups - 1) / kManyGroups, chunk);
-    const int64_t cut = even > kMinSegment ? even : kMinSegment;
-    if (cut < seg) seg = cut;
+  if (z.packed) {
+    // sequences may differ in length: their tokens count, not their number
+    const int64_t cut = up((z.tokens * groups + places - 1) / places, chunk);
+    if (cut < seg) seg = cut > kMinSegment ? cut : kMinSegment;
+    if (seg > longest) seg = up(longest > 0 ? longest : 1, chunk);
+  } else {
+    int64_t segs = places / (z.nseq * groups);
+    if (segs > longest / kMinSegment) segs = longest / kMinSegment;
+    if (segs > 1) seg = up((longest + segs - 1) / segs, chunk);
   }
   if (decay_grad && seg > kMaxGradSegment) seg = kMaxGradSegment;
   ssm::LinPlan p{};
@@ -281,13 +299,15 @@ ssm::LinSide side(const void *p, int64_t stride, int64_t d, int64_t div) {
 
 extern "C" {
 
-int ssm_linattn_plan(int64_t tokens, int64_t nseq, int packed, int64_t heads, int64_t qk_dim,
-                     int64_t v_dim, int dtype, int backward, int64_t *plan_out) {
+int ssm_linattn_plan(int64_t tokens, int64_t nseq, int packed, int64_t heads, int64_t qk_heads,
+                     int64_t qk_dim, int64_t v_dim, int dtype, int backward, int64_t *plan_out) {
   if (!plan_out) return fail(SSM_ERR_INVALID_ARG, "plan_out is NULL");
-  const Sizes z{tokens, nseq, heads, heads, qk_dim, v_dim, dtype, packed != 0};
+  if (backward < 0 || backward > 2)
+    return fail(SSM_ERR_INVALID_ARG, "backward=%d: 0..2", backward);
+  const Sizes z{tokens, nseq, heads, qk_heads, qk_dim, v_dim, dtype, packed != 0};
   int st = check_sizes(z);
   if (st != SSM_OK) return st;
-  const ssm::LinPlan p = make_plan(z, backward != 0);
+  const ssm::LinPlan p = make_plan(z, backward != 0, backward == 2);
   if ((st = check_plan(z, p)) != SSM_OK) return st;
   plan_out[0] = p.seg_len;
   plan_out[1] = p.slots;
@@ -297,12 +317,13 @@ int ssm_linattn_plan(int64_t tokens, int64_t nseq, int packed, int64_t heads, in
 }
 
 int ssm_linattn_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t heads,
-                               int64_t qk_dim, int64_t v_dim, int dtype, size_t *bytes) {
+                               int64_t qk_heads, int64_t qk_dim, int64_t v_dim, int dtype,
+                               size_t *bytes) {
   if (!bytes) return fail(SSM_ERR_INVALID_ARG, "bytes is NULL");
-  const Sizes z{tokens, nseq, heads, heads, qk_dim, v_dim, dtype, packed != 0};
+  const Sizes z{tokens, nseq, heads, qk_heads, qk_dim, v_dim, dtype, packed != 0};
   int st = check_sizes(z);
   if (st != SSM_OK) return st;
-  const ssm::LinPlan p = make_plan(z, false);
+  const ssm::LinPlan p = make_plan(z, false, false);
   if ((st = check_plan(z, p)) != SSM_OK) return st;
   *bytes = static_cast<size_t>(fwd_layout(z, p).total);
   return ok();
@@ -323,7 +344,7 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   if (tokens > 0 && !o) return fail(SSM_ERR_INVALID_ARG, "o is NULL");
   if (!aligned(o, es) || !aligned(h_final, 4))
     return fail(SSM_ERR_INVALID_ARG, "output not aligned (o=%p h_final=%p)", o, (void *)h_final);
-  ssm::LinPlan plan = make_plan(z, false);
+  ssm::LinPlan plan = make_plan(z, false, false);
   if ((st = check_plan(z, plan)) != SSM_OK) return st;
   const FwdLayout l = fwd_layout(z, plan);
   if ((st = check_workspace(workspace, workspace_bytes, static_cast<size_t>(l.total))) != SSM_OK)
@@ -361,17 +382,17 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     char *w = static_cast<char *>(workspace);
     a.out_slots = reinterpret_cast<float *>(w + l.states);
     a.out_decay = reinterpret_cast<float *>(w + l.decay);
-    if ((err = ssm::launch_linattn_core(a, ssm::kLinState, false, z.bf16(), stream)) != 0)
-      return hip_failed(err);
+    err = z.bf16() ? ssm::launch_linattn_states_bf16(a, nullptr, stream)
+                   : ssm::launch_linattn_states_f32(a, nullptr, stream);
+    if (err != 0) return hip_failed(err);
     const ssm::LinChain ch{plan, a.out_slots, a.out_decay, h0, qk_dim * v_dim, 0};
-    if ((err = ssm::launch_linattn_chain(ch, stream)) != 0) return hip_failed(err);
+    if ((err = ssm::launch_linattn_chain(ch, nullptr, stream)) != 0) return hip_failed(err);
     a.in_slots = a.out_slots;
   }
   a.out_seqs = h_final;
   a.out = o;
-  if ((err = ssm::launch_linattn_core(a, ssm::kLinOut, false, z.bf16(), stream)) != 0)
-    return hip_failed(err);
-  return ok();
+  err = z.bf16() ? ssm::launch_linattn_out_bf16(a, stream) : ssm::launch_linattn_out_f32(a, stream);
+  return err != 0 ? hip_failed(err) : ok();
 }
 
 int ssm_linattn_bwd_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t heads,
@@ -382,7 +403,7 @@ int ssm_linattn_bwd_workspace_size(int64_t tokens, int64_t nseq, int packed, int
   const Sizes z{tokens, nseq, heads, qk_heads, qk_dim, v_dim, dtype, packed != 0};
   int st = check_sizes(z);
   if (st != SSM_OK) return st;
-  const ssm::LinPlan p = make_plan(z, want_dg != 0);
+  const ssm::LinPlan p = make_plan(z, true, want_dg != 0);
   if ((st = check_plan(z, p)) != SSM_OK) return st;
   *bytes = static_cast<size_t>(bwd_layout(z, p, want_dg).total);
   return ok();
@@ -414,7 +435,7 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   for (const void *p : words)
     if (!aligned(p, 4)) return fail(SSM_ERR_INVALID_ARG, "pointer %p not 4-byte aligned", p);
   const int want_dg = !dg ? 0 : flags & SSM_FLAG_HEAD_DECAY ? 2 : 1;
-  ssm::LinPlan plan = make_plan(z, want_dg != 0);
+  ssm::LinPlan plan = make_plan(z, true, want_dg != 0);
   if ((st = check_plan(z, plan)) != SSM_OK) return st;
   const BwdLayout l = bwd_layout(z, plan, want_dg);
   if ((st = check_workspace(workspace, workspace_bytes, static_cast<size_t>(l.total))) != SSM_OK)
@@ -461,78 +482,61 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     a.sb = 1;
     a.out_slots = f32(l.states);
     a.out_decay = f32(l.decay);
-    if ((err = ssm::launch_linattn_core(a, ssm::kLinState, false, bf16, stream)) != 0)
-      return hip_failed(err);
+    ssm::LinCore b = a;  // and their adjoints
+    b.q = Q;
+    b.k = Q;
+    b.v = O;
+    b.into = scale;
+    b.out_slots = f32(l.adjoints);
+    b.out_decay = f32(l.adecay);
+    err = bf16 ? ssm::launch_linattn_states_bf16(a, &b, stream)
+               : ssm::launch_linattn_states_f32(a, &b, stream);
+    if (err != 0) return hip_failed(err);
     const ssm::LinChain fwd{plan, f32(l.states), f32(l.decay), h0, qk_dim * v_dim, 0};
-    if ((err = ssm::launch_linattn_chain(fwd, stream)) != 0) return hip_failed(err);
-    a.q = Q;  // and their adjoints
-    a.k = Q;
-    a.v = O;
-    a.into = scale;
-    a.out_slots = f32(l.adjoints);
-    a.out_decay = f32(l.adecay);
-    if ((err = ssm::launch_linattn_core(a, ssm::kLinState, true, bf16, stream)) != 0)
-      return hip_failed(err);
     const ssm::LinChain rev{plan, f32(l.adjoints), f32(l.adecay), dh_final, qk_dim * v_dim, 1};
-    if ((err = ssm::launch_linattn_chain(rev, stream)) != 0) return hip_failed(err);
+    if ((err = ssm::launch_linattn_chain(fwd, &rev, stream)) != 0) return hip_failed(err);
   }
   const bool shared = div > 1;
-  const int dot = want_dg ? ssm::kLinOutDot : ssm::kLinOut;
-  {  // dq: in token order on S^T
-    ssm::LinCore a = base;
-    a.q = O;
-    a.k = V;
-    a.v = K;
-    a.inter = a.inside = scale;
-    a.into = 1.0f;
-    a.in_slots = many ? f32(l.states) : nullptr;
-    a.in_seqs = h0;
-    a.sa = 1;
-    a.sb = static_cast<int>(v_dim);
-    a.out = shared ? static_cast<void *>(f32(l.dq)) : dq;
-    a.out_f32 = shared;
-    if (want_dg) {
-      a.x = Q;
-      a.dots = f32(l.xdots);
-      a.out_seqs = f32(l.last);
-    }
-    if ((err = ssm::launch_linattn_core(a, dot, false, bf16, stream)) != 0) return hip_failed(err);
+  ssm::LinCore gq = base;  // dq: in token order on S^T
+  gq.q = O;
+  gq.k = V;
+  gq.v = K;
+  gq.inter = gq.inside = scale;
+  gq.into = 1.0f;
+  gq.in_slots = many ? f32(l.states) : nullptr;
+  gq.in_seqs = h0;
+  gq.sa = 1;
+  gq.sb = static_cast<int>(v_dim);
+  gq.out = shared ? static_cast<void *>(f32(l.dq)) : dq;
+  gq.out_f32 = shared;
+  ssm::LinCore gk = gq;  // dk: against it on M^T
+  gk.q = V;
+  gk.k = O;
+  gk.v = Q;
+  gk.inter = 1.0f;
+  gk.into = scale;
+  gk.in_slots = many ? f32(l.adjoints) : nullptr;
+  gk.in_seqs = dh_final;
+  gk.out = shared ? static_cast<void *>(f32(l.dk)) : dk;
+  ssm::LinCore gv = gk;  // dv: against it on M
+  gv.q = K;
+  gv.k = Q;
+  gv.v = O;
+  gv.sa = static_cast<int>(v_dim);
+  gv.sb = 1;
+  gv.out = dv;
+  gv.out_f32 = 0;
+  gv.out_seqs = dh0;
+  if (want_dg) {
+    gq.x = Q;
+    gq.dots = f32(l.xdots);
+    gq.out_seqs = f32(l.last);
+    gk.x = K;
+    gk.dots = f32(l.ydots);
   }
-  {  // dk: against it on M^T
-    ssm::LinCore a = base;
-    a.q = V;
-    a.k = O;
-    a.v = Q;
-    a.inter = 1.0f;
-    a.inside = a.into = scale;
-    a.in_slots = many ? f32(l.adjoints) : nullptr;
-    a.in_seqs = dh_final;
-    a.sa = 1;
-    a.sb = static_cast<int>(v_dim);
-    a.out = shared ? static_cast<void *>(f32(l.dk)) : dk;
-    a.out_f32 = shared;
-    if (want_dg) {
-      a.x = K;
-      a.dots = f32(l.ydots);
-    }
-    if ((err = ssm::launch_linattn_core(a, dot, true, bf16, stream)) != 0) return hip_failed(err);
-  }
-  {  // dv: against it on M
-    ssm::LinCore a = base;
-    a.q = K;
-    a.k = Q;
-    a.v = O;
-    a.inter = 1.0f;
-    a.inside = a.into = scale;
-    a.in_slots = many ? f32(l.adjoints) : nullptr;
-    a.in_seqs = dh_final;
-    a.sa = static_cast<int>(v_dim);
-    a.sb = 1;
-    a.out = dv;
-    a.out_seqs = dh0;
-    if ((err = ssm::launch_linattn_core(a, ssm::kLinOut, true, bf16, stream)) != 0)
-      return hip_failed(err);
-  }
+  err = bf16 ? ssm::launch_linattn_grads_bf16(gq, gk, gv, stream)
+             : ssm::launch_linattn_grads_f32(gq, gk, gv, stream);
+  if (err != 0) return hip_failed(err);
   if (shared && tokens > 0) {
     const int n = static_cast<int>(div), d = static_cast<int>(qk_dim);
     if ((err = ssm::launch_linattn_head_sum(f32(l.dq), dq, plan, n, d, bf16, stream)) != 0 ||

@@ -356,40 +356,61 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t v, int off, f32x4 
 // The sums of decays, at most 2^14 in size, are subtracted in 32 bits for
 // the weights of the pairs in bf16 (2^-10 at the largest sizes, a quarter of
 // the rounding the product then has), else in 64.
+template <typename T, int kDK, int kWaves, int kHeads, int kMode>
+struct CoreShared {
+  typedef Traits<T> Tr;
+  typedef typename Tr::Elem Elem;
+  static constexpr int C = Tr::kChunk, kCols = 16 * kWaves / kHeads;
+  static constexpr bool kOut = kMode != kLinState;
+  // row strides: 8 banks apart for the transposing reads and those of 16
+  // bytes, 4 for those of 8 bytes (cycles a read, measured: 2 and 4, with the
+  // other stride 4 and 8)
+  static constexpr int kRowQ = kDK + (Tr::kBf16 ? 8 : 4), kRowK = kDK + (Tr::kBf16 ? 16 : 4);
+  static constexpr int kRowV = kCols + (Tr::kBf16 ? 16 : 4), kRowP = C + (Tr::kBf16 ? 8 : 4);
+  alignas(16) Elem Qs[kOut ? C * kRowQ : 8];
+  alignas(16) Elem Ks[C * kRowK];
+  alignas(16) Elem Vs[kHeads][C * kRowV];
+  alignas(16) Elem Ps[kHeads][kOut ? C * kRowP : 8];
+  typename Tr::Sum As[kHeads][C];      // sums of decays (log2)
+  alignas(16) float Wi[kHeads][C];     // weights into,
+  float Wo[kHeads][C];                 // out of the state
+  float Wd[kHeads];                    // the chunk's decay
+  float Dots[kMode == kLinOutDot ? kWaves * C : 1];
+};
+
 template <typename T, int kDK, int kWaves, int kHeads, int kMode, bool kRev, bool kVec>
-__global__ __launch_bounds__(64 * kWaves, kDK > 128 ? 2 : 4) void linattn_core_kernel(LinCore p) {
+__device__ __forceinline__ void core(const LinCore &p, unsigned block,
+                                     CoreShared<T, kDK, kWaves, kHeads, kMode> &sm) {
   typedef Traits<T> Tr;
   typedef typename Tr::Frag Frag;
   typedef typename Tr::Elem Elem;
   typedef typename Tr::Sum Sum;
+  typedef CoreShared<T, kDK, kWaves, kHeads, kMode> Shared;
   constexpr int C = Tr::kChunk, kNT = C / 16, kTS = C / 32;
   constexpr int kKS = kDK / 32, kIT = kDK / 16;
-  constexpr int kThreads = 64 * kWaves, kCols = 16 * kWaves / kHeads;
+  constexpr int kThreads = 64 * kWaves, kCols = Shared::kCols;
   constexpr bool kBf16 = Tr::kBf16;
   constexpr bool kOut = kMode != kLinState, kDot = kMode == kLinOutDot;
-  // row strides: 8 banks apart for the transposing reads and those of 16
-  // bytes, 4 for those of 8 bytes (cycles a read, measured: 2 and 4, with the
-  // other stride 4 and 8)
-  constexpr int kRowQ = kDK + (kBf16 ? 8 : 4), kRowK = kDK + (kBf16 ? 16 : 4);
-  constexpr int kRowV = kCols + (kBf16 ? 16 : 4), kRowP = C + (kBf16 ? 8 : 4);
-  __shared__ __align__(16) Elem Qs[kOut ? C * kRowQ : 8];
-  __shared__ __align__(16) Elem Ks[C * kRowK];
-  __shared__ __align__(16) Elem Vs[kHeads][C * kRowV];
-  __shared__ __align__(16) Elem Ps[kHeads][kOut ? C * kRowP : 8];
-  __shared__ Sum As[kHeads][C];                  // sums of decays (log2)
-  __shared__ __align__(16) float Wi[kHeads][C];  // weights into,
-  __shared__ float Wo[kHeads][C];                // out of the state
-  __shared__ float Wd[kHeads];                   // the chunk's decay
-  __shared__ float Dots[kDot ? kWaves * C : 1];
+  constexpr int kRowQ = Shared::kRowQ, kRowK = Shared::kRowK;
+  constexpr int kRowV = Shared::kRowV, kRowP = Shared::kRowP;
+  auto &Qs = sm.Qs;
+  auto &Ks = sm.Ks;
+  auto &Vs = sm.Vs;
+  auto &Ps = sm.Ps;
+  auto &As = sm.As;
+  auto &Wi = sm.Wi;
+  auto &Wo = sm.Wo;
+  auto &Wd = sm.Wd;
+  auto &Dots = sm.Dots;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const unsigned slices = (p.v.d + kCols - 1) / kCols;
   const unsigned teams = static_cast<unsigned>(p.plan.heads) / kHeads;
-  const int slice = blockIdx.x % slices;
-  const int h0 = blockIdx.x / slices % teams * kHeads;
-  const int64_t slot = blockIdx.x / (slices * teams);
+  const int slice = block % slices;
+  const int h0 = block / slices % teams * kHeads;
+  const int64_t slot = block / (slices * teams);
   const Segment sg = segment_of(p.plan, slot);
   if (!sg.real) return;
   const bool ends = kRev ? sg.seg == 0 : sg.last;  // nothing comes after it
@@ -674,51 +695,154 @@ __global__ __launch_bounds__(64 * kWaves, kDK > 128 ? 2 : 4) void linattn_core_k
     p.out_decay[slot * p.plan.heads + h] = fast_exp2(static_cast<float>(total));
 }
 
+constexpr int waves_per_simd(int dk) { return dk > 128 ? 2 : 4; }
+
+template <typename T, int kDK, int kWaves, int kHeads, int kMode, bool kRev, bool kVec>
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(kDK)) void linattn_core_kernel(LinCore p) {
+  __shared__ CoreShared<T, kDK, kWaves, kHeads, kMode> sm;
+  core<T, kDK, kWaves, kHeads, kMode, kRev, kVec>(p, blockIdx.x, sm);
+}
+
+template <int kWaves, int kHeads>
+unsigned core_blocks(const LinCore &a) {
+  constexpr int kCols = 16 * kWaves / kHeads;
+  return static_cast<unsigned>(a.plan.slots * (a.plan.heads / kHeads) *
+                               ((a.v.d + kCols - 1) / kCols));
+}
+
 template <typename T, int kDK, int kWaves, int kHeads, int kMode, bool kRev>
 int launch_core_t(const LinCore &a, hipStream_t s) {
-  constexpr int kCols = 16 * kWaves / kHeads;
-  const int64_t slices = (a.v.d + kCols - 1) / kCols;
-  const dim3 grid(static_cast<unsigned>(a.plan.slots * (a.plan.heads / kHeads) * slices));
+  const dim3 grid(core_blocks<kWaves, kHeads>(a)), block(64 * kWaves);
   if (a.plan.vec)
     hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kWaves, kHeads, kMode, kRev, true>), grid,
-                       dim3(64 * kWaves), 0, s, a);
+                       block, 0, s, a);
   else
     hipLaunchKernelGGL((linattn_core_kernel<T, kDK, kWaves, kHeads, kMode, kRev, false>), grid,
-                       dim3(64 * kWaves), 0, s, a);
+                       block, 0, s, a);
   return static_cast<int>(hipGetLastError());
 }
 
-// kHeads = 2 has no kLinOutDot: there the first two operands are those of one
-// value head.
-template <typename T, int kDK, int kWaves, int kHeads>
-int launch_core_m(const LinCore &a, int mode, bool reverse, hipStream_t s) {
-  if (mode == kLinState)
-    return reverse ? launch_core_t<T, kDK, kWaves, kHeads, kLinState, true>(a, s)
-                   : launch_core_t<T, kDK, kWaves, kHeads, kLinState, false>(a, s);
-  if constexpr (kHeads == 1)
-    if (mode == kLinOutDot)
-      return reverse ? launch_core_t<T, kDK, kWaves, kHeads, kLinOutDot, true>(a, s)
-                     : launch_core_t<T, kDK, kWaves, kHeads, kLinOutDot, false>(a, s);
-  return reverse ? launch_core_t<T, kDK, kWaves, kHeads, kLinOut, true>(a, s)
-                 : launch_core_t<T, kDK, kWaves, kHeads, kLinOut, false>(a, s);
+// The class of a contracted size: what its tiles are padded to.
+template <typename F>
+int by_class(int d, F &&f) {
+  if (d <= 64) return f(std::integral_constant<int, 64>{});
+  if (d <= 128) return f(std::integral_constant<int, 128>{});
+  return f(std::integral_constant<int, 256>{});
 }
 
 // Workgroups: 8 waves on 128 columns of a head; where heads have at most 64,
 // on two heads that share the first two operands (which are then read, and
 // multiplied, once for both); else 4 waves on 64 columns.
-template <typename T, int kDK>
-int launch_core_k(const LinCore &a, int mode, bool reverse, hipStream_t s) {
-  if (a.v.d > 64) return launch_core_m<T, kDK, 8, 1>(a, mode, reverse, s);
-  if (linattn_pairs_heads(a, mode)) return launch_core_m<T, kDK, 8, 2>(a, mode, reverse, s);
-  return launch_core_m<T, kDK, 4, 1>(a, mode, reverse, s);
+template <typename F>
+int by_team(const LinCore &a, F &&f) {
+  typedef std::integral_constant<int, 1> One;
+  typedef std::integral_constant<int, 2> Two;
+  typedef std::integral_constant<int, 4> Four_;
+  typedef std::integral_constant<int, 8> Eight;
+  if (a.v.d > 64) return f(Eight{}, One{});
+  if (linattn_pairs_heads(a.k.div, a.v.d)) return f(Eight{}, Two{});
+  return f(Four_{}, One{});
+}
+
+// The forward output pass.
+template <typename T>
+int launch_out(const LinCore &a, hipStream_t s) {
+  return by_class(a.k.d, [&](auto dk) {
+    return by_team(a, [&](auto waves, auto heads) {
+      return launch_core_t<T, dk(), waves(), heads(), kLinOut, false>(a, s);
+    });
+  });
+}
+
+// The states that segments add: of the forward recurrence, and with `back`
+// also its adjoint's against token order, side by side in one launch.
+template <typename T, int kDK, int kWaves, int kHeads, bool kVec>
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(kDK)) void linattn_states_kernel(
+    LinCore fwd, LinCore back, unsigned nfwd) {
+  __shared__ CoreShared<T, kDK, kWaves, kHeads, kLinState> sm;
+  if (blockIdx.x < nfwd)
+    core<T, kDK, kWaves, kHeads, kLinState, false, kVec>(fwd, blockIdx.x, sm);
+  else
+    core<T, kDK, kWaves, kHeads, kLinState, true, kVec>(back, blockIdx.x - nfwd, sm);
 }
 
 template <typename T>
-int launch_core(const LinCore &a, int mode, bool reverse, void *stream) {
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a.k.d <= 64) return launch_core_k<T, 64>(a, mode, reverse, s);
-  if (a.k.d <= 128) return launch_core_k<T, 128>(a, mode, reverse, s);
-  return launch_core_k<T, 256>(a, mode, reverse, s);
+int launch_states(const LinCore &a, const LinCore *back, hipStream_t s) {
+  return by_class(a.k.d, [&](auto dk) {
+    return by_team(a, [&](auto waves, auto heads) {
+      constexpr int kDK = dk(), kWaves = waves(), kHeads = heads();
+      if (!back) return launch_core_t<T, kDK, kWaves, kHeads, kLinState, false>(a, s);
+      const unsigned n = core_blocks<kWaves, kHeads>(a);
+      const dim3 grid(2 * n), block(64 * kWaves);
+      if (a.plan.vec)
+        hipLaunchKernelGGL((linattn_states_kernel<T, kDK, kWaves, kHeads, true>), grid, block, 0,
+                           s, a, *back, n);
+      else
+        hipLaunchKernelGGL((linattn_states_kernel<T, kDK, kWaves, kHeads, false>), grid, block, 0,
+                           s, a, *back, n);
+      return static_cast<int>(hipGetLastError());
+    });
+  });
+}
+
+// The three gradients in one launch, so that together they fill the GPU
+// where one alone has too few workgroups: dq and dk contract over v_dim
+// (kDKv), dv over qk_dim (kDKq).  All of one workgroup size.
+template <typename T, int kDKv, int kDKq, int kWaves, int kHeads, bool kDots, bool kVec>
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(kDKv > kDKq ? kDKv : kDKq)) void
+linattn_grads_kernel(LinCore dq, LinCore dk, LinCore dv, unsigned n) {
+  constexpr int kMode = kDots ? kLinOutDot : kLinOut;
+  __shared__ union {
+    CoreShared<T, kDKv, kWaves, 1, kMode> a;
+    CoreShared<T, kDKq, kWaves, kHeads, kLinOut> b;
+  } sm;
+  if (blockIdx.x < n)
+    core<T, kDKv, kWaves, 1, kMode, false, kVec>(dq, blockIdx.x, sm.a);
+  else if (blockIdx.x < 2 * n)
+    core<T, kDKv, kWaves, 1, kMode, true, kVec>(dk, blockIdx.x - n, sm.a);
+  else
+    core<T, kDKq, kWaves, kHeads, kLinOut, true, kVec>(dv, blockIdx.x - 2 * n, sm.b);
+}
+
+template <typename T, int kDKv, int kDKq, int kWaves, int kHeads>
+int launch_grads_t(const LinCore &dq, const LinCore &dk, const LinCore &dv, hipStream_t s) {
+  const unsigned n = core_blocks<kWaves, 1>(dq);
+  const dim3 grid(2 * n + core_blocks<kWaves, kHeads>(dv)), block(64 * kWaves);
+  auto go = [&](auto dots, auto vec) {
+    hipLaunchKernelGGL((linattn_grads_kernel<T, kDKv, kDKq, kWaves, kHeads, dots(), vec()>), grid,
+                       block, 0, s, dq, dk, dv, n);
+  };
+  typedef std::true_type Yes;
+  typedef std::false_type No;
+  if (dq.dots)
+    dq.plan.vec ? go(Yes{}, Yes{}) : go(Yes{}, No{});
+  else
+    dq.plan.vec ? go(No{}, Yes{}) : go(No{}, No{});
+  return static_cast<int>(hipGetLastError());
+}
+
+// The gradients' workgroups have 8 waves unless both head sizes are at most
+// 64; 128 columns of an output of at most 64 are then half empty, except
+// where dv takes two heads.
+template <typename T>
+int launch_grads(const LinCore &dq, const LinCore &dk, const LinCore &dv, hipStream_t s) {
+  const int qk = dv.k.d, v = dq.k.d;
+  if (qk <= 64 && v <= 64) return launch_grads_t<T, 64, 64, 4, 1>(dq, dk, dv, s);
+  return by_class(v, [&](auto cv) {
+    return by_class(qk, [&](auto cq) {
+      constexpr int kDKv = cv(), kDKq = cq();
+      if constexpr (kDKv == 64) {
+        if constexpr (kDKq == 64)
+          return static_cast<int>(hipErrorInvalidValue);  // taken above
+        else if (linattn_pairs_heads(dv.k.div, dv.v.d))
+          return launch_grads_t<T, kDKv, kDKq, 8, 2>(dq, dk, dv, s);
+        else
+          return launch_grads_t<T, kDKv, kDKq, 8, 1>(dq, dk, dv, s);
+      } else {
+        return launch_grads_t<T, kDKv, kDKq, 8, 1>(dq, dk, dv, s);
+      }
+    });
+  });
 }
 
 }  // namespace lin

@@ -111,12 +111,20 @@ struct LinStep {
 // tokens of a chunk, output columns of one workgroup
 int linattn_chunk(bool bf16);
 int linattn_slice(int dv);
-// whether one workgroup takes two value heads
-bool linattn_pairs_heads(const LinCore &a, int mode);
-int launch_linattn_core(const LinCore &a, int mode, bool reverse, bool bf16, void *stream);
-int launch_linattn_core_bf16(const LinCore &a, int mode, bool reverse, void *stream);
-int launch_linattn_core_f32(const LinCore &a, int mode, bool reverse, void *stream);
-int launch_linattn_chain(const LinChain &a, void *stream);
+// whether a workgroup takes two value heads: they share the first two
+// operands (`div` value heads to one of theirs) and have at most 64 columns
+bool linattn_pairs_heads(int div, int dv);
+int launch_linattn_out_bf16(const LinCore &a, void *stream);
+int launch_linattn_out_f32(const LinCore &a, void *stream);
+// the states that segments add (a: in token order; back, if not null: against it)
+int launch_linattn_states_bf16(const LinCore &a, const LinCore *back, void *stream);
+int launch_linattn_states_f32(const LinCore &a, const LinCore *back, void *stream);
+int launch_linattn_grads_bf16(const LinCore &dq, const LinCore &dk, const LinCore &dv,
+                              void *stream);
+int launch_linattn_grads_f32(const LinCore &dq, const LinCore &dk, const LinCore &dv,
+                             void *stream);
+// one or two (b not null) chains over the same segments
+int launch_linattn_chain(const LinChain &a, const LinChain *b, void *stream);
 int launch_linattn_pairs(const LinPairs &a, bool bf16, void *stream);
 int launch_linattn_decay_grad(const LinDecayGrad &a, void *stream);
 // sums of `div` consecutive heads: in (tokens, heads, d) fp32 -> out (tokens, heads / div, d)

@@ -115,24 +115,24 @@ def test_refused_before_any_hip_call(lib, case):
 
 def test_sizes_and_plans(lib):
     size = ctypes.c_size_t(0)
-    assert lib.ssm_linattn_workspace_size(64, 1, 0, 4, 64, 64, BF16, None) == 1
-    assert lib.ssm_linattn_workspace_size(64, 1, 0, 4, 300, 64, BF16, ctypes.byref(size)) == 2
+    assert lib.ssm_linattn_workspace_size(64, 1, 0, 4, 4, 64, 64, BF16, None) == 1
+    assert lib.ssm_linattn_workspace_size(64, 1, 0, 4, 4, 300, 64, BF16, ctypes.byref(size)) == 2
     assert lib.ssm_linattn_bwd_workspace_size(64, 1, 0, 4, 3, 64, 64, BF16, 0,
                                               ctypes.byref(size)) == 1
     assert lib.ssm_linattn_bwd_workspace_size(64, 1, 0, 4, 4, 64, 64, BF16, 3,
                                               ctypes.byref(size)) == 1
-    assert lib.ssm_linattn_plan(64, 1, 0, 4, 64, 64, BF16, 0, None) == 1
+    assert lib.ssm_linattn_plan(64, 1, 0, 4, 4, 64, 64, BF16, 0, None) == 1
     assert lib.ssm_block_norm_bwd_workspace_size(8, 64, None) == 1
     # one short sequence, or many: nothing to cut, no workspace
-    assert ssm.ssm_linattn_workspace_size(64, 1, 4, 64, 64) == 0
-    assert ssm.ssm_linattn_workspace_size(4096 * 64, 64, 16, 128, 128) == 0
-    assert ssm.ssm_linattn_workspace_size(8192, 1, 2, 64, 64) > 0
+    assert ssm.ssm_linattn_workspace_size(64, 1, 4, 4, 64, 64) == 0
+    assert ssm.ssm_linattn_workspace_size(4096 * 64, 64, 16, 16, 128, 128) == 0
+    assert ssm.ssm_linattn_workspace_size(8192, 1, 2, 2, 64, 64) > 0
     for packed in (False, True):
         for tokens, nseq in ((0, 1), (1, 1), (5000, 1), (5000, 4), (65536, 1)):
-            for back in (False, True):
-                p = ssm.ssm_linattn_plan(tokens, nseq, 8, 128, 128, packed=packed, backward=back)
+            for back in (0, 1, 2):
+                p = ssm.ssm_linattn_plan(tokens, nseq, 8, 4, 128, 128, packed=packed, backward=back)
                 assert p["segment"] % p["chunk"] == 0 and p["segments"] >= nseq
-                assert not back or p["segment"] <= 1024
+                assert back < 2 or p["segment"] <= 1024
                 if packed:
                     # first slot of sequence i, whatever the lengths
                     assert p["segments"] >= tokens // p["segment"] + nseq

@@ -226,7 +226,7 @@ def test_segments_agree_with_one_after_another():
     """A long sequence (cut into segments taken in parallel) against its
     halves, the second continuing from the first's state."""
     inp = Inputs(BF16, (1, 2500), 1, 2, 1, 64, 64, "token", True, seed=4, rate=0.02).dev()
-    assert ssm.ssm_linattn_plan(2500, 1, 2, 64, 64)["state_pass"]
+    assert ssm.ssm_linattn_plan(2500, 1, 2, 1, 64, 64)["state_pass"]
     o, h = ssm.ssm_linattn_fwd(inp.q, inp.k, inp.v, inp.g, inp.scale, h0=inp.h0)
     part = lambda x, a, b: x[:, a:b].contiguous()  # noqa: E731
     h1 = inp.h0
@@ -251,7 +251,7 @@ def test_deterministic():
 def test_workspace_contents_do_not_matter():
     inp = Inputs(BF16, (1, 900), 1, 2, 1, 64, 64, "token", True, seed=7).dev()
     a = (inp.q, inp.k, inp.v, inp.g, inp.scale)
-    nf = ssm.ssm_linattn_workspace_size(900, 1, 2, 64, 64)
+    nf = ssm.ssm_linattn_workspace_size(900, 1, 2, 1, 64, 64)
     nb = ssm.ssm_linattn_bwd_workspace_size(900, 1, 2, 1, 64, 64, want_dg=1)
     got = []
     for fill in (0, 255):  # 255: NaNs
