@@ -13,205 +13,89 @@ using namespace lin;
 // that enters it, one segment after another.  A thread carries one element;
 // kAhead segments are requested at once, so that the latency of memory is
 // paid once for all of them.
+// The first segment's state is the sequence's own, which its readers take
+// from there.  kElems elements a thread: 1, or 4 where there are workgroups
+// enough (24 packed prompts of 16 heads: 68 us with 1, most of them for
+// sequences of one or two segments).
 constexpr int kAhead = 8;
 
+template <int kElems>
 __global__ __launch_bounds__(256) void linattn_chain_kernel(LinChain a, LinChain other) {
   const LinChain &p = blockIdx.z ? other : a;
   const int h = blockIdx.x % static_cast<unsigned>(p.plan.heads);
   const int seq = blockIdx.x / static_cast<unsigned>(p.plan.heads);
   int64_t b, e;
   sequence_rows(p.plan, seq, &b, &e);
-  int64_t segs = (e - b + p.plan.seg_len - 1) / p.plan.seg_len;
-  if (segs < 1) segs = 1;
-  const int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
-  if (i >= p.size) return;
+  const int segs = static_cast<int>((static_cast<unsigned>(e - b) +
+                                     static_cast<unsigned>(p.plan.seg_len) - 1) /
+                                    static_cast<unsigned>(p.plan.seg_len));
+  if (segs < 2) return;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.y) * 256 * kElems + threadIdx.x;
   const int64_t slot0 = first_slot(p.plan, seq) + (p.reverse ? segs - 1 : 0);
   const int64_t step = p.reverse ? -p.plan.heads : p.plan.heads;  // cells
   const int64_t cell0 = slot0 * p.plan.heads + h;
-  float acc = p.first ? p.first[(static_cast<int64_t>(seq) * p.plan.heads + h) * p.size + i] : 0.0f;
-  for (int64_t k = 0; k < segs; k += kAhead) {
-    float add[kAhead], decay[kAhead];
+  const float *first =
+      p.first ? p.first + (static_cast<int64_t>(seq) * p.plan.heads + h) * p.size : nullptr;
+  float acc[kElems];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      // nothing reads what the last segment adds
-      const bool in = k + j + 1 < segs;
-      const int64_t cell = cell0 + (in ? k + j : 0) * step;
-      add[j] = in ? p.states[cell * p.size + i] : 0.0f;
-      decay[j] = in ? p.decay[cell] : 0.0f;
+  for (int j = 0; j < kElems; ++j)
+    acc[j] = first && i0 + 256 * j < p.size ? first[i0 + 256 * j] : 0.0f;
+  for (int k = 0; k < segs; k += kAhead) {
+    float add[kAhead][kElems], decay[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const bool in = k + u + 1 < segs;  // nothing reads what the last segment adds
+      const int64_t cell = cell0 + (in ? k + u : 0) * step;
+      decay[u] = in ? p.decay[cell] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < kElems; ++j)
+        add[u][j] = in && i0 + 256 * j < p.size ? p.states[cell * p.size + i0 + 256 * j] : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (k + j < segs) {
-        p.states[(cell0 + (k + j) * step) * p.size + i] = acc;
-        acc = fmaf(acc, decay[j], add[j]);
+    for (int u = 0; u < kAhead; ++u)
+      if (k + u < segs) {
+        float *s = p.states + (cell0 + (k + u) * step) * p.size;
+#pragma unroll
+        for (int j = 0; j < kElems; ++j) {
+          if (k + u > 0 && i0 + 256 * j < p.size) s[i0 + 256 * j] = acc[j];
+          acc[j] = fmaf(acc[j], decay[u], add[u][j]);
+        }
       }
   }
 }
 
 // -------------------------------------------------- gradient of the decay ---
-// With W_ts = scale e^{a_t - a_s} (q_t . k_s) (do_t . v_s) over all pairs
-// s < t of a sequence, dL/dg_t is the sum of W over the pairs that straddle
-// t (s < t <= r).  From the end of a segment backwards,
-//   dg_t = dg_{t+1} + (what t's row adds) - (what t's column adds),
-// dg at a segment's end being the inner product of the state there with its
-// adjoint.  Row and column sums leave out the pair (t, t), and pairs inside a
-// chunk enter rows and columns with the same 32-bit value, so that what
-// cancels, cancels: only the sums' own rounding is left.  At a sequence's
-// end the adjoint (dh_final) also meets the last tokens' own terms, which no
-// dg holds and which may be far larger; so the last chunk is summed from the
-// state before it: dg_t = e^{a_T} <S, dh_final> + rows from t on + columns
-// before t.
-
-// Pairs inside each chunk: out_t = sum_{s<t} W_ts - sum_{r>t} W_rt.  One
-// workgroup per (chunk, head); a wave takes 16 tokens t and half of the tokens
-// s (bf16) or all (fp32).  Operands come from memory straight into fragments,
-// 128 columns of all of them at once (latency bounds it: every row is read
-// by few waves and used in 8 products).
-template <typename T, bool kVec>
-__device__ __forceinline__ typename Traits<T>::Frag view_frag(__amdgpu_buffer_rsrc_t v, int off,
-                                                              int left) {
-  typedef typename Traits<T>::Frag Frag;
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (kVec) {
-      return __builtin_bit_cast(
-          Frag, __builtin_amdgcn_raw_buffer_load_b128(v, left > 0 ? off : kNowhere, 0, 0));
-    } else {
-      typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-      u16x8 x;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = __builtin_amdgcn_raw_buffer_load_b16(v, e < left ? off + 2 * e : kNowhere, 0, 0);
-      return __builtin_bit_cast(Frag, x);
-    }
-  } else {
-    Frag f;
-    if constexpr (kVec) {
-      const f32x4 a = __builtin_bit_cast(
-          f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, left > 0 ? off : kNowhere, 0, 0));
-      const f32x4 b = __builtin_bit_cast(
-          f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, left > 4 ? off + 16 : kNowhere, 0, 0));
-      f = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        f[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-            v, e < left ? off + 4 * e : kNowhere, 0, 0));
-    }
-    return f;
-  }
-}
-
-template <typename T, bool kVec>
-__global__ __launch_bounds__(512) void linattn_pairs_kernel(LinPairs p) {
-  typedef Traits<T> Tr;
-  typedef typename Tr::Frag Frag;
-  constexpr int C = Tr::kChunk, kNT = C / 16;
-  constexpr int kSub = Tr::kBf16 ? 2 : 1, kPer = kNT / kSub;  // tiles a wave, waves a tile row
-  constexpr int kKS = 4;                                      // steps of 32 columns in flight
-  __shared__ double As[C];
-  __shared__ float Cols[kNT][C];
-  __shared__ float Rows[kPer][C];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int li = lane & 15, lq = lane >> 4;
-  const int h = blockIdx.x % static_cast<unsigned>(p.plan.heads);
-  const unsigned per_seg = static_cast<unsigned>(p.plan.seg_len) / C;
-  const unsigned cs = blockIdx.x / static_cast<unsigned>(p.plan.heads);
-  const Segment sg = segment_of(p.plan, cs / per_seg);
-  const int64_t t0 = sg.begin + static_cast<int64_t>(cs % per_seg) * C;
-  if (!sg.real || t0 >= sg.end) return;
-  const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
-  const int ti = wave / kPer, s0 = wave % kPer * kSub;
-  const bool some = s0 <= ti;  // else every pair of this wave's is empty
-  f32x4 w[kSub];
-#pragma unroll
-  for (int si = 0; si < kSub; ++si) w[si] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (some) {
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const LinSide &xr = part ? p.o : p.q, &xc = part ? p.v : p.k;
-      const __amdgpu_buffer_rsrc_t vr = rows_view(
-          static_cast<const T *>(xr.p) + t0 * xr.stride + (h / xr.div) * xr.d, xr.stride, rows, xr.d);
-      const __amdgpu_buffer_rsrc_t vc = rows_view(
-          static_cast<const T *>(xc.p) + t0 * xc.stride + (h / xc.div) * xc.d, xc.stride, rows, xc.d);
-      f32x4 acc[kSub];
-#pragma unroll
-      for (int si = 0; si < kSub; ++si) acc[si] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int c0 = 0; c0 < xr.d; c0 += 32 * kKS) {
-        Frag b[kKS], a[kKS][kSub];
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks) {
-          const int c = c0 + 32 * ks + 8 * lq;
-          b[ks] = view_frag<T, kVec>(
-              vr, static_cast<int>(((16 * ti + li) * xr.stride + c) * sizeof(T)), xr.d - c);
-#pragma unroll
-          for (int si = 0; si < kSub; ++si)
-            a[ks][si] = view_frag<T, kVec>(
-                vc, static_cast<int>(((16 * (s0 + si) + li) * xc.stride + c) * sizeof(T)),
-                xc.d - c);
-        }
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-          for (int si = 0; si < kSub; ++si) acc[si] = mma(a[ks][si], b[ks], acc[si]);
-      }
-#pragma unroll
-      for (int si = 0; si < kSub; ++si) w[si] = part ? w[si] * acc[si] : acc[si];
-    }
-  }
-  if (wave == 0) {
-    const float g = lane < rows ? decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h) : 0.0f;
-    const double a = wave_sums<C>(lane < C ? log2_decay(g) : 0.0, lane);
-    if (lane < C) As[lane] = a;
-  }
-  __syncthreads();
-  // lane: token t = 16 ti + li against s = 16 (s0 + si) + 4 lq + e
-  const int t = 16 * ti + li;
-  const double at = As[t];
-  float row_sum = 0.0f;
-#pragma unroll
-  for (int si = 0; si < kSub; ++si) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int s = 16 * (s0 + si) + 4 * lq + e;
-      const float f = fast_exp2(static_cast<float>(at - As[s])) * p.scale;
-      const float x = s < t ? w[si][e] * f : 0.0f;
-      row_sum += x;
-      float col = x;
-      col += __shfl_xor(col, 1);
-      col += __shfl_xor(col, 2);
-      col += __shfl_xor(col, 4);
-      col += __shfl_xor(col, 8);
-      if (li == 0) Cols[ti][s] = col;
-    }
-  }
-  row_sum += __shfl_xor(row_sum, 16);
-  row_sum += __shfl_xor(row_sum, 32);
-  if (lq == 0) Rows[wave % kPer][t] = row_sum;
-  __syncthreads();
-  if (tid < rows) {
-    float c = 0.0f, r = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kNT; ++i) c += Cols[i][tid];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) r += Rows[i][tid];
-    p.out[(t0 + tid) * p.plan.heads + h] = r - c;
-  }
-}
-
 // One workgroup per (segment, head): the inner product at the segment's end,
-// then the sums from there backwards, in 64 bits.
-__global__ __launch_bounds__(256) void linattn_decay_grad_kernel(LinDecayGrad p) {
-  __shared__ double Red[4];
-  __shared__ double Run[4][2];
+// then the sums from there backwards, in 64 bits, a thread a token (a segment
+// has at most 1024).
+constexpr int kGradThreads = 1024;
+
+__global__ __launch_bounds__(kGradThreads) void linattn_decay_grad_kernel(LinDecayGrad p) {
+  constexpr int kWaves = kGradThreads / 64;
+  __shared__ double Red[kWaves];
+  __shared__ double Run[kWaves][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.x % p.plan.heads;
-  const int64_t slot = blockIdx.x / p.plan.heads;
+  const int h = blockIdx.x % static_cast<unsigned>(p.plan.heads);
+  const int64_t slot = blockIdx.x / static_cast<unsigned>(p.plan.heads);
   const Segment sg = segment_of(p.plan, slot);
   if (!sg.real || sg.begin >= sg.end) return;
-  const int64_t n = sg.end - sg.begin;
+  const int n = static_cast<int>(sg.end - sg.begin);
   // tokens from here on are summed from the state before them
-  const int64_t tail = sg.last ? (n - 1) / p.chunk * p.chunk : n;
+  const int tail = sg.last ? (n - 1) / p.chunk * p.chunk : n;
+  // thread i takes token n - 1 - i: sums from the end are prefix sums
+  const int k = n - 1 - tid;
+  const int64_t at = (sg.begin + k) * p.plan.heads + h;
+  float pair = 0.0f, xs[2] = {0.0f, 0.0f}, ys[2] = {0.0f, 0.0f};
+  if (k >= 0) {
+    const int64_t all = p.plan.tokens * p.plan.heads;
+    pair = p.pairs[at];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (s < p.slices) {
+        xs[s] = p.xdots[s * all + at];
+        ys[s] = p.ydots[s * all + at];
+      }
+  }
   const float *state = nullptr, *adj = nullptr;
   const int64_t by_seq = (static_cast<int64_t>(sg.seq) * p.plan.heads + h) * p.size;
   double factor = 1.0;
@@ -233,11 +117,11 @@ __global__ __launch_bounds__(256) void linattn_decay_grad_kernel(LinDecayGrad p)
   if (state) {
     // 16 elements of both in flight a thread (latency, not bytes)
     constexpr int kFly = 16;
-    for (int64_t i0 = tid; i0 < p.size; i0 += 256 * kFly) {
+    for (int i0 = tid; i0 < p.size; i0 += kGradThreads * kFly) {
       float x[kFly], y[kFly];
 #pragma unroll
       for (int j = 0; j < kFly; ++j) {
-        const int64_t i = i0 + 256 * j;
+        const int i = i0 + kGradThreads * j;
         x[j] = i < p.size ? state[i] : 0.0f;
         y[j] = i < p.size ? adj[i] : 0.0f;
       }
@@ -247,43 +131,32 @@ __global__ __launch_bounds__(256) void linattn_decay_grad_kernel(LinDecayGrad p)
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
-  if (lane == 0) Red[wave] = dot;
+  double v = static_cast<double>(pair) + xs[0] + xs[1];
+  double y = static_cast<double>(ys[0]) + ys[1];
+  if (k < tail) {
+    v -= y;
+    y = 0.0;
+  }
+  v = wave_sums<64>(v, lane);
+  y = wave_sums<64>(y, lane);
+  if (lane == 63) {
+    Red[wave] = dot;
+    Run[wave][0] = v;
+    Run[wave][1] = y;
+  }
   __syncthreads();
-  double end = (Red[0] + Red[1] + Red[2] + Red[3]) * factor;
-  for (int64_t base = (n - 1) / 256 * 256; base >= 0; base -= 256) {
-    // thread i takes token base + 255 - i: sums from the end are prefix sums
-    const int64_t k = base + 255 - tid;
-    double v = 0.0, y = 0.0;
-    const int64_t at = (sg.begin + k) * p.plan.heads + h;
-    if (k < n) {
-      v = p.pairs[at];
-      for (int s = 0; s < p.xslices; ++s) v += p.xdots[s * p.plan.tokens * p.plan.heads + at];
-      for (int s = 0; s < p.yslices; ++s) y += p.ydots[s * p.plan.tokens * p.plan.heads + at];
-      if (k < tail) {
-        v -= y;
-        y = 0.0;
-      }
-    }
-    v = wave_sums<64>(v, lane);
-    y = wave_sums<64>(y, lane);
-    if (lane == 63) {
-      Run[wave][0] = v;
-      Run[wave][1] = y;
-    }
-    __syncthreads();
-    double before = end, from = 0.0;  // sums over the tokens behind this wave's
-    for (int w = 0; w < wave; ++w) {
+  double end = 0.0, before = 0.0, from = 0.0, ally = 0.0;
+  for (int w = 0; w < kWaves; ++w) {
+    end += Red[w];
+    ally += Run[w][1];
+    if (w < wave) {  // sums over the tokens behind this wave's
       before += Run[w][0];
       from += Run[w][1];
     }
-    const double all = end + Run[0][0] + Run[1][0] + Run[2][0] + Run[3][0];
-    const double ally = Run[0][1] + Run[1][1] + Run[2][1] + Run[3][1];
-    // columns of the tail's tokens before k (the others' are 0)
-    const double columns = k >= tail ? ally - (from + y) : 0.0;
-    if (k < n) p.dg[at] = static_cast<float>(before + v + columns);
-    __syncthreads();
-    end = all;
   }
+  // columns of the tail's tokens before k (the others' are 0)
+  const double columns = k >= tail ? ally - (from + y) : 0.0;
+  if (k >= 0) p.dg[at] = static_cast<float>(end * factor + before + v + columns);
 }
 
 // ------------------------------------------------------------ reductions ---
@@ -431,37 +304,25 @@ int linattn_slice(int dv) { return dv > 64 ? 128 : 64; }
 bool linattn_pairs_heads(int div, int dv) { return dv <= 64 && div % 2 == 0; }
 
 int launch_linattn_chain(const LinChain &a, const LinChain *b, void *stream) {
+  const int64_t cells = a.plan.nseq * static_cast<int64_t>(a.plan.heads);
   const int64_t parts = (a.size + 255) / 256;
-  hipLaunchKernelGGL(linattn_chain_kernel,
-                     dim3(static_cast<unsigned>(a.plan.nseq * static_cast<int64_t>(a.plan.heads)),
-                          static_cast<unsigned>(parts), b ? 2 : 1),
-                     dim3(256), 0, static_cast<hipStream_t>(stream), a, b ? *b : a);
-  return static_cast<int>(hipGetLastError());
-}
-
-int launch_linattn_pairs(const LinPairs &a, bool bf16, void *stream) {
-  const dim3 grid(
-      static_cast<unsigned>(a.plan.slots * (a.plan.seg_len / a.chunk) * a.plan.heads));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  // 16 tiles in pairs, or 4: a wave each
-  if (bf16) {
-    if (a.plan.vec)
-      hipLaunchKernelGGL((linattn_pairs_kernel<uint16_t, true>), grid, dim3(512), 0, s, a);
-    else
-      hipLaunchKernelGGL((linattn_pairs_kernel<uint16_t, false>), grid, dim3(512), 0, s, a);
-  } else {
-    if (a.plan.vec)
-      hipLaunchKernelGGL((linattn_pairs_kernel<float, true>), grid, dim3(256), 0, s, a);
-    else
-      hipLaunchKernelGGL((linattn_pairs_kernel<float, false>), grid, dim3(256), 0, s, a);
-  }
+  if (cells * parts > 4096)
+    hipLaunchKernelGGL(linattn_chain_kernel<4>,
+                       dim3(static_cast<unsigned>(cells), static_cast<unsigned>((parts + 3) / 4),
+                            b ? 2 : 1),
+                       dim3(256), 0, s, a, b ? *b : a);
+  else
+    hipLaunchKernelGGL(linattn_chain_kernel<1>,
+                       dim3(static_cast<unsigned>(cells), static_cast<unsigned>(parts), b ? 2 : 1),
+                       dim3(256), 0, s, a, b ? *b : a);
   return static_cast<int>(hipGetLastError());
 }
 
 int launch_linattn_decay_grad(const LinDecayGrad &a, void *stream) {
   hipLaunchKernelGGL(linattn_decay_grad_kernel,
-                     dim3(static_cast<unsigned>(a.plan.slots * a.plan.heads)), dim3(256), 0,
-                     static_cast<hipStream_t>(stream), a);
+                     dim3(static_cast<unsigned>(a.plan.slots * a.plan.heads)), dim3(kGradThreads),
+                     0, static_cast<hipStream_t>(stream), a);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -168,9 +168,10 @@ bool many_segments(const Sizes &z, const ssm::LinPlan &p) {
 int check_plan(const Sizes &z, const ssm::LinPlan &p) {
   if (z.heads * z.dk > kMaxStride || z.heads * z.dv > kMaxStride)
     return fail(SSM_ERR_UNSUPPORTED, "heads=%lld: rows too long", (long long)z.heads);
-  // the widest grids (of 512 threads): slices of 128 columns; chunks of token pairs
-  if (p.slots * z.heads * 4 > kMaxGroups || z.nseq * z.heads > kMaxGroups ||
-      p.slots * (p.seg_len / ssm::linattn_chunk(z.bf16())) * z.heads > kMaxGroups)
+  // the widest grid: three gradients of two slices and the chunks' token pairs
+  // (times two for their 512 threads)
+  if (z.nseq * z.heads > kMaxGroups ||
+      2 * p.slots * z.heads * (6 + p.seg_len / ssm::linattn_chunk(z.bf16())) > kMaxGroups)
     return fail(SSM_ERR_UNSUPPORTED, "tokens=%lld heads=%lld nseq=%lld: too many workgroups",
                 (long long)z.tokens, (long long)z.heads, (long long)z.nseq);
   return SSM_OK;
@@ -534,8 +535,9 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     gk.x = K;
     gk.dots = f32(l.ydots);
   }
-  err = bf16 ? ssm::launch_linattn_grads_bf16(gq, gk, gv, stream)
-             : ssm::launch_linattn_grads_f32(gq, gk, gv, stream);
+  const ssm::LinPairs pr{plan, Q, K, V, O, g, base.g_kind, scale, want_dg ? f32(l.pairs) : nullptr};
+  err = bf16 ? ssm::launch_linattn_grads_bf16(gq, gk, gv, want_dg ? &pr : nullptr, stream)
+             : ssm::launch_linattn_grads_f32(gq, gk, gv, want_dg ? &pr : nullptr, stream);
   if (err != 0) return hip_failed(err);
   if (shared && tokens > 0) {
     const int n = static_cast<int>(div), d = static_cast<int>(qk_dim);
@@ -544,21 +546,17 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
       return hip_failed(err);
   }
   if (want_dg) {
-    const ssm::LinPairs pr{plan, Q, K, V, O, g, base.g_kind, ssm::linattn_chunk(bf16), scale,
-                           f32(l.pairs)};
-    if ((err = ssm::launch_linattn_pairs(pr, bf16, stream)) != 0) return hip_failed(err);
-    const int slices = static_cast<int>(slices_of(qk_dim));
     ssm::LinDecayGrad a{};
     a.plan = plan;
     a.pairs = f32(l.pairs);
     a.xdots = f32(l.xdots);
     a.ydots = f32(l.ydots);
-    a.xslices = a.yslices = slices;
+    a.slices = static_cast<int>(slices_of(qk_dim));
     a.states = f32(l.states);
     a.adjoints = f32(l.adjoints);
     a.last = f32(l.last);
     a.dlast = dh_final;
-    a.size = qk_dim * v_dim;
+    a.size = static_cast<int>(qk_dim * v_dim);
     a.g = g;
     a.g_kind = base.g_kind;
     a.chunk = ssm::linattn_chunk(bf16);

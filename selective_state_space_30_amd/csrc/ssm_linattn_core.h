@@ -308,6 +308,42 @@ struct Four {
   }
 };
 
+// A fragment straight from memory: 8 elements at a byte offset of a view,
+// `left` of them in the row.
+template <typename T, bool kVec>
+__device__ __forceinline__ typename Traits<T>::Frag view_frag(__amdgpu_buffer_rsrc_t v, int off,
+                                                              int left) {
+  typedef typename Traits<T>::Frag Frag;
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (kVec) {
+      return __builtin_bit_cast(
+          Frag, __builtin_amdgcn_raw_buffer_load_b128(v, left > 0 ? off : kNowhere, 0, 0));
+    } else {
+      typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+      u16x8 x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = __builtin_amdgcn_raw_buffer_load_b16(v, e < left ? off + 2 * e : kNowhere, 0, 0);
+      return __builtin_bit_cast(Frag, x);
+    }
+  } else {
+    Frag f;
+    if constexpr (kVec) {
+      const f32x4 a = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, left > 0 ? off : kNowhere, 0, 0));
+      const f32x4 b = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, left > 4 ? off + 16 : kNowhere, 0, 0));
+      f = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        f[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            v, e < left ? off + 4 * e : kNowhere, 0, 0));
+    }
+    return f;
+  }
+}
+
 // Stores 4 neighbouring elements at a byte offset of a view, n of them in
 // the row.  (A store behind the view is dropped.)
 template <bool kVec>
@@ -444,8 +480,9 @@ __device__ __forceinline__ void core(const LinCore &p, unsigned block,
   const int state0 = 4 * (4 * lq * p.sa + (j0 + jw + li) * p.sb);
   {
     const float *in = nullptr;
+    const bool begins = kRev ? sg.last : sg.seg == 0;  // nothing comes before it
     if (kMode != kLinState)
-      in = p.in_slots ? p.in_slots + by_slot : p.in_seqs ? p.in_seqs + by_seq : nullptr;
+      in = !begins ? p.in_slots + by_slot : p.in_seqs ? p.in_seqs + by_seq : nullptr;
 #pragma unroll
     for (int it = 0; it < kIT; ++it) S[it] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (in) {
@@ -695,6 +732,153 @@ __device__ __forceinline__ void core(const LinCore &p, unsigned block,
     p.out_decay[slot * p.plan.heads + h] = fast_exp2(static_cast<float>(total));
 }
 
+// -------------------------------------------------- gradient of the decay ---
+// With W_ts = scale e^{a_t - a_s} (q_t . k_s) (do_t . v_s) over all pairs
+// s < t of a sequence, dL/dg_t is the sum of W over the pairs that straddle
+// t (s < t <= r).  From the end of a segment backwards,
+//   dg_t = dg_{t+1} + (what t's row adds) - (what t's column adds),
+// dg at a segment's end being the inner product of the state there with its
+// adjoint.  Row and column sums leave out the pair (t, t), and pairs inside a
+// chunk enter rows and columns with the same 32-bit value, so that what
+// cancels, cancels: only the sums' own rounding is left.  At a sequence's
+// end the adjoint (dh_final) also meets the last tokens' own terms, which no
+// dg holds and which may be far larger; so the last chunk is summed from the
+// state before it: dg_t = e^{a_T} <S, dh_final> + rows from t on + columns
+// before t.
+
+// Pairs inside each chunk: out_t = sum_{s<t} W_ts - sum_{r>t} W_rt, for one
+// chunk of kHeads heads that share q and k.  k and v go through LDS (every
+// wave needs half of their rows), q's and do's rows from memory into the
+// fragments of the two waves that use them.
+template <typename T, int kDKq, int kDKv, int kHeads>
+struct PairsShared {
+  typedef Traits<T> Tr;
+  static constexpr int C = Tr::kChunk, kNT = C / 16;
+  static constexpr int kSub = Tr::kBf16 ? 2 : 1, kPer = kNT / kSub;  // tiles a wave, waves a tile row
+  static constexpr int kPad = Tr::kBf16 ? 16 : 4, kRowK = kDKq + kPad, kRowV = kDKv + kPad;
+  alignas(16) typename Tr::Elem Ks[C * kRowK];
+  alignas(16) typename Tr::Elem Vs[kHeads][C * kRowV];
+  double As[kHeads][C];
+  float Cols[kHeads][kNT][C];
+  float Rows[kHeads][kPer][C];
+};
+
+template <typename T, int kDKq, int kDKv, int kWaves, int kHeads, bool kVec>
+__device__ __forceinline__ void pairs(const LinPairs &p, unsigned block,
+                                      PairsShared<T, kDKq, kDKv, kHeads> &sm) {
+  typedef Traits<T> Tr;
+  typedef typename Tr::Frag Frag;
+  typedef PairsShared<T, kDKq, kDKv, kHeads> Shared;
+  constexpr int C = Tr::kChunk, kNT = C / 16, kThreads = 64 * kWaves;
+  constexpr int kSub = Shared::kSub, kPer = Shared::kPer, kBusy = kNT * kPer;
+  static_assert(kBusy <= kWaves, "a wave for each part of a tile row");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const unsigned teams = static_cast<unsigned>(p.plan.heads) / kHeads;
+  const int h0 = block % teams * kHeads;
+  const unsigned per_seg = static_cast<unsigned>(p.plan.seg_len) / C;
+  const unsigned cs = block / teams;
+  const Segment sg = segment_of(p.plan, cs / per_seg);
+  const int64_t t0 = sg.begin + static_cast<int64_t>(cs % per_seg) * C;
+  if (!sg.real || t0 >= sg.end) return;
+  const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
+  auto head = [&](const LinSide &x, int h) __attribute__((always_inline)) {
+    return static_cast<const T *>(x.p) + t0 * x.stride + (h / x.div) * x.d;
+  };
+  const int ti = wave / kPer % kNT, s0 = wave % kPer * kSub;
+  const bool some = wave < kBusy && s0 <= ti;  // else every pair of this wave's is empty
+  Frag qf[kDKq / 32], of[kHeads][kDKv / 32];
+  {
+    Tile<T, C, kDKq, kThreads, kVec> tk;
+    Tile<T, C, kDKv, kThreads, kVec> tv[kHeads];
+    tk.load(head(p.k, h0), p.k.stride, rows, p.k.d, tid);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      tv[i].load(head(p.v, h0 + i), p.v.stride, rows, p.v.d, tid);
+    auto rows_of = [&](const LinSide &x, int h, Frag *f, int steps) __attribute__((always_inline)) {
+      const __amdgpu_buffer_rsrc_t v = rows_view(head(x, h), x.stride, rows, x.d);
+#pragma unroll
+      for (int ks = 0; ks < steps; ++ks) {
+        const int c = 32 * ks + 8 * lq;
+        f[ks] = view_frag<T, kVec>(
+            v, static_cast<int>(((16 * ti + li) * x.stride + c) * sizeof(T)), some ? x.d - c : 0);
+      }
+    };
+    rows_of(p.q, h0, qf, kDKq / 32);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) rows_of(p.o, h0 + i, of[i], kDKv / 32);
+    if (wave < kHeads) {
+      const float g = lane < rows ? decay_at(p.g, p.g_kind, t0 + lane, p.plan.heads, h0 + wave) : 0.0f;
+      const double a = wave_sums<C>(lane < C ? log2_decay(g) : 0.0, lane);
+      if (lane < C) sm.As[wave][lane] = a;
+    }
+    tk.template store<Shared::kRowK>(sm.Ks, tid);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) tv[i].template store<Shared::kRowV>(sm.Vs[i], tid);
+  }
+  __syncthreads();
+  if (wave < kBusy) {
+    f32x4 qk[kSub];
+#pragma unroll
+    for (int si = 0; si < kSub; ++si) qk[si] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (some) {
+#pragma unroll
+      for (int ks = 0; ks < kDKq / 32; ++ks)
+#pragma unroll
+        for (int si = 0; si < kSub; ++si)
+          qk[si] = mma(*reinterpret_cast<const Frag *>(
+                           &sm.Ks[(16 * (s0 + si) + li) * Shared::kRowK + 32 * ks + 8 * lq]),
+                       qf[ks], qk[si]);
+    }
+    // lane: token t = 16 ti + li against s = 16 (s0 + si) + 4 lq + e
+    const int t = 16 * ti + li;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const double at = sm.As[i][t];
+      float row_sum = 0.0f;
+#pragma unroll
+      for (int si = 0; si < kSub; ++si) {
+        f32x4 ov = {0.f, 0.f, 0.f, 0.f};
+        if (some) {
+#pragma unroll
+          for (int ks = 0; ks < kDKv / 32; ++ks)
+            ov = mma(*reinterpret_cast<const Frag *>(
+                         &sm.Vs[i][(16 * (s0 + si) + li) * Shared::kRowV + 32 * ks + 8 * lq]),
+                     of[i][ks], ov);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = 16 * (s0 + si) + 4 * lq + e;
+          const float f = fast_exp2(static_cast<float>(at - sm.As[i][s])) * p.scale;
+          const float x = s < t ? qk[si][e] * ov[e] * f : 0.0f;
+          row_sum += x;
+          float col = x;
+          col += __shfl_xor(col, 1);
+          col += __shfl_xor(col, 2);
+          col += __shfl_xor(col, 4);
+          col += __shfl_xor(col, 8);
+          if (li == 0) sm.Cols[i][ti][s] = col;
+        }
+      }
+      row_sum += __shfl_xor(row_sum, 16);
+      row_sum += __shfl_xor(row_sum, 32);
+      if (lq == 0) sm.Rows[i][wave % kPer][t] = row_sum;
+    }
+  }
+  __syncthreads();
+  if (tid < kHeads * C && tid % C < rows) {
+    const int i = tid / C, t = tid % C;
+    float c = 0.0f, r = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kNT; ++w) c += sm.Cols[i][w][t];
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) r += sm.Rows[i][w][t];
+    p.out[(t0 + t) * p.plan.heads + h0 + i] = r - c;
+  }
+}
+
+// ------------------------------------------------------------- launches ---
 constexpr int waves_per_simd(int dk) { return dk > 128 ? 2 : 4; }
 
 template <typename T, int kDK, int kWaves, int kHeads, int kMode, bool kRev, bool kVec>
@@ -785,62 +969,64 @@ int launch_states(const LinCore &a, const LinCore *back, hipStream_t s) {
   });
 }
 
-// The three gradients in one launch, so that together they fill the GPU
-// where one alone has too few workgroups: dq and dk contract over v_dim
-// (kDKv), dv over qk_dim (kDKq).  All of one workgroup size.
+// The three gradients and, with kDots, the sums over pairs in one launch, so
+// that together they fill the GPU where one alone has too few workgroups: dq
+// and dk contract over v_dim (kDKv), dv over qk_dim (kDKq).  All of one
+// workgroup size; the pairs' short workgroups come last.
 template <typename T, int kDKv, int kDKq, int kWaves, int kHeads, bool kDots, bool kVec>
 __global__ __launch_bounds__(64 * kWaves, waves_per_simd(kDKv > kDKq ? kDKv : kDKq)) void
-linattn_grads_kernel(LinCore dq, LinCore dk, LinCore dv, unsigned n) {
+linattn_grads_kernel(LinCore dq, LinCore dk, LinCore dv, LinPairs pr, unsigned n, unsigned nv) {
   constexpr int kMode = kDots ? kLinOutDot : kLinOut;
   __shared__ union {
     CoreShared<T, kDKv, kWaves, 1, kMode> a;
     CoreShared<T, kDKq, kWaves, kHeads, kLinOut> b;
+    PairsShared<T, kDKq, kDKv, kHeads> c;
   } sm;
-  if (blockIdx.x < n)
-    core<T, kDKv, kWaves, 1, kMode, false, kVec>(dq, blockIdx.x, sm.a);
-  else if (blockIdx.x < 2 * n)
-    core<T, kDKv, kWaves, 1, kMode, true, kVec>(dk, blockIdx.x - n, sm.a);
-  else
-    core<T, kDKq, kWaves, kHeads, kLinOut, true, kVec>(dv, blockIdx.x - 2 * n, sm.b);
+  if (blockIdx.x < nv)
+    core<T, kDKq, kWaves, kHeads, kLinOut, true, kVec>(dv, blockIdx.x, sm.b);
+  else if (blockIdx.x < nv + n)
+    core<T, kDKv, kWaves, 1, kMode, false, kVec>(dq, blockIdx.x - nv, sm.a);
+  else if (!kDots || blockIdx.x < nv + 2 * n)
+    core<T, kDKv, kWaves, 1, kMode, true, kVec>(dk, blockIdx.x - nv - n, sm.a);
+  else if constexpr (kDots)
+    pairs<T, kDKq, kDKv, kWaves, kHeads, kVec>(pr, blockIdx.x - nv - 2 * n, sm.c);
 }
 
 template <typename T, int kDKv, int kDKq, int kWaves, int kHeads>
-int launch_grads_t(const LinCore &dq, const LinCore &dk, const LinCore &dv, hipStream_t s) {
-  const unsigned n = core_blocks<kWaves, 1>(dq);
-  const dim3 grid(2 * n + core_blocks<kWaves, kHeads>(dv)), block(64 * kWaves);
+int launch_grads_t(const LinCore &dq, const LinCore &dk, const LinCore &dv, const LinPairs *pr,
+                   hipStream_t s) {
+  const unsigned n = core_blocks<kWaves, 1>(dq), nv = core_blocks<kWaves, kHeads>(dv);
+  const unsigned np =
+      pr ? static_cast<unsigned>(pr->plan.slots * (pr->plan.seg_len / Traits<T>::kChunk) *
+                                 (pr->plan.heads / kHeads))
+         : 0;
+  const dim3 grid(2 * n + nv + np), block(64 * kWaves);
   auto go = [&](auto dots, auto vec) {
     hipLaunchKernelGGL((linattn_grads_kernel<T, kDKv, kDKq, kWaves, kHeads, dots(), vec()>), grid,
-                       block, 0, s, dq, dk, dv, n);
+                       block, 0, s, dq, dk, dv, pr ? *pr : LinPairs{}, n, nv);
   };
   typedef std::true_type Yes;
   typedef std::false_type No;
-  if (dq.dots)
+  if (pr)
     dq.plan.vec ? go(Yes{}, Yes{}) : go(Yes{}, No{});
   else
     dq.plan.vec ? go(No{}, Yes{}) : go(No{}, No{});
   return static_cast<int>(hipGetLastError());
 }
 
-// The gradients' workgroups have 8 waves unless both head sizes are at most
-// 64; 128 columns of an output of at most 64 are then half empty, except
-// where dv takes two heads.
+// The gradients' workgroups have 8 waves (a wave for each half row of the
+// pairs' tiles); 128 columns of an output of at most 64 are then half empty,
+// except where dv takes two heads.
 template <typename T>
-int launch_grads(const LinCore &dq, const LinCore &dk, const LinCore &dv, hipStream_t s) {
-  const int qk = dv.k.d, v = dq.k.d;
-  if (qk <= 64 && v <= 64) return launch_grads_t<T, 64, 64, 4, 1>(dq, dk, dv, s);
-  return by_class(v, [&](auto cv) {
-    return by_class(qk, [&](auto cq) {
+int launch_grads(const LinCore &dq, const LinCore &dk, const LinCore &dv, const LinPairs *pr,
+                 hipStream_t s) {
+  return by_class(dq.k.d, [&](auto cv) {
+    return by_class(dv.k.d, [&](auto cq) {
       constexpr int kDKv = cv(), kDKq = cq();
-      if constexpr (kDKv == 64) {
-        if constexpr (kDKq == 64)
-          return static_cast<int>(hipErrorInvalidValue);  // taken above
-        else if (linattn_pairs_heads(dv.k.div, dv.v.d))
-          return launch_grads_t<T, kDKv, kDKq, 8, 2>(dq, dk, dv, s);
-        else
-          return launch_grads_t<T, kDKv, kDKq, 8, 1>(dq, dk, dv, s);
-      } else {
-        return launch_grads_t<T, kDKv, kDKq, 8, 1>(dq, dk, dv, s);
-      }
+      if constexpr (kDKv == 64)
+        if (linattn_pairs_heads(dv.k.div, dv.v.d))
+          return launch_grads_t<T, kDKv, kDKq, 8, 2>(dq, dk, dv, pr, s);
+      return launch_grads_t<T, kDKv, kDKq, 8, 1>(dq, dk, dv, pr, s);
     });
   });
 }

@@ -4,8 +4,8 @@
 namespace ssm {
 
 int launch_linattn_grads_bf16(const LinCore &dq, const LinCore &dk, const LinCore &dv,
-                              void *stream) {
-  return lin::launch_grads<uint16_t>(dq, dk, dv, static_cast<hipStream_t>(stream));
+                              const LinPairs *pairs, void *stream) {
+  return lin::launch_grads<uint16_t>(dq, dk, dv, pairs, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace ssm

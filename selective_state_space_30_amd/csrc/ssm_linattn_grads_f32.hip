@@ -4,8 +4,8 @@
 namespace ssm {
 
 int launch_linattn_grads_f32(const LinCore &dq, const LinCore &dk, const LinCore &dv,
-                              void *stream) {
-  return lin::launch_grads<float>(dq, dk, dv, static_cast<hipStream_t>(stream));
+                              const LinPairs *pairs, void *stream) {
+  return lin::launch_grads<float>(dq, dk, dv, pairs, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace ssm

@@ -57,7 +57,8 @@ struct LinCore {
   int sa, sb;
   void *out;            // (tokens, heads, v.d), or null (state pass)
   int out_f32;          // out in fp32 whatever the activations
-  // the inter part's dot products with the rows of x: dots (slice, tokens, heads)
+  // kLinOutDot: the state part's dot products with the rows of x, dots (slice,
+  // tokens, heads)
   LinSide x;
   float *dots;
 };
@@ -77,7 +78,7 @@ struct LinPairs {       // sums over token pairs inside each chunk
   LinPlan plan;
   LinSide q, k, v, o;
   const float *g;
-  int g_kind, chunk;
+  int g_kind;
   float scale;
   float *out;           // (tokens, heads)
 };
@@ -85,12 +86,12 @@ struct LinPairs {       // sums over token pairs inside each chunk
 struct LinDecayGrad {
   LinPlan plan;
   const float *pairs, *xdots, *ydots;  // (tokens, heads); dots by slice
-  int xslices, yslices;
+  int slices;                          // of the dots: 1 or 2
   const float *states, *adjoints;      // entering each segment, by slot
   // (sequence, head, size): the state before the last chunk, the adjoint of
   // the final state (null: zero)
   const float *last, *dlast;
-  int64_t size;
+  int size;
   const float *g;
   int g_kind, chunk;
   float *dg;
@@ -119,13 +120,13 @@ int launch_linattn_out_f32(const LinCore &a, void *stream);
 // the states that segments add (a: in token order; back, if not null: against it)
 int launch_linattn_states_bf16(const LinCore &a, const LinCore *back, void *stream);
 int launch_linattn_states_f32(const LinCore &a, const LinCore *back, void *stream);
+// dq, dk, dv and, if not null, the sums over pairs
 int launch_linattn_grads_bf16(const LinCore &dq, const LinCore &dk, const LinCore &dv,
-                              void *stream);
+                              const LinPairs *pairs, void *stream);
 int launch_linattn_grads_f32(const LinCore &dq, const LinCore &dk, const LinCore &dv,
-                             void *stream);
+                             const LinPairs *pairs, void *stream);
 // one or two (b not null) chains over the same segments
 int launch_linattn_chain(const LinChain &a, const LinChain *b, void *stream);
-int launch_linattn_pairs(const LinPairs &a, bool bf16, void *stream);
 int launch_linattn_decay_grad(const LinDecayGrad &a, void *stream);
 // sums of `div` consecutive heads: in (tokens, heads, d) fp32 -> out (tokens, heads / div, d)
 int launch_linattn_head_sum(const float *in, void *out, const LinPlan &plan, int div, int d,
