@@ -778,13 +778,31 @@ def _on_device(fn):
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         t = args[0] if args else kwargs.get(first)
-        call = fn if kwargs.get("stream") is None else inner
+        call = inner if kwargs.get("stream") is not None else fn
         if (isinstance(t, torch.Tensor) and t.is_cuda
-                and t.device.index != torch.cuda.current_device()):
+                and t.get_device() != torch.cuda.current_device()):
             with torch.cuda.device(t.device):
                 return call(*args, **kwargs)
         return call(*args, **kwargs)
     return wrapper
+
+
+def _raw_stream(dev, stream):
+    """The HIP stream of a call that already runs on ``dev`` (see
+    :func:`_on_device`)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _dense(t, name, dtype, shape, dev):
+    """Address of a dense tensor of this shape (a tuple), None of None."""
+    if t is None:
+        return None
+    if (t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape
+            and t.device == dev and t.is_contiguous()):
+        return t.data_ptr()
+    return _ptr(t, name, dtype, shape, dev)  # a subclass, or says what is wrong
 
 
 def _rows(t, name, dtype, lead, tail, dev):
@@ -795,13 +813,11 @@ def _rows(t, name, dtype, lead, tail, dev):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != lead + tail:
+    if t.shape != lead + tail:
         raise ValueError("%s must have shape %s, got %s"
-                         % (name, lead + tail, tuple(t.shape)))
+                         % (name, tuple(lead + tail), tuple(t.shape)))
     if t.device != dev:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
-    if dev.type != "cuda":
-        raise ValueError("%s must be a device (HIP) tensor" % name)
     row = 1
     for n in tail:
         row *= n
@@ -887,42 +903,50 @@ class _Linattn:
 
     __slots__ = ("dev", "act", "lead", "tokens", "nseq", "heads", "qk_heads",
                  "dk", "dv", "code", "qkv", "g", "flags", "scale", "h0", "cu",
-                 "states")
+                 "states", "qk", "vo")
 
     def __init__(self, q, k, v, g, scale, h0, cu_seqlens, step=False):
         if not (isinstance(q, torch.Tensor) and isinstance(v, torch.Tensor)):
             raise TypeError("q and v must be torch.Tensors")
         flat = step or cu_seqlens is not None
-        if q.dim() != (3 if flat else 4) or v.dim() != q.dim():
+        qs, vs = q.shape, v.shape
+        if len(qs) != (3 if flat else 4) or len(vs) != len(qs):
             raise ValueError("q, k, v must be %s" % (
                 "(batch, heads, dim)" if step else "(tokens, heads, dim) with cu_seqlens"
                 if flat else "(batch, seqlen, heads, dim)"))
-        self.dev, self.act = q.device, q.dtype
-        self.code = _code(q.dtype)
-        lead = self.lead = tuple(v.shape[:-2])
-        self.heads, self.dv = v.shape[-2:]
-        self.qk_heads, self.dk = q.shape[-2:]
+        dev, act = self.dev, self.act = q.device, q.dtype
+        self.code = _code(act)
+        if dev.type != "cuda":
+            raise ValueError("q must be a device (HIP) tensor")
+        lead, vo = vs[:-2], vs[-2:]
+        qk = qs[-2:]
+        self.lead, self.qk, self.vo = lead, qk, vo
+        heads, self.dv = vo
+        self.heads = heads
+        self.qk_heads, self.dk = qk
         self.tokens = lead[0] if flat else lead[0] * lead[1]
-        dev, act = self.dev, self.act
-        qk = (self.qk_heads, self.dk)
         self.qkv = (_rows(q, "q", act, lead, qk, dev) + _rows(k, "k", act, lead, qk, dev) +
-                    _rows(v, "v", act, lead, (self.heads, self.dv), dev))
+                    _rows(v, "v", act, lead, vo, dev))
         self.flags = 0
-        if g is not None and g.dim() == 1:
+        if g is None:
+            self.g = None
+        elif g.dim() == 1:
             self.flags = SSM_FLAG_HEAD_DECAY
-            self.g = _ptr(g, "g", torch.float32, (self.heads,), dev)
+            self.g = _dense(g, "g", torch.float32, (heads,), dev)
         else:
-            self.g = _ptr(g, "g", torch.float32, lead + (self.heads,), dev)
+            self.g = _dense(g, "g", torch.float32, lead + (heads,), dev)
         self.scale = self.dk ** -0.5 if scale is None else float(scale)
         self.cu = None
-        self.nseq = 0 if step else lead[0]
-        if not step and cu_seqlens is not None:
+        if step:
+            return
+        self.nseq = lead[0]
+        if cu_seqlens is not None:
             if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
                 raise ValueError("cu_seqlens must be (sequences + 1,)")
             self.nseq = cu_seqlens.shape[0] - 1
-            self.cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (self.nseq + 1,), dev)
-        self.states = (self.nseq, self.heads, self.dk, self.dv)
-        self.h0 = _ptr(h0, "h0", torch.float32, self.states, dev)
+            self.cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (self.nseq + 1,), dev)
+        self.states = (self.nseq, heads, self.dk, self.dv)
+        self.h0 = _dense(h0, "h0", torch.float32, self.states, dev)
 
 
 @_on_device
@@ -944,7 +968,7 @@ def ssm_linattn_fwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     a = _Linattn(q, k, v, g, scale, h0, cu_seqlens)
     lib = load_library()
     if o is None:
-        o = torch.empty(a.lead + (a.heads, a.dv), dtype=a.act, device=a.dev)
+        o = torch.empty(a.lead + a.vo, dtype=a.act, device=a.dev)
     if not return_final_state:
         h_final = None
     elif h_final is None:
@@ -954,10 +978,10 @@ def ssm_linattn_fwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     keep, ws, ws_bytes = _scratch(workspace, need, a.dev)
     _check(lib.ssm_linattn_fwd(
         *a.qkv, a.g, a.flags, a.scale, a.h0, a.cu,
-        _ptr(o, "o", a.act, a.lead + (a.heads, a.dv), a.dev),
-        _ptr(h_final, "h_final", torch.float32, a.states, a.dev),
+        _dense(o, "o", a.act, a.lead + a.vo, a.dev),
+        _dense(h_final, "h_final", torch.float32, a.states, a.dev),
         a.tokens, a.nseq, a.heads, a.qk_heads, a.dk, a.dv, a.code, ws, ws_bytes,
-        _stream_handle(a.dev, stream)))
+        _raw_stream(a.dev, stream)))
     return o, h_final
 
 
@@ -975,9 +999,9 @@ def ssm_linattn_bwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     a = _Linattn(q, k, v, g, scale, h0, cu_seqlens)
     lib = load_library()
     f32 = torch.float32
-    shapes = {"dq": (a.lead + (a.qk_heads, a.dk), a.act),
-              "dk": (a.lead + (a.qk_heads, a.dk), a.act),
-              "dv": (a.lead + (a.heads, a.dv), a.act)}
+    shapes = {"dq": (a.lead + a.qk, a.act),
+              "dk": (a.lead + a.qk, a.act),
+              "dv": (a.lead + a.vo, a.act)}
     if g is not None and want_dg:
         shapes["dg"] = (tuple(g.shape), f32)
     if want_dh0:
@@ -987,18 +1011,18 @@ def ssm_linattn_bwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     for name, (shape, dtype) in shapes.items():
         if name not in out:
             out[name] = torch.empty(shape, dtype=dtype, device=a.dev)
-        p[name] = _ptr(out[name], name, dtype, shape, a.dev)
+        p[name] = _dense(out[name], name, dtype, shape, a.dev)
     kind = 0 if "dg" not in shapes else 2 if a.flags else 1
     need = _size(lib.ssm_linattn_bwd_workspace_size, a.tokens, a.nseq, a.cu is not None,
                  a.heads, a.qk_heads, a.dk, a.dv, a.code, kind)
     keep, ws, ws_bytes = _scratch(workspace, need, a.dev)
     _check(lib.ssm_linattn_bwd(
         *a.qkv, a.g, a.flags, a.scale, a.h0, a.cu,
-        _ptr(do, "do", a.act, a.lead + (a.heads, a.dv), a.dev),
-        _ptr(dh_final, "dh_final", f32, a.states, a.dev),
+        _dense(do, "do", a.act, a.lead + a.vo, a.dev),
+        _dense(dh_final, "dh_final", f32, a.states, a.dev),
         p["dq"], p["dk"], p["dv"], p.get("dg"), p.get("dh0"),
         a.tokens, a.nseq, a.heads, a.qk_heads, a.dk, a.dv, a.code, ws, ws_bytes,
-        _stream_handle(a.dev, stream)))
+        _raw_stream(a.dev, stream)))
     return {name: out[name] for name in shapes}
 
 
@@ -1016,14 +1040,14 @@ def ssm_linattn_step(state, q, k, v, g=None, scale=None, slots=None, o=None,
         raise ValueError("state must be (nslots, heads, qk_dim, v_dim)")
     nslots = state.shape[0]
     if o is None:
-        o = torch.empty(a.lead + (a.heads, a.dv), dtype=a.act, device=a.dev)
+        o = torch.empty(a.lead + a.vo, dtype=a.act, device=a.dev)
     _check(load_library().ssm_linattn_step(
-        _ptr(state, "state", torch.float32, (nslots, a.heads, a.dk, a.dv), a.dev),
+        _dense(state, "state", torch.float32, (nslots, a.heads, a.dk, a.dv), a.dev),
         *a.qkv, a.g, a.flags, a.scale,
-        _ptr(slots, "slots", torch.int32, a.lead, a.dev),
-        _ptr(o, "o", a.act, a.lead + (a.heads, a.dv), a.dev),
+        _dense(slots, "slots", torch.int32, a.lead, a.dev),
+        _dense(o, "o", a.act, a.lead + a.vo, a.dev),
         a.tokens, nslots, a.heads, a.qk_heads, a.dk, a.dv, a.code,
-        _stream_handle(a.dev, stream)))
+        _raw_stream(a.dev, stream)))
     return o
 
 
@@ -1037,19 +1061,21 @@ def _norm_args(x, w_post, z, scale, residual, w_pre):
         raise TypeError("x must be a torch.Tensor (..., dim)")
     dev, act, f32 = x.device, x.dtype, torch.float32
     code = _code(act)
-    lead, dim = tuple(x.shape[:-1]), x.shape[-1]
+    lead, dim = x.shape[:-1], x.shape[-1]
     rows = 1
     for n in lead:
         rows *= n
     rdt = act if residual is None else residual.dtype
     rcode = _code(rdt)
+    if dev.type != "cuda":
+        raise ValueError("x must be a device (HIP) tensor")
 
     def side(t, name, dtype):
         return (None, 0) if t is None else _rows(t, name, dtype, lead, (dim,), dev)
 
-    args = (side(x, "x", act) + (_ptr(w_post, "w_post", f32, (dim,), dev),) +
-            side(z, "z", act) + (_ptr(scale, "scale", f32, (dim,), dev),) +
-            side(residual, "residual", rdt) + (_ptr(w_pre, "w_pre", f32, (dim,), dev),))
+    args = (side(x, "x", act) + (_dense(w_post, "w_post", f32, (dim,), dev),) +
+            side(z, "z", act) + (_dense(scale, "scale", f32, (dim,), dev),) +
+            side(residual, "residual", rdt) + (_dense(w_pre, "w_pre", f32, (dim,), dev),))
     return args, rows, dim, code, rcode, rdt
 
 
@@ -1072,8 +1098,8 @@ def ssm_block_norm_fwd(x, w_post=None, z=None, scale=None, residual=None,
     elif y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _check(load_library().ssm_block_norm_fwd(
-        *args, _ptr(r, "r", rdt, x.shape, x.device), _ptr(y, "y", x.dtype, x.shape, x.device),
-        rows, dim, groups, eps, code, rcode, _stream_handle(x.device, stream)))
+        *args, _dense(r, "r", rdt, x.shape, x.device), _dense(y, "y", x.dtype, x.shape, x.device),
+        rows, dim, groups, eps, code, rcode, _raw_stream(x.device, stream)))
     return r, y
 
 
@@ -1099,13 +1125,13 @@ def ssm_block_norm_bwd(x, w_post=None, z=None, scale=None, residual=None,
     for name, (shape, dtype) in shapes.items():
         if name not in out:
             out[name] = torch.empty(shape, dtype=dtype, device=dev)
-        p[name] = _ptr(out[name], name, dtype, shape, dev)
+        p[name] = _dense(out[name], name, dtype, shape, dev)
     lib = load_library()
     keep, ws, ws_bytes = _scratch(
         workspace, _size(lib.ssm_block_norm_bwd_workspace_size, rows, dim), dev)
     _check(lib.ssm_block_norm_bwd(
-        *args, _ptr(dr, "dr", rdt, x.shape, dev), _ptr(dy, "dy", act, x.shape, dev),
+        *args, _dense(dr, "dr", rdt, x.shape, dev), _dense(dy, "dy", act, x.shape, dev),
         p["dx"], p.get("dw_post"), p.get("dz"), p.get("dscale"), p.get("dresidual"),
         p.get("dw_pre"), rows, dim, groups, eps, code, rcode, ws, ws_bytes,
-        _stream_handle(dev, stream)))
+        _raw_stream(dev, stream)))
     return {name: out[name] for name in shapes}

@@ -22,6 +22,9 @@
 // columns in registers; a second kernel adds the workgroups' sums in a fixed
 // order.
 #include "ssm_block_norm.h"
+
+#include <type_traits>
+
 #include "ssm_device.h"
 
 namespace ssm {
@@ -36,39 +39,43 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // power of two of neighbouring lanes covers; any parts (through LDS).
 enum Parts { kRow = 0, kLanes = 1, kAny = 2 };
 
-// kN neighbouring elements from memory to fp32 and back (kN = 1, or pieces
-// of 8 (bf16) and 4 (fp32) that may be moved as a whole).
-template <int kN>
-__device__ __forceinline__ void get(const uint16_t *p, float (&v)[kN]) {
-  if constexpr (kN == 8) {
-    const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+// kN neighbouring elements as they are in memory (kN = 1, or pieces of 8
+// (bf16) and 4 (fp32) that are moved as a whole), and in fp32.
+template <typename T, int kN>
+struct Raw {
+  static constexpr int kWords = kN * sizeof(T) < 4 ? 1 : kN * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
-    }
-  } else if constexpr (kN == 4) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    v[0] = bf16_lo(w.x);
-    v[1] = bf16_hi(w.x);
-    v[2] = bf16_lo(w.y);
-    v[3] = bf16_hi(w.y);
-  } else {
-    v[0] = to_f32<uint16_t>(p[0]);
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
-}
-template <int kN>
-__device__ __forceinline__ void get(const float *p, float (&v)[kN]) {
-  if constexpr (kN == 1) {
-    v[0] = p[0];
-  } else {
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (kN == 1 && sizeof(T) == 2) {
+      w[0] = p[0];
+    } else if constexpr (kN == 1) {
+      w[0] = __float_as_uint(p[0]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kN / 4; ++i) {
-      const f32x4 w = reinterpret_cast<const f32x4 *>(p)[i];
+      for (int i = 0; i < kWords / 4; ++i) {
+        const u32x4 x = reinterpret_cast<const u32x4 *>(p)[i];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * i + e] = w[e];
+        for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
+      }
     }
   }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 2)
+      return e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    else
+      return __uint_as_float(w[e]);
+  }
+};
+template <int kN, typename T>
+__device__ __forceinline__ void get(const T *p, float (&v)[kN]) {
+  Raw<T, kN> r;
+  r.load(p);
+#pragma unroll
+  for (int e = 0; e < kN; ++e) v[e] = r[e];
 }
 template <int kN>
 __device__ __forceinline__ void put(uint16_t *p, const float (&v)[kN]) {
@@ -77,11 +84,6 @@ __device__ __forceinline__ void put(uint16_t *p, const float (&v)[kN]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<u32x4 *>(p) = w;
-  } else if constexpr (kN == 4) {
-    uint2 w;
-    w.x = pack_bf16x2(v[0], v[1]);
-    w.y = pack_bf16x2(v[2], v[3]);
-    *reinterpret_cast<uint2 *>(p) = w;
   } else {
     p[0] = from_f32<uint16_t>(v[0]);
   }
@@ -104,8 +106,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Sums over the workgroup (up to 16 waves), the same in every thread.  `buf`
-// is free to be written again after the next call's barrier, so calls
-// alternate between two.
+// may be written again once every thread has passed a later barrier, so a
+// loop's calls take turns between two.
 template <int kK>
 __device__ __forceinline__ void block_sums(float (&v)[kK], float (*buf)[kK]) {
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
@@ -251,9 +253,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p) {
 }
 
 template <typename T, typename R, int kN, int kP, int kParts, int kBound>
-__global__ __launch_bounds__(kBound) void norm_bwd_kernel(NormArgs p) {
-  __shared__ float Buf1[2][16][1];
-  __shared__ float Buf2[16][2];
+__global__ __launch_bounds__(kBound, sizeof(R) == 2 && kN == 8 ? 3 : 1) void norm_bwd_kernel(NormArgs p) {
+  __shared__ float Buf1[16][1];
+  __shared__ float Buf2[4][16][2];
   extern __shared__ float Dyn[];
   const int tid = threadIdx.x;
   const int pieces = p.dim / kN;
@@ -274,64 +276,90 @@ __global__ __launch_bounds__(kBound) void norm_bwd_kernel(NormArgs p) {
       if (p.w_pre) get<kN>(p.w_pre + q * kN, wpre[i]);
     }
   }
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T *x = static_cast<const T *>(p.x) + row * p.x_stride;
-    const T *z = p.z ? static_cast<const T *>(p.z) + row * p.z_stride : nullptr;
-    const R *res = p.residual ? static_cast<const R *>(p.residual) + row * p.r_stride : nullptr;
-    float xx[kP][kN], zz[kP][kN], rr[kP][kN], dd[kP][kN], yy[kP][kN];
+  // a row's inputs as they are in memory: the next row's are asked for while
+  // this one's are worked on
+  Raw<T, kN> rx[kP], rz[kP], ry[kP];
+  Raw<R, kN> rres[kP], rdr[kP];
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
       const int q = tid + i * blockDim.x;
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        xx[i][e] = zz[i][e] = rr[i][e] = dd[i][e] = yy[i][e] = 0.0f;
       if (q < pieces) {
-        get<kN>(x + q * kN, xx[i]);
-        if (z) get<kN>(z + q * kN, zz[i]);
-        if (res) get<kN>(res + q * kN, rr[i]);
-        if (p.dr) get<kN>(static_cast<const R *>(p.dr) + row * p.dim + q * kN, dd[i]);
-        if (p.dy) get<kN>(static_cast<const T *>(p.dy) + row * p.dim + q * kN, yy[i]);
+        rx[i].load(static_cast<const T *>(p.x) + row * p.x_stride + q * kN);
+        if (p.z) rz[i].load(static_cast<const T *>(p.z) + row * p.z_stride + q * kN);
+        if (p.residual)
+          rres[i].load(static_cast<const R *>(p.residual) + row * p.r_stride + q * kN);
+        if (p.dy) ry[i].load(static_cast<const T *>(p.dy) + row * p.dim + q * kN);
+        if (p.dr) rdr[i].load(static_cast<const R *>(p.dr) + row * p.dim + q * kN);
       }
     }
-    float s[kP];
-    if (p.w_post) {
+  };
+  auto squares = [&](float (&s)[kP]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        s[i] = 0.0f;
+    for (int i = 0; i < kP; ++i) {
+      s[i] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kN; ++e) s[i] = fmaf(xx[i][e], xx[i][e], s[i]);
-      }
-      part_means<kParts, kP, kN>(s, p, pieces, Buf1[0], elems, sums);
-#pragma unroll
-      for (int i = 0; i < kP; ++i) s[i] = 1.0f / sqrtf(s[i] + p.eps);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kP; ++i) s[i] = 1.0f;
+      for (int e = 0; e < kN; ++e) s[i] = fmaf(rx[i][e], rx[i][e], s[i]);
     }
-    // r, and dy w_pre in yy's place
+  };
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    rx[i].zero();
+    rz[i].zero();
+    rres[i].zero();
+    ry[i].zero();
+    rdr[i].zero();
+  }
+  float s[kP];  // x's means of squares, of this row and, at its end, of the next
+  load(blockIdx.x);
+  if (p.w_post) {
+    squares(s);
+    part_means<kParts, kP, kN>(s, p, pieces, Buf1, elems, sums);
+  }
+  int turn = 0;  // of the buffers: a row's sums may not meet the last row's readers
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    // x, z and dy stay as they are in memory (16-bit ones take half the registers)
+    Raw<T, kN> cx[kP], cz[kP], cy[kP];
+    float rr[kP][kN], dd[kP][kN];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      s[i] = p.w_post ? 1.0f / sqrtf(s[i] + p.eps) : 1.0f;
+      cx[i] = rx[i];
+      cz[i] = rz[i];
+      cy[i] = ry[i];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        rr[i][e] = rres[i][e];
+        dd[i][e] = rdr[i][e];
+      }
+    }
+    const bool more = row + gridDim.x < p.rows;
+    if (more) load(row + gridDim.x);
+    // r in rr
     float v[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kP; ++i)
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
-        const float g = z ? silu_f(zz[i][e]) : 1.0f;
-        rr[i][e] = fmaf(xx[i][e] * s[i] * wpost[i][e] * g, wscale[i][e], rr[i][e]);
+        const float g = p.z ? silu_f(cz[i][e]) : 1.0f;
+        rr[i][e] = fmaf(cx[i][e] * s[i] * wpost[i][e] * g, wscale[i][e], rr[i][e]);
         v[0] = fmaf(rr[i][e], rr[i][e], v[0]);
-        v[1] = fmaf(yy[i][e] * wpre[i][e], rr[i][e], v[1]);
+        v[1] = fmaf(cy[i][e] * wpre[i][e], rr[i][e], v[1]);
       }
     if (p.dy) {
-      block_sums<2>(v, Buf2);
+      block_sums<2>(v, Buf2[turn]);
       const float rho = 1.0f / sqrtf(v[0] / static_cast<float>(p.dim) + p.eps);
       const float m = v[1] / static_cast<float>(p.dim) * rho * rho;
 #pragma unroll
-      for (int i = 0; i < kP; ++i)
+      for (int i = 0; i < kP; ++i) {
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-          gpre[i][e] = fmaf(yy[i][e] * rho, rr[i][e], gpre[i][e]);
-          dd[i][e] = fmaf(rho, fmaf(-m, rr[i][e], yy[i][e] * wpre[i][e]), dd[i][e]);
+          gpre[i][e] = fmaf(cy[i][e] * rho, rr[i][e], gpre[i][e]);
+          dd[i][e] = fmaf(rho, fmaf(-m, rr[i][e], cy[i][e] * wpre[i][e]), dd[i][e]);
         }
+      }
     }
-    // dd: the gradient of r.  rr: h w_post; yy: dz
+    // dd: the gradient of r.  rr becomes h w_post
     float t[kP];
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
@@ -339,21 +367,45 @@ __global__ __launch_bounds__(kBound) void norm_bwd_kernel(NormArgs p) {
       t[i] = 0.0f;
       if (q < pieces && p.dresidual)
         put<kN>(static_cast<R *>(p.dresidual) + row * p.dim + q * kN, dd[i]);
+      float dz[kN];
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
-        const float g = z ? silu_f(zz[i][e]) : 1.0f;
-        const float u = xx[i][e] * s[i], n = u * wpost[i][e];
+        // silu(z) = z sg, its slope sg (1 + z (1 - sg))
+        const float z = cz[i][e], sg = sigmoid_f(z);
+        const float g = p.z ? z * sg : 1.0f;
+        const float u = cx[i][e] * s[i], n = u * wpost[i][e];
         gscale[i][e] = fmaf(dd[i][e], n * g, gscale[i][e]);
-        yy[i][e] = z ? dd[i][e] * n * wscale[i][e] * dsilu_f(zz[i][e]) : 0.0f;
+        dz[e] = dd[i][e] * n * wscale[i][e] * sg * fmaf(z, 1.0f - sg, 1.0f);
         const float h = dd[i][e] * g * wscale[i][e];
         gpost[i][e] = fmaf(h, u, gpost[i][e]);
         rr[i][e] = h * wpost[i][e];
-        t[i] = fmaf(rr[i][e], xx[i][e], t[i]);
+        t[i] = fmaf(rr[i][e], cx[i][e], t[i]);
       }
-      if (q < pieces && p.dz) put<kN>(static_cast<T *>(p.dz) + row * p.dim + q * kN, yy[i]);
+      if (q < pieces && p.dz) put<kN>(static_cast<T *>(p.dz) + row * p.dim + q * kN, dz);
     }
+    float next[kP];
     if (p.w_post) {
-      part_means<kParts, kP, kN>(t, p, pieces, Buf1[1], elems, sums);
+      // the mean of this row's h w_post x, and of the next row's x^2, by one
+      // reduction where the part is the row
+      if (more) squares(next);
+      if constexpr (kParts == kRow) {
+        float w[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          w[0] += t[i];
+          w[1] += more ? next[i] : 0.0f;
+        }
+        block_sums<2>(w, Buf2[2 + turn]);
+        const float inv = 1.0f / static_cast<float>(p.dim);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          t[i] = w[0] * inv;
+          next[i] = w[1] * inv;
+        }
+      } else {
+        part_means<kParts, kP, kN>(t, p, pieces, Buf1, elems, sums);
+        if (more) part_means<kParts, kP, kN>(next, p, pieces, Buf1, elems, sums);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
@@ -362,14 +414,13 @@ __global__ __launch_bounds__(kBound) void norm_bwd_kernel(NormArgs p) {
         if (p.w_post) {
           const float m = t[i] * s[i] * s[i];
 #pragma unroll
-          for (int e = 0; e < kN; ++e) rr[i][e] = s[i] * fmaf(-m, xx[i][e], rr[i][e]);
+          for (int e = 0; e < kN; ++e) rr[i][e] = s[i] * fmaf(-m, cx[i][e], rr[i][e]);
         }
         put<kN>(static_cast<T *>(p.dx) + row * p.dim + q * kN, rr[i]);
       }
+      s[i] = next[i];
     }
-    // one wave needs no barrier in block_sums; more waves pass one between
-    // any two uses of the same buffer only if every buffer is used each row
-    __syncthreads();
+    turn ^= 1;
   }
   float *part = p.parts + static_cast<int64_t>(blockIdx.x) * 3 * p.dim;
 #pragma unroll
@@ -412,8 +463,9 @@ __global__ __launch_bounds__(1024) void norm_parts_kernel(NormArgs p) {
   }
 }
 
-// Pieces a thread holds (1, 2, 4, 8 or 16) and threads of a workgroup: with
-// whole pieces one each up to 1024 threads; single elements, up to 16 each.
+// Pieces a thread holds (1, 2, 4, 8 or 16) and threads of a workgroup: whole
+// pieces one each up to 1024 threads, single elements up to 512 threads, then
+// more each.
 struct Shape {
   int per, threads;
 };
@@ -421,51 +473,56 @@ Shape shape_of(int dim, int n) {
   const int pieces = dim / n;
   const int most_per = n > 1 ? 4 : 16;
   int per = 1;
-  while (per < most_per && pieces > per * (n > 1 ? 1024 : 256)) per *= 2;
+  while (per < most_per && pieces > per * (n > 1 ? 1024 : 512)) per *= 2;
   return {per, ((pieces + per - 1) / per + 63) / 64 * 64};
 }
 
 int piece_of(bool bf16, bool vec) { return vec ? (bf16 ? 8 : 4) : 1; }
 
-template <typename T, typename R, int kN, int kP>
-int launch_norm_p(const NormArgs &a, bool backward, int threads, hipStream_t s) {
+template <typename T, typename R, int kN, int kP, bool kBack>
+int launch_norm_p(const NormArgs &a, int threads, hipStream_t s) {
   const int width = a.dim / a.groups, lanes = width / kN;
   const bool neighbours =
       width % kN == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0 && lanes > 0;
   const int parts = !a.w_post || a.groups == 1 ? kRow : neighbours ? kLanes : kAny;
-  const unsigned grid = static_cast<unsigned>(backward ? a.nparts : a.rows);
+  const unsigned grid = static_cast<unsigned>(kBack ? a.nparts : a.rows);
   const size_t dyn = parts == kAny ? (a.dim / kN + a.groups) * sizeof(float) : 0;
-  auto go = [&](auto fwd, auto bwd) {
-    if (backward)
-      hipLaunchKernelGGL(bwd, dim3(grid), dim3(threads), dyn, s, a);
-    else
-      hipLaunchKernelGGL(fwd, dim3(grid), dim3(threads), dyn, s, a);
+  auto go = [&](auto kind) {
+    constexpr int kKind = decltype(kind)::value;
+    auto run = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), dyn, s, a);
+      return static_cast<int>(hipGetLastError());
+    };
+    if constexpr (!kBack) {
+      return run(norm_fwd_kernel<T, R, kN, kP, kKind>);
+    } else {
+      // it holds up to 190 values a thread: 256, 168 or 128 registers
+      return threads <= 512   ? run(norm_bwd_kernel<T, R, kN, kP, kKind, 512>)
+             : threads <= 768 ? run(norm_bwd_kernel<T, R, kN, kP, kKind, 768>)
+                              : run(norm_bwd_kernel<T, R, kN, kP, kKind, 1024>);
+    }
   };
-  // up to 512 threads leave 256 registers a thread
-  const bool half = threads <= 512;
-  if (parts == kRow)
-    go(norm_fwd_kernel<T, R, kN, kP, kRow>, half ? norm_bwd_kernel<T, R, kN, kP, kRow, 512>
-                                                 : norm_bwd_kernel<T, R, kN, kP, kRow, 1024>);
-  else if (parts == kLanes)
-    go(norm_fwd_kernel<T, R, kN, kP, kLanes>, half ? norm_bwd_kernel<T, R, kN, kP, kLanes, 512>
-                                                   : norm_bwd_kernel<T, R, kN, kP, kLanes, 1024>);
-  else
-    go(norm_fwd_kernel<T, R, kN, kP, kAny>, half ? norm_bwd_kernel<T, R, kN, kP, kAny, 512>
-                                                 : norm_bwd_kernel<T, R, kN, kP, kAny, 1024>);
-  return static_cast<int>(hipGetLastError());
+  if (parts == kRow) return go(std::integral_constant<int, kRow>{});
+  if (parts == kLanes) return go(std::integral_constant<int, kLanes>{});
+  return go(std::integral_constant<int, kAny>{});
 }
 
-template <typename T, typename R, int kN>
-int launch_norm_n(const NormArgs &a, bool backward, hipStream_t s) {
+template <typename T, typename R, int kN, bool kBack>
+int launch_norm_n(const NormArgs &a, hipStream_t s) {
   const Shape sh = shape_of(a.dim, kN);
-  if (sh.per == 1) return launch_norm_p<T, R, kN, 1>(a, backward, sh.threads, s);
-  if (sh.per == 2) return launch_norm_p<T, R, kN, 2>(a, backward, sh.threads, s);
-  if (sh.per == 4) return launch_norm_p<T, R, kN, 4>(a, backward, sh.threads, s);
+  if (sh.per == 1) return launch_norm_p<T, R, kN, 1, kBack>(a, sh.threads, s);
+  if (sh.per == 2) return launch_norm_p<T, R, kN, 2, kBack>(a, sh.threads, s);
+  if (sh.per == 4) return launch_norm_p<T, R, kN, 4, kBack>(a, sh.threads, s);
   if constexpr (kN == 1) {
-    if (sh.per == 8) return launch_norm_p<T, R, kN, 8>(a, backward, sh.threads, s);
-    return launch_norm_p<T, R, kN, 16>(a, backward, sh.threads, s);
+    if (sh.per == 8) return launch_norm_p<T, R, kN, 8, kBack>(a, sh.threads, s);
+    return launch_norm_p<T, R, kN, 16, kBack>(a, sh.threads, s);
   }
   return static_cast<int>(hipErrorInvalidValue);
+}
+
+template <typename T, typename R>
+int launch_norm_1(const NormArgs &a, bool backward, hipStream_t s) {
+  return backward ? launch_norm_n<T, R, 1, true>(a, s) : launch_norm_n<T, R, 1, false>(a, s);
 }
 
 int launch_norm(const NormArgs &a, bool backward, bool bf16, hipStream_t s) {
@@ -473,13 +530,16 @@ int launch_norm(const NormArgs &a, bool backward, bool bf16, hipStream_t s) {
   const int n = piece_of(bf16, a.vec && (a.dim / a.groups) % (bf16 ? 8 : 4) == 0);
   if (bf16) {
     if (a.wide)
-      return n > 1 ? launch_norm_n<uint16_t, float, 8>(a, backward, s)
-                   : launch_norm_n<uint16_t, float, 1>(a, backward, s);
-    return n > 1 ? launch_norm_n<uint16_t, uint16_t, 8>(a, backward, s)
-                 : launch_norm_n<uint16_t, uint16_t, 1>(a, backward, s);
+      return n > 1 ? (backward ? launch_norm_n<uint16_t, float, 8, true>(a, s)
+                               : launch_norm_n<uint16_t, float, 8, false>(a, s))
+                   : launch_norm_1<uint16_t, float>(a, backward, s);
+    return n > 1 ? (backward ? launch_norm_n<uint16_t, uint16_t, 8, true>(a, s)
+                             : launch_norm_n<uint16_t, uint16_t, 8, false>(a, s))
+                 : launch_norm_1<uint16_t, uint16_t>(a, backward, s);
   }
-  return n > 1 ? launch_norm_n<float, float, 4>(a, backward, s)
-               : launch_norm_n<float, float, 1>(a, backward, s);
+  return n > 1 ? (backward ? launch_norm_n<float, float, 4, true>(a, s)
+                           : launch_norm_n<float, float, 4, false>(a, s))
+               : launch_norm_1<float, float>(a, backward, s);
 }
 
 }  // namespace

@@ -113,13 +113,16 @@ int check_sizes(const Sizes &z) {
 // and column slices.  Where they fill the GPU's places for workgroups less
 // than half, the sequences are cut into as many segments of at least
 // kMinSegment tokens as fill them once, for the price of a pass over k and v
-// (and q and do) that forms the states between them: that pass and the chain
-// cost about half of the output pass (measured, 8192 tokens, 80 heads of 64
-// on states of 128: 50 + 14 of 175 us; uncut 290 us).  A CU holds two
-// workgroups, or one of heads over 128 wide.  The gradient of the decay is
-// summed over one segment in 64 bits from an inner product at its end, so
-// with it segments have at most kMaxGradSegment tokens.
-constexpr int64_t kPlaces = 512, kMinSegment = 256, kMaxGradSegment = 1024;
+// (and q and do) that forms the states between them.  A CU holds two
+// workgroups, or one of heads over 128 wide.  Measured with 256, 512 and 1024
+// places: prompts of 2 x 4096 tokens, 80 heads of 64 on states of 128, 170,
+// 150 and 172 us; one of 65536 tokens, 8 heads of 128, 241, 224 and 258 us;
+// with segments of at least 128, 256 and 512 tokens: 7 short fp32 prompts
+// 103, 176 and 333 us, a training step of 2 x 2048 tokens 181, 173 and 186 us.
+// The gradient of the decay is summed over one segment in 64 bits from an
+// inner product at its end, so with it segments have at most
+// kMaxGradSegment tokens.
+constexpr int64_t kPlaces = 512, kMinSegment = 128, kMaxGradSegment = 1024;
 
 // workgroups that a sequence's chunk pass has
 int64_t groups_of(const Sizes &z, bool backward) {
