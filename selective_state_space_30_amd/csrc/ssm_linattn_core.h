@@ -112,6 +112,15 @@ __device__ __forceinline__ bf16x8 to_frag(f32x8 v, bf16x8) {
 }
 __device__ __forceinline__ f32x8 to_frag(f32x8 v, f32x8) { return v; }
 
+// What is left of v behind hi, as two more bf16 values: with hi 24 bits, those
+// of fp32.
+__device__ __forceinline__ void split(f32x8 v, bf16x8 hi, bf16x8 *mid, bf16x8 *lo) {
+  const f32x8 rest = v - __builtin_convertvector(hi, f32x8);
+  *mid = to_frag(rest, bf16x8{});
+  *lo = to_frag(rest - __builtin_convertvector(*mid, f32x8), bf16x8{});
+}
+__device__ __forceinline__ void split(f32x8, f32x8, f32x8 *, f32x8 *) {}
+
 // The same value, unknown to the compiler: what is computed from it is made
 // anew where it is used, not kept in registers from chunk to chunk.
 __device__ __forceinline__ int anew(int x) {
@@ -386,9 +395,11 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t v, int off, f32x4 
 //
 // bf16 roundings: the weighted pair products and the state where it is an
 // operand, once each (2^-8 of each term, as the output's own rounding); what
-// goes into the state enters as a pair of bf16 values (2^-16), since the
-// state is returned in 32 bits and is carried over the sequence; likewise
-// the state itself where dot products in 32 bits are wanted (kLinOutDot).
+// goes into the state enters as three bf16 values, 24 bits of it, since the
+// state is returned in 32 bits and is carried over the sequence (with two,
+// 16 bits, the final state and the decay's gradient were off by 2.6e-6 and
+// 1e-5 in the norm); likewise the state itself where dot products in 32 bits
+// are wanted (kLinOutDot).
 // The sums of decays, at most 2^14 in size, are subtracted in 32 bits for
 // the weights of the pairs in bf16 (2^-10 at the largest sizes, a quarter of
 // the rounding the product then has), else in 64.
@@ -630,14 +641,16 @@ __device__ __forceinline__ void core(const LinCore &p, unsigned block,
         __builtin_amdgcn_sched_barrier(0);
         const f32x8 s = __builtin_shufflevector(S[2 * ks], S[2 * ks + 1], 0, 1, 2, 3, 4, 5, 6, 7);
         const Frag hi = to_frag(s, Frag{});
-        Frag lo;
-        if constexpr (kDot && kBf16)
-          lo = to_frag(s - __builtin_convertvector(hi, f32x8), Frag{});
+        Frag mid, lo;
+        if constexpr (kDot && kBf16) split(s, hi, &mid, &lo);
 #pragma unroll
         for (int ti = 0; ti < kNT; ++ti) {
           const Frag b = two_halves(&Qs[(16 * ti + li) * kRowQ + 32 * ks + 4 * lq]);
           O[ti] = mma(hi, b, O[ti]);
-          if constexpr (kDot && kBf16) O[ti] = mma(lo, b, O[ti]);
+          if constexpr (kDot && kBf16) {
+            O[ti] = mma(mid, b, O[ti]);
+            O[ti] = mma(lo, b, O[ti]);
+          }
         }
       }
 #pragma unroll
@@ -672,14 +685,17 @@ __device__ __forceinline__ void core(const LinCore &p, unsigned block,
       vf[ts] = frag_by_column<kRowV>(Vs[mine], 32 * ts, jw, fresh);
       const f32x8 x = __builtin_convertvector(vf[ts], f32x8) * w;
       const Frag hi = to_frag(x, Frag{});
-      Frag lo;
-      if constexpr (kBf16) lo = to_frag(x - __builtin_convertvector(hi, f32x8), Frag{});
+      Frag mid, lo;
+      if constexpr (kBf16) split(x, hi, &mid, &lo);
 #pragma unroll
       for (int it = 0; it < kIT; ++it) {
         if (it % 4 == 0) __builtin_amdgcn_sched_barrier(0);
         const Frag a = frag_by_column<kRowK>(Ks, 32 * ts, 16 * it, fresh);
         S[it] = mma(a, hi, S[it]);
-        if constexpr (kBf16) S[it] = mma(a, lo, S[it]);
+        if constexpr (kBf16) {
+          S[it] = mma(a, mid, S[it]);
+          S[it] = mma(a, lo, S[it]);
+        }
       }
     }
 
