@@ -167,21 +167,41 @@ __device__ __forceinline__ void all_rows(const LinPlan &p, int64_t *begin, int64
   *end = e;
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void linattn_head_sum_kernel(const float *in, T *out,
-                                                               LinPlan plan, int div, int d) {
+// Sums of `div` consecutive heads' fp32 rows, of dq's and dk's partial
+// results at once (blockIdx.y); 4 neighbouring elements a thread where the
+// head size allows, 8 heads' loads in flight (24 heads to one of 128: 61 us
+// for both with single elements and one load after the other).
+template <typename T, int kN>
+__global__ __launch_bounds__(256) void linattn_head_sum_kernel(const float *in0, const float *in1,
+                                                               T *out0, T *out1, LinPlan plan,
+                                                               int div, int d) {
+  const float *in = blockIdx.y ? in1 : in0;
+  T *out = blockIdx.y ? out1 : out0;
   int64_t begin, end;
   all_rows(plan, &begin, &end);
-  const int64_t row = static_cast<int64_t>(plan.heads / div) * d;  // of out
-  const int64_t stop = end * row, step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t i = begin * row + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < stop;
-       i += step) {
-    const int64_t t = i / row, c = i % row;
-    const float *s = in + t * plan.heads * d + c / d * div * d + c % d;
-    float acc = 0.0f;
-    for (int k = 0; k < div; ++k) acc += s[static_cast<int64_t>(k) * d];
-    out[i] = from_f32<T>(acc);
-  }
+  const unsigned row = static_cast<unsigned>(plan.heads / div) * d / kN;  // pieces of an out row
+  const unsigned per_head = static_cast<unsigned>(d) / kN;
+  for (int64_t t = begin + blockIdx.x; t < end; t += gridDim.x)
+    for (unsigned c = threadIdx.x; c < row; c += 256) {
+      const float *s = in + t * plan.heads * d +
+                       static_cast<int64_t>(c / per_head) * div * d + c % per_head * kN;
+      float acc[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
+#pragma unroll 8
+      for (int k = 0; k < div; ++k) {
+        if constexpr (kN == 4) {
+          const f32x4 x = *reinterpret_cast<const f32x4 *>(s + k * d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += x[e];
+        } else {
+          acc[0] += s[k * d];
+        }
+      }
+      T *o = out + (t * row + c) * kN;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) o[e] = from_f32<T>(acc[e]);
+    }
 }
 
 __global__ __launch_bounds__(1024) void linattn_token_sum_kernel(const float *in, float *out,
@@ -326,18 +346,23 @@ int launch_linattn_decay_grad(const LinDecayGrad &a, void *stream) {
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_linattn_head_sum(const float *in, void *out, const LinPlan &plan, int div, int d,
-                            bool bf16, void *stream) {
-  const int64_t n = plan.tokens * (plan.heads / div) * d, most = 1 << 16;
-  const dim3 grid(static_cast<unsigned>((n + 255) / 256 < most ? (n + 255) / 256 : most));
+int launch_linattn_head_sum(const float *in0, const float *in1, void *out0, void *out1,
+                            const LinPlan &plan, int div, int d, bool bf16, void *stream) {
+  const int64_t most = 1 << 16;
+  const dim3 grid(static_cast<unsigned>(plan.tokens < most ? plan.tokens : most), 2);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (bf16)
-    hipLaunchKernelGGL(linattn_head_sum_kernel<uint16_t>, grid, dim3(256), 0, s, in,
-                       static_cast<uint16_t *>(out), plan, div, d);
-  else
-    hipLaunchKernelGGL(linattn_head_sum_kernel<float>, grid, dim3(256), 0, s, in,
-                       static_cast<float *>(out), plan, div, d);
-  return static_cast<int>(hipGetLastError());
+  auto go = [&](auto kernel, auto *o0, auto *o1) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, in0, in1, o0, o1, plan, div, d);
+    return static_cast<int>(hipGetLastError());
+  };
+  if (bf16) {
+    uint16_t *o0 = static_cast<uint16_t *>(out0), *o1 = static_cast<uint16_t *>(out1);
+    return d % 4 == 0 ? go(linattn_head_sum_kernel<uint16_t, 4>, o0, o1)
+                      : go(linattn_head_sum_kernel<uint16_t, 1>, o0, o1);
+  }
+  float *o0 = static_cast<float *>(out0), *o1 = static_cast<float *>(out1);
+  return d % 4 == 0 ? go(linattn_head_sum_kernel<float, 4>, o0, o1)
+                    : go(linattn_head_sum_kernel<float, 1>, o0, o1);
 }
 
 int launch_linattn_token_sum(const float *in, float *out, const LinPlan &plan, void *stream) {

@@ -544,8 +544,8 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   if (err != 0) return hip_failed(err);
   if (shared && tokens > 0) {
     const int n = static_cast<int>(div), d = static_cast<int>(qk_dim);
-    if ((err = ssm::launch_linattn_head_sum(f32(l.dq), dq, plan, n, d, bf16, stream)) != 0 ||
-        (err = ssm::launch_linattn_head_sum(f32(l.dk), dk, plan, n, d, bf16, stream)) != 0)
+    if ((err = ssm::launch_linattn_head_sum(f32(l.dq), f32(l.dk), dq, dk, plan, n, d, bf16,
+                                            stream)) != 0)
       return hip_failed(err);
   }
   if (want_dg) {

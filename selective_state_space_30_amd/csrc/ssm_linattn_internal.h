@@ -128,9 +128,10 @@ int launch_linattn_grads_f32(const LinCore &dq, const LinCore &dk, const LinCore
 // one or two (b not null) chains over the same segments
 int launch_linattn_chain(const LinChain &a, const LinChain *b, void *stream);
 int launch_linattn_decay_grad(const LinDecayGrad &a, void *stream);
-// sums of `div` consecutive heads: in (tokens, heads, d) fp32 -> out (tokens, heads / div, d)
-int launch_linattn_head_sum(const float *in, void *out, const LinPlan &plan, int div, int d,
-                            bool bf16, void *stream);
+// sums of `div` consecutive heads, for two arrays: in (tokens, heads, d) fp32 -> out
+// (tokens, heads / div, d)
+int launch_linattn_head_sum(const float *in0, const float *in1, void *out0, void *out1,
+                            const LinPlan &plan, int div, int d, bool bf16, void *stream);
 // out[h] = sum of in[t][h]
 int launch_linattn_token_sum(const float *in, float *out, const LinPlan &plan, void *stream);
 int launch_linattn_step(const LinStep &a, bool bf16, void *stream);
