@@ -22,9 +22,9 @@
  * Value head h uses query/key head h / (heads / qk_heads).  A row stride
  * larger than the row lets q, k and v be parts of one projection's output.
  * Sizes: qk_dim and v_dim 1..256; heads a multiple of qk_heads; row strides
- * up to 2^22; activations fp32 or bf16 (ssm_dtype).  bf16 rows whose starts, strides and head sizes
- * are multiples of 16 bytes are read 16 bytes at a time; others element by
- * element.
+ * up to 2^22; activations fp32 or bf16 (ssm_dtype).  Rows whose starts,
+ * strides and head sizes are multiples of 16 bytes are read 16 bytes at a
+ * time; others element by element.
  *
  * Sequences: without cu_seqlens the tokens are nseq sequences of tokens /
  * nseq rows; with it (device, int32, nseq + 1 offsets, not falling, within
@@ -80,8 +80,12 @@ int ssm_linattn_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t
  *              use until the enqueued work is done; its contents on entry do
  *              not matter
  * bf16: the weighted products of token pairs, and the state where o is read
- * from it, are rounded to bf16 once; what enters the state is a pair of bf16
- * values a product (2^-16 of it), carried in fp32.  fp32 runs in fp32. */
+ * from it, are rounded to bf16 once; what enters the state does so with 24
+ * bits (as three bf16 values) and is carried in fp32.  fp32 runs in fp32.
+ * An infinity or NaN in a token's q, k, v or g may make every result of its
+ * chunk of 64 tokens (fp32: 32), counted from the start of its segment, and
+ * of those after it in the sequence NaN, not only those the recurrence
+ * reaches; other sequences and heads with other inputs are not touched. */
 int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                     const void *v, int64_t v_stride, const float *g, unsigned flags, float scale,
                     const float *h0, const int32_t *cu_seqlens, void *o, float *h_final,

@@ -172,6 +172,10 @@ __device__ __forceinline__ void part_means(float (&own)[kP], const NormArgs &p, 
   }
 }
 
+// Bound by memory.  Measured: 8192 rows of 5120 bf16 in 80 parts with a gate,
+// 252 MB: 41 us on inputs that the caches hold in part, 52 us a call on others
+// (4.9 TB/s; a large copy: 5.2); 8192 rows of 2560 with both norms, gate, scale
+// and an fp32 residual, 57 us (294 MB, 5.1 TB/s); 8 rows of 2560, 3.5 us.
 template <typename T, typename R, int kN, int kP, int kParts>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p) {
   __shared__ float Buf[2][16][1];
@@ -252,6 +256,12 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p) {
   }
 }
 
+// The row's inputs stay as they are in memory (packed) until they are used,
+// and the next row's are asked for before this row's sums.  Measured: 8192
+// rows of 2560, both norms, gate, scale, fp32 residual, 126 us (462 MB, 3.7
+// TB/s; 175 us without the early loads); bound by the instructions of a
+// workgroup's 5 waves on 4 SIMDs, since the sums for the weights leave room
+// for one workgroup a CU.  (With those sums in LDS, two a CU: 181 to 211 us.)
 template <typename T, typename R, int kN, int kP, int kParts, int kBound>
 __global__ __launch_bounds__(kBound, sizeof(R) == 2 && kN == 8 ? 3 : 1) void norm_bwd_kernel(NormArgs p) {
   __shared__ float Buf1[16][1];
@@ -435,7 +445,7 @@ __global__ __launch_bounds__(kBound, sizeof(R) == 2 && kN == 8 ? 3 : 1) void nor
 }
 
 // Sum of the workgroups' partial rows, 32 columns and 32 row groups a
-// workgroup, in a fixed order.
+// workgroup, in a fixed order.  (8 us for 3 x 2560 columns.)
 __global__ __launch_bounds__(1024) void norm_parts_kernel(NormArgs p) {
   __shared__ float Sums[32][33];
   const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;

@@ -8,10 +8,11 @@ bf16 off by at most 2^-8 of the value (half of torch.finfo's eps), to fp32
  - bf16 outputs: each term is rounded once as an operand (a weighted pair
    product, or the state it stands in) and the sum once on its way out:
    |g - r| <= 2^-8 |r| + 2^-8 A (1 + 2^-6), the last factor for products of
-   roundings, the fp32 sums and the pairs below.
- - fp32 outputs of bf16 inputs: a term enters the state as a pair of bf16
-   values and leaves it as one, 2^-16 of itself each, and goes through at most
-   512 fp32 additions or products: |g - r| <= 2^-15 A + 2^-15 A.
+   roundings, the fp32 sums and the split below.
+ - fp32 outputs of bf16 inputs: a term enters the state, and leaves it, as
+   two or more bf16 values, within 2^-16 of itself each (three: 2^-24), and
+   goes through at most 512 fp32 additions or products:
+   |g - r| <= 2^-15 A + 2^-15 A.
  - fp32 inputs: the additions and products alone, 2^-15 A.
  - dg is summed from the end of a segment, dg_t = dg_{t+1} + row_t - col_t,
    with |row_t| <= A_t and |col_t| <= A_{t+1}: the bound of dg_t is that of
