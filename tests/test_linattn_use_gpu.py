@@ -237,3 +237,85 @@ def test_offsets_outside_the_rows_touch_nothing_else():
                                                                     device=DEV), o=o)
         torch.cuda.synchronize()
         assert (buf[:t] == 5.0).all() and (buf[2 * t:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_nan_stays_in_its_sequence(dtype):
+    """NaN in one packed sequence and in the rows outside all of them, and in
+    idle rows and foreign slots of a step, reaches nothing else: the same bits
+    as with finite values there."""
+    cu = [5, 75, 140, 471]
+    t, H, dk, dv = 480, 4, 64, 64
+    gen = torch.Generator().manual_seed(21)
+    r = lambda *s: torch.randn(*s, generator=gen).to(DEV)  # noqa: E731
+    q, k = r(t, 2, dk).to(dtype), r(t, 2, dk).to(dtype)
+    v, do, g = r(t, H, dv).to(dtype), r(t, H, dv).to(dtype), -torch.rand(t, H, generator=gen).to(DEV)
+    h0, dh = r(3, H, dk, dv), r(3, H, dk, dv)
+    off = torch.tensor(cu, dtype=torch.int32, device=DEV)
+
+    def run(*a):
+        q, k, v, do, g, h0, dh = a
+        o, h = ssm.ssm_linattn_fwd(q, k, v, g, h0=h0, cu_seqlens=off)
+        d = ssm.ssm_linattn_bwd(q, k, v, g, h0=h0, cu_seqlens=off, do=do, dh_final=dh)
+        return [o] + [d[n] for n in ("dq", "dk", "dv", "dg")], [h, d["dh0"]]
+
+    clean = (q, k, v, do, g, h0, dh)
+    dirty = [x.clone() for x in clean]
+    for x in dirty[:5]:
+        x[:cu[0]] = x[cu[1]:cu[2]] = x[cu[3]:] = float("nan")
+    for x in dirty[5:]:
+        x[1] = float("nan")
+    want, got = run(*clean), run(*dirty)
+    for a, b in zip(want[0], got[0]):
+        for rows in (slice(cu[0], cu[1]), slice(cu[2], cu[3])):
+            assert torch.equal(a[rows], b[rows])
+    for a, b in zip(want[1], got[1]):
+        assert torch.equal(a[[0, 2]], b[[0, 2]]) and torch.isnan(b[1]).any()
+
+    slots = torch.tensor([2, -1, 0], dtype=torch.int32, device=DEV)
+    first = [x[:3].clone() for x in (q, k, v, g)]
+    ref_state = h0.clone()
+    ref_o = ssm.ssm_linattn_step(ref_state, *first, slots=slots)
+    state = h0.clone()
+    for x in first:
+        x[1] = float("nan")
+    state[1] = float("nan")
+    o = ssm.ssm_linattn_step(state, *first, slots=slots)
+    assert torch.equal(o, ref_o) and (o[1] == 0).all()
+    assert torch.equal(state[[0, 2]], ref_state[[0, 2]]) and torch.isnan(state[1]).all()
+
+
+def test_offsets_past_32_bits():
+    """The last of three packed sequences lies more than 2^31 elements into v,
+    o and their gradients, the last slot as far into the states."""
+    t, H, dk, dv = 530000, 32, 16, 128
+    cu = [100, 264000, 529000, 529900]
+    gen = torch.Generator(device=DEV).manual_seed(22)
+    r = lambda *s: torch.randn(*s, generator=gen, device=DEV, dtype=BF16)  # noqa: E731
+    q, k, v, do = r(t, 1, dk), r(t, 1, dk), r(t, H, dv), r(t, H, dv)
+    g = -torch.rand(t, H, generator=gen, device=DEV)
+    off = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    own = slice(cu[2], cu[3])
+    alone = [x[own][None] for x in (q, k, v, g)]
+    o, h = ssm.ssm_linattn_fwd(q, k, v, g, cu_seqlens=off)
+    o1, h1 = ssm.ssm_linattn_fwd(*alone)
+    check(o[own].cpu(), o1[0].cpu().double(), "o", 2e-2)
+    check(h[2:].cpu(), h1.cpu().double(), "h_final")
+    del o
+    d = ssm.ssm_linattn_bwd(q, k, v, g, cu_seqlens=off, do=do)
+    d1 = ssm.ssm_linattn_bwd(*alone, do=do[own][None])
+    for n in ("dq", "dk", "dv"):
+        check(d[n][own].cpu(), d1[n][0].cpu().double(), n, 2e-2)
+    check(d["dg"][own].cpu(), d1["dg"][0].cpu().double(), "dg")
+    del d, v, do
+
+    nslots, H, dk, dv = 8200, 16, 128, 128
+    state = torch.zeros(nslots, H, dk, dv, device=DEV)
+    state[nslots - 1].normal_(generator=gen)
+    few = state[nslots - 2:].clone()
+    a = (r(2, H, dk), r(2, H, dk), r(2, H, dv), -torch.rand(2, H, generator=gen, device=DEV))
+    slots = torch.tensor([nslots - 1, nslots - 2], dtype=torch.int32, device=DEV)
+    o = ssm.ssm_linattn_step(state, *a, slots=slots)
+    o1 = ssm.ssm_linattn_step(few, *a, slots=slots - (nslots - 2))
+    assert torch.equal(o, o1) and torch.equal(state[nslots - 2:], few)
+    assert not state[:nslots - 2].any()
