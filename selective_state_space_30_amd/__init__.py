@@ -773,12 +773,14 @@ def _on_device(fn):
     (kernels are launched on the current device), and with ``stream`` (when
     given) as torch's current stream, as :func:`_on_stream` does."""
     inner = _on_stream(fn)
-    first = next(iter(inspect.signature(fn).parameters))
+    names = list(inspect.signature(fn).parameters)
+    first, at = names[0], names.index("stream")
 
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         t = args[0] if args else kwargs.get(first)
-        call = inner if kwargs.get("stream") is not None else fn
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        call = fn if stream is None else inner
         if (isinstance(t, torch.Tensor) and t.is_cuda
                 and t.get_device() != torch.cuda.current_device()):
             with torch.cuda.device(t.device):
