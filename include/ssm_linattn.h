@@ -30,7 +30,7 @@
  * nseq rows; with it (device, int32, nseq + 1 offsets, not falling, within
  * 0..tokens) sequence i is rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1, of
  * any length, 0 included.  Rows before the first and behind the last
- * sequence are neither read nor written.  The offsets are not checked
+ * sequence are not read, and written only with SSM_FLAG_ZERO_OUTSIDE.  The offsets are not checked
  * (that would need a synchronisation): ones outside 0..tokens are brought
  * into that range and a falling one ends its sequence, so that no memory
  * outside the arrays is touched, but results are then unspecified.
@@ -46,6 +46,9 @@ extern "C" {
 
 /* g holds one log decay a head, for every token: (heads) */
 #define SSM_FLAG_HEAD_DECAY 8u
+/* rows of o, dq, dk, dv and dg that lie in no sequence are set to 0 (without
+ * it they are left as they are) */
+#define SSM_FLAG_ZERO_OUTSIDE 32u
 
 /* How ssm_linattn_fwd (backward = 0) or ssm_linattn_bwd (backward = 1, or 2
  * with dg) cuts the sequences, in plan_out[4] (no HIP call):

@@ -59,6 +59,7 @@ SSM_FLAG_DELTA_SOFTPLUS = 1
 SSM_FLAG_ZOH_B = 2
 SSM_FLAG_BWD_SAVED = 4
 SSM_FLAG_HEAD_DECAY = 8
+SSM_FLAG_ZERO_OUTSIDE = 32
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_INVALID_ARG", 2: "SSM_ERR_UNSUPPORTED",
           3: "SSM_ERR_WORKSPACE", 4: "SSM_ERR_HIP"}
 EXPORTS = ("ssm_abi_version", "ssm_scan_plan", "ssm_scan_workspace_size",
@@ -965,12 +966,14 @@ def ssm_linattn_fwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     h0: (batch, heads, qk_dim, v_dim) fp32 or None.  With ``cu_seqlens``
     (int32, device, sequences + 1 row offsets) the sequences are packed: q, k,
     v (and g) have one leading dimension, tokens, and states one per
-    sequence; rows outside the sequences are left as they are.  q, k and v
-    may be slices of wider rows.  Returns ``(o, h_final)``."""
+    sequence; rows of o outside the sequences are 0, those of a given ``o``
+    left as they are.  q, k and v may be slices of wider rows.  Returns
+    ``(o, h_final)``."""
     a = _Linattn(q, k, v, g, scale, h0, cu_seqlens)
     lib = load_library()
     if o is None:
         o = torch.empty(a.lead + a.vo, dtype=a.act, device=a.dev)
+        a.flags |= SSM_FLAG_ZERO_OUTSIDE
     if not return_final_state:
         h_final = None
     elif h_final is None:
@@ -995,7 +998,8 @@ def ssm_linattn_bwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     (like o) and ``dh_final`` (like h_final, or None).  Returns a dict: dq,
     dk, dv (activation dtype; dq and dk summed over the value heads that share
     a query/key head), dg (fp32, like g; when g is given) and dh0 (fp32).
-    ``out`` may supply any of them."""
+    ``out`` may supply any of them.  Rows outside packed sequences are 0, those
+    of given tensors left as they are."""
     if do is None:
         raise ValueError("do is required")
     a = _Linattn(q, k, v, g, scale, h0, cu_seqlens)
@@ -1008,13 +1012,22 @@ def ssm_linattn_bwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
         shapes["dg"] = (tuple(g.shape), f32)
     if want_dh0:
         shapes["dh0"] = (a.states, f32)
+    kind = 0 if "dg" not in shapes else 2 if a.flags else 1
     out = dict(out or {})
+    # rows outside packed sequences: the library clears those of all outputs
+    # by token or of none
+    new = torch.empty
+    if a.cu is not None:
+        by_token = ["dq", "dk", "dv"] + ["dg"] * (kind == 1)
+        if not any(name in out for name in by_token):
+            a.flags |= SSM_FLAG_ZERO_OUTSIDE
+        else:
+            new = torch.zeros
     p = {}
     for name, (shape, dtype) in shapes.items():
         if name not in out:
-            out[name] = torch.empty(shape, dtype=dtype, device=a.dev)
+            out[name] = new(shape, dtype=dtype, device=a.dev)
         p[name] = _dense(out[name], name, dtype, shape, a.dev)
-    kind = 0 if "dg" not in shapes else 2 if a.flags else 1
     need = _size(lib.ssm_linattn_bwd_workspace_size, a.tokens, a.nseq, a.cu is not None,
                  a.heads, a.qk_heads, a.dk, a.dv, a.code, kind)
     keep, ws, ws_bytes = _scratch(workspace, need, a.dev)

@@ -224,6 +224,29 @@ __global__ __launch_bounds__(1024) void linattn_token_sum_kernel(const float *in
   if (tid == 0) out[h] = static_cast<float>(Red[0]);
 }
 
+// ------------------------------------------------- rows of no sequence ---
+// Rows before the first and behind the last sequence of one array
+// (blockIdx.y).  Rows start on any element: 16 bytes at a time between the
+// first and the last such boundary, and 2 before and behind.
+__global__ __launch_bounds__(256) void linattn_zero_outside_kernel(LinZero z) {
+  char *base = static_cast<char *>(z.arrays[blockIdx.y].p);
+  const int64_t row = z.arrays[blockIdx.y].row_bytes;
+  int64_t begin, end;
+  all_rows(z.plan, &begin, &end);
+  const int64_t first = blockIdx.x * 256 + threadIdx.x, step = gridDim.x * 256;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(base) + (side ? end : 0) * row;
+    const uintptr_t hi = reinterpret_cast<uintptr_t>(base) + (side ? z.plan.tokens : begin) * row;
+    uintptr_t a = (lo + 15) / 16 * 16, b = hi / 16 * 16;
+    if (a > b) a = b = hi;  // inside one piece of 16 bytes
+    for (uintptr_t p = lo + 2 * first; p < a; p += 2 * step) *reinterpret_cast<uint16_t *>(p) = 0;
+    for (uintptr_t p = a + 16 * first; p < b; p += 16 * step)
+      *reinterpret_cast<u32x4 *>(p) = u32x4{0u, 0u, 0u, 0u};
+    for (uintptr_t p = b + 2 * first; p < hi; p += 2 * step) *reinterpret_cast<uint16_t *>(p) = 0;
+  }
+}
+
 // ------------------------------------------------------------------ step ---
 // One token: a workgroup takes 64 columns of one row's head state, 16
 // threads with 4 neighbouring columns each in 16 groups over the state's
@@ -375,6 +398,14 @@ int launch_linattn_head_sum(const float *in0, const float *in1, void *out0, void
 int launch_linattn_token_sum(const float *in, float *out, const LinPlan &plan, void *stream) {
   hipLaunchKernelGGL(linattn_token_sum_kernel, dim3(static_cast<unsigned>(plan.heads)), dim3(1024),
                      0, static_cast<hipStream_t>(stream), in, out, plan);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_linattn_zero_outside(const LinZero &a, void *stream) {
+  unsigned arrays = 0;
+  for (const auto &x : a.arrays) arrays += x.p != nullptr;
+  hipLaunchKernelGGL(linattn_zero_outside_kernel, dim3(256, arrays), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), a);
   return static_cast<int>(hipGetLastError());
 }
 

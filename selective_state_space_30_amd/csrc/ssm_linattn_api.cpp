@@ -268,11 +268,11 @@ int g_kind(const Call &c) {
               : c.flags & SSM_FLAG_HEAD_DECAY ? ssm::kLinDecayHead : ssm::kLinDecayToken;
 }
 
-// The checks that forward and backward share.
-int check_call(const Call &c) {
+// The checks that the calls share; `flags`: those that this one takes.
+int check_call(const Call &c, unsigned flags) {
   int st = check_sizes(c.z);
   if (st != SSM_OK) return st;
-  if (c.flags & ~SSM_FLAG_HEAD_DECAY)
+  if (c.flags & ~flags)
     return fail(SSM_ERR_INVALID_ARG, "unknown flag bits 0x%x", c.flags);
   if (c.z.tokens > 0 && (!c.q || !c.k || !c.v))
     return fail(SSM_ERR_INVALID_ARG, "required pointer is NULL (q=%p k=%p v=%p)", c.q, c.k, c.v);
@@ -289,6 +289,12 @@ int check_call(const Call &c) {
   for (const void *p : words)
     if (!aligned(p, 4)) return fail(SSM_ERR_INVALID_ARG, "pointer %p not 4-byte aligned", p);
   return SSM_OK;
+}
+
+// Whether the call sets the rows outside its sequences to 0 (only packed
+// ones leave any).
+bool zero_outside(const Call &c) {
+  return (c.flags & SSM_FLAG_ZERO_OUTSIDE) && c.cu && c.z.tokens > 0;
 }
 
 bool rows16(const void *p, int64_t stride, int64_t d, int64_t es) {
@@ -341,7 +347,7 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
                     void *stream) {
   const Call c{{tokens, nseq, heads, qk_heads, qk_dim, v_dim, dtype, cu_seqlens != nullptr},
                q, k, v, q_stride, k_stride, v_stride, g, h0, cu_seqlens, flags, scale};
-  int st = check_call(c);
+  int st = check_call(c, SSM_FLAG_HEAD_DECAY | SSM_FLAG_ZERO_OUTSIDE);
   if (st != SSM_OK) return st;
   const Sizes &z = c.z;
   const int64_t es = z.es();
@@ -396,7 +402,14 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   a.out_seqs = h_final;
   a.out = o;
   err = z.bf16() ? ssm::launch_linattn_out_bf16(a, stream) : ssm::launch_linattn_out_f32(a, stream);
-  return err != 0 ? hip_failed(err) : ok();
+  if (err != 0) return hip_failed(err);
+  if (zero_outside(c)) {
+    ssm::LinZero r{};
+    r.plan = plan;
+    r.arrays[0] = {o, heads * v_dim * es};
+    if ((err = ssm::launch_linattn_zero_outside(r, stream)) != 0) return hip_failed(err);
+  }
+  return ok();
 }
 
 int ssm_linattn_bwd_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t heads,
@@ -422,7 +435,7 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
                     void *stream) {
   const Call c{{tokens, nseq, heads, qk_heads, qk_dim, v_dim, dtype, cu_seqlens != nullptr},
                q, k, v, q_stride, k_stride, v_stride, g, h0, cu_seqlens, flags, scale};
-  int st = check_call(c);
+  int st = check_call(c, SSM_FLAG_HEAD_DECAY | SSM_FLAG_ZERO_OUTSIDE);
   if (st != SSM_OK) return st;
   const Sizes &z = c.z;
   const int64_t es = z.es();
@@ -569,6 +582,15 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
         (err = ssm::launch_linattn_token_sum(f32(l.dg), dg, plan, stream)) != 0)
       return hip_failed(err);
   }
+  if (zero_outside(c)) {
+    ssm::LinZero r{};
+    r.plan = plan;
+    r.arrays[0] = {dq, qk_heads * qk_dim * es};
+    r.arrays[1] = {dk, qk_heads * qk_dim * es};
+    r.arrays[2] = {dv, heads * v_dim * es};
+    if (want_dg == 1) r.arrays[3] = {dg, heads * 4};
+    if ((err = ssm::launch_linattn_zero_outside(r, stream)) != 0) return hip_failed(err);
+  }
   return ok();
 }
 
@@ -579,7 +601,7 @@ int ssm_linattn_step(float *state, const void *q, int64_t q_stride, const void *
                      int64_t v_dim, int dtype, void *stream) {
   const Call c{{batch, 1, heads, qk_heads, qk_dim, v_dim, dtype, true},
                q, k, v, q_stride, k_stride, v_stride, g, nullptr, slots, flags, scale};
-  int st = check_call(c);
+  int st = check_call(c, SSM_FLAG_HEAD_DECAY);
   if (st != SSM_OK) return st;
   const int64_t es = c.z.es();
   if (nslots <= 0 || nslots >= (int64_t(1) << 31))

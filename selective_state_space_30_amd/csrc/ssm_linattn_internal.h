@@ -97,6 +97,11 @@ struct LinDecayGrad {
   float *dg;
 };
 
+struct LinZero {          // rows outside the sequences, set to 0
+  LinPlan plan;
+  struct { void *p; int64_t row_bytes; } arrays[4];  // those with p first
+};
+
 struct LinStep {
   float *state;
   const void *q, *k, *v;
@@ -134,6 +139,7 @@ int launch_linattn_head_sum(const float *in0, const float *in1, void *out0, void
                             const LinPlan &plan, int div, int d, bool bf16, void *stream);
 // out[h] = sum of in[t][h]
 int launch_linattn_token_sum(const float *in, float *out, const LinPlan &plan, void *stream);
+int launch_linattn_zero_outside(const LinZero &a, void *stream);
 int launch_linattn_step(const LinStep &a, bool bf16, void *stream);
 
 }  // namespace ssm

@@ -1,0 +1,100 @@
+"""Rows of packed linear attention that lie in no sequence: 0 in what the
+binding allocates (the gradient of an input that nothing reads), left as they
+are in tensors that the caller gives, unless SSM_FLAG_ZERO_OUTSIDE is set."""
+import pytest
+import torch
+
+import selective_state_space_30_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _inputs(dtype, tokens, heads, qk_heads, dk, dv, decay):
+    gen = torch.Generator().manual_seed(tokens + dk)
+    r = lambda *s: torch.randn(*s, generator=gen).to(dtype).to(DEV)  # noqa: E731
+    q, k = r(tokens, qk_heads, dk), r(tokens, qk_heads, dk)
+    v, do = r(tokens, heads, dv), r(tokens, heads, dv)
+    g = None
+    if decay == "token":
+        g = -torch.rand(tokens, heads, generator=gen).to(DEV)
+    elif decay == "head":
+        g = -torch.rand(heads, generator=gen).to(DEV)
+    return q, k, v, g, do
+
+
+def _fill_allocator(*like):
+    """Leaves NaN in the memory that the next tensors of these sizes get."""
+    old = [torch.full_like(t, float("nan")) for t in like for _ in range(3)]
+    torch.cuda.synchronize()
+    del old
+
+
+CASES = [
+    # dtype, offsets, tokens, heads, qk_heads, dk, dv, decay
+    (BF16, [3, 3, 70, 390], 400, 2, 2, 64, 64, "token"),
+    (BF16, [1, 40], 41, 3, 1, 5, 7, "token"),     # rows that no 16 bytes divide
+    (BF16, [7, 7, 7], 9, 1, 1, 1, 1, "none"),     # every row outside
+    (F32, [0, 33, 300], 1000, 2, 1, 40, 100, "head"),
+    (F32, [50, 64], 64, 2, 2, 16, 16, "token"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "%s_t%d_%s" % (
+    "bf16" if c[0] == BF16 else "f32", c[2], c[7]))
+def test_new_tensors_hold_zeros_outside(case):
+    dtype, offsets, tokens, heads, qk_heads, dk, dv, decay = case
+    q, k, v, g, do = _inputs(*((dtype,) + case[2:]))
+    cu = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    inside = slice(offsets[0], offsets[-1])
+    outside = [slice(0, offsets[0]), slice(offsets[-1], tokens)]
+    given = torch.full_like(v, 7.0)
+    ssm.ssm_linattn_fwd(q, k, v, g, cu_seqlens=cu, o=given)
+    _fill_allocator(v)
+    o, _ = ssm.ssm_linattn_fwd(q, k, v, g, cu_seqlens=cu)
+    assert torch.equal(o[inside], given[inside])
+    for rows in outside:
+        assert (o[rows] == 0).all() and (given[rows] == 7.0).all()
+    by_token = {"dq": q, "dk": k, "dv": v}
+    if decay == "token":
+        by_token["dg"] = g
+    given = {n: torch.full_like(t, 7.0) for n, t in by_token.items()}
+    ssm.ssm_linattn_bwd(q, k, v, g, cu_seqlens=cu, do=do, out=given)
+    _fill_allocator(*by_token.values())
+    d = ssm.ssm_linattn_bwd(q, k, v, g, cu_seqlens=cu, do=do)
+    _fill_allocator(*by_token.values())
+    part = ssm.ssm_linattn_bwd(q, k, v, g, cu_seqlens=cu, do=do, out={
+        "dk": torch.full_like(k, 7.0)})
+    for n in by_token:
+        assert torch.equal(d[n][inside], given[n][inside])
+        assert torch.equal(part[n][inside], given[n][inside])
+        for rows in outside:
+            assert (d[n][rows] == 0).all(), n
+            assert (given[n][rows] == 7.0).all(), n
+            assert (part[n][rows] == (7.0 if n == "dk" else 0.0)).all(), n
+
+
+def test_zeros_reach_only_the_rows_outside():
+    """The flag through the C ABI, on rows in the middle of a larger buffer
+    that starts on no 16 bytes."""
+    dtype, offsets, tokens, heads, qk_heads, dk, dv, decay = CASES[1]
+    q, k, v, g, do = _inputs(*((dtype,) + CASES[1][2:]))
+    cu = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    n = tokens * heads * dv
+    want, _ = ssm.ssm_linattn_fwd(q, k, v, g, 1.0, cu_seqlens=cu)
+    buf = torch.full((n + 200,), 5.0, dtype=BF16, device=DEV)
+    for at in (1, 8, 13):
+        buf.fill_(5.0)
+        o = buf[at:at + n]
+        assert ssm.load_library().ssm_linattn_fwd(
+            q.data_ptr(), qk_heads * dk, k.data_ptr(), qk_heads * dk, v.data_ptr(), heads * dv,
+            g.data_ptr(), ssm.SSM_FLAG_ZERO_OUTSIDE, 1.0, None, cu.data_ptr(), o.data_ptr(), None,
+            tokens, len(offsets) - 1, heads, qk_heads, dk, dv, ssm.SSM_DTYPE_BF16, None, 0,
+            torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        rows = o.view(tokens, -1)
+        assert (rows[:offsets[0]] == 0).all() and (rows[offsets[-1]:] == 0).all()
+        inside = slice(offsets[0], offsets[-1])
+        assert torch.equal(rows[inside], want.view(tokens, -1)[inside])
+        assert (buf[:at] == 5.0).all() and (buf[at + n:] == 5.0).all()
