@@ -24,7 +24,10 @@
  * Sizes: qk_dim and v_dim 1..256; heads a multiple of qk_heads; row strides
  * up to 2^22; activations fp32 or bf16 (ssm_dtype).  Rows whose starts,
  * strides and head sizes are multiples of 16 bytes are read 16 bytes at a
- * time; others element by element.
+ * time; others element by element.  Calls that would need a launch of 2^32
+ * threads are refused (SSM_ERR_UNSUPPORTED, by ssm_linattn_plan too): segments
+ * (below) times heads times the 128-column slices of the outputs, and with dg
+ * chunks times heads as well, have to stay under 2^23.
  *
  * Sequences: without cu_seqlens the tokens are nseq sequences of tokens /
  * nseq rows; with it (device, int32, nseq + 1 offsets, not falling, within

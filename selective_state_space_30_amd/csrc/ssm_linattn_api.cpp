@@ -124,16 +124,22 @@ int check_sizes(const Sizes &z) {
 // kMaxGradSegment tokens.
 constexpr int64_t kPlaces = 512, kMinSegment = 128, kMaxGradSegment = 1024;
 
+// workgroups that `out` output columns take
+int64_t slices_of(int64_t out) {
+  const int64_t w = ssm::linattn_slice(static_cast<int>(out));
+  return (out + w - 1) / w;
+}
+
+// value heads that a workgroup takes
+int64_t heads_per_group(const Sizes &z) {
+  return ssm::linattn_pairs_heads(static_cast<int>(z.heads / z.qk_heads), static_cast<int>(z.dv))
+             ? 2 : 1;
+}
+
 // workgroups that a sequence's chunk pass has
 int64_t groups_of(const Sizes &z, bool backward) {
-  const int64_t div = z.heads / z.qk_heads;
-  auto slices = [](int64_t d) {
-    const int64_t w = ssm::linattn_slice(static_cast<int>(d));
-    return (d + w - 1) / w;
-  };
-  const int64_t pair = ssm::linattn_pairs_heads(static_cast<int>(div), static_cast<int>(z.dv)) ? 2 : 1;
-  const int64_t one = z.heads / pair * slices(z.dv);
-  return backward ? one + 2 * z.heads * slices(z.dk) : one;
+  const int64_t one = z.heads / heads_per_group(z) * slices_of(z.dv);
+  return backward ? one + 2 * z.heads * slices_of(z.dk) : one;
 }
 
 ssm::LinPlan make_plan(const Sizes &z, bool backward, bool decay_grad) {
@@ -168,13 +174,28 @@ bool many_segments(const Sizes &z, const ssm::LinPlan &p) {
   return z.packed ? p.seg_len < z.tokens : p.segs > 1;
 }
 
-int check_plan(const Sizes &z, const ssm::LinPlan &p) {
+// The plan of the sums over pairs, whose workgroups take a chunk each:
+// segments of one chunk.  Their number grows with the tokens, not with the
+// length that the segments happen to have.
+ssm::LinPlan pairs_plan(const Sizes &z, ssm::LinPlan p) {
+  const int64_t chunk = ssm::linattn_chunk(z.bf16());
+  p.seg_len = chunk;
+  p.segs = z.packed ? 0 : p.seqlen > chunk ? (p.seqlen + chunk - 1) / chunk : 1;
+  p.slots = z.packed ? z.tokens / chunk + z.nseq : z.nseq * p.segs;
+  return p;
+}
+
+// Whether every launch of the call stays within 2^32 threads.  backward: 0
+// no, 1 yes, 2 with dg.
+int check_plan(const Sizes &z, const ssm::LinPlan &p, int backward) {
   if (z.heads * z.dk > kMaxStride || z.heads * z.dv > kMaxStride)
     return fail(SSM_ERR_UNSUPPORTED, "heads=%lld: rows too long", (long long)z.heads);
-  // the widest grid: three gradients of two slices and the chunks' token pairs
-  // (times two for their 512 threads)
-  if (z.nseq * z.heads > kMaxGroups ||
-      2 * p.slots * z.heads * (6 + p.seg_len / ssm::linattn_chunk(z.bf16())) > kMaxGroups)
+  // the chain; and the widest of the others: the output pass, or the gradients'
+  // three and with dg the pairs', all of at most 512 threads
+  int64_t groups = p.slots * z.heads * slices_of(z.dv);
+  if (backward) groups += 2 * p.slots * z.heads * slices_of(z.dk);
+  if (backward == 2) groups += pairs_plan(z, p).slots * z.heads / heads_per_group(z);
+  if (z.nseq * z.heads > kMaxGroups || 2 * groups > kMaxGroups)
     return fail(SSM_ERR_UNSUPPORTED, "tokens=%lld heads=%lld nseq=%lld: too many workgroups",
                 (long long)z.tokens, (long long)z.heads, (long long)z.nseq);
   return SSM_OK;
@@ -197,11 +218,6 @@ FwdLayout fwd_layout(const Sizes &z, const ssm::LinPlan &p) {
 struct BwdLayout {
   int64_t states, adjoints, decay, adecay, last, dq, dk, pairs, xdots, ydots, dg, total;
 };
-
-int64_t slices_of(int64_t out) {
-  const int64_t w = ssm::linattn_slice(static_cast<int>(out));
-  return (out + w - 1) / w;
-}
 
 // want_dg: 0 no, 1 a token, 2 a head
 BwdLayout bwd_layout(const Sizes &z, const ssm::LinPlan &p, int want_dg) {
@@ -318,7 +334,7 @@ int ssm_linattn_plan(int64_t tokens, int64_t nseq, int packed, int64_t heads, in
   int st = check_sizes(z);
   if (st != SSM_OK) return st;
   const ssm::LinPlan p = make_plan(z, backward != 0, backward == 2);
-  if ((st = check_plan(z, p)) != SSM_OK) return st;
+  if ((st = check_plan(z, p, backward)) != SSM_OK) return st;
   plan_out[0] = p.seg_len;
   plan_out[1] = p.slots;
   plan_out[2] = ssm::linattn_chunk(z.bf16());
@@ -334,7 +350,7 @@ int ssm_linattn_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t
   int st = check_sizes(z);
   if (st != SSM_OK) return st;
   const ssm::LinPlan p = make_plan(z, false, false);
-  if ((st = check_plan(z, p)) != SSM_OK) return st;
+  if ((st = check_plan(z, p, 0)) != SSM_OK) return st;
   *bytes = static_cast<size_t>(fwd_layout(z, p).total);
   return ok();
 }
@@ -355,7 +371,7 @@ int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
   if (!aligned(o, es) || !aligned(h_final, 4))
     return fail(SSM_ERR_INVALID_ARG, "output not aligned (o=%p h_final=%p)", o, (void *)h_final);
   ssm::LinPlan plan = make_plan(z, false, false);
-  if ((st = check_plan(z, plan)) != SSM_OK) return st;
+  if ((st = check_plan(z, plan, 0)) != SSM_OK) return st;
   const FwdLayout l = fwd_layout(z, plan);
   if ((st = check_workspace(workspace, workspace_bytes, static_cast<size_t>(l.total))) != SSM_OK)
     return st;
@@ -421,7 +437,7 @@ int ssm_linattn_bwd_workspace_size(int64_t tokens, int64_t nseq, int packed, int
   int st = check_sizes(z);
   if (st != SSM_OK) return st;
   const ssm::LinPlan p = make_plan(z, true, want_dg != 0);
-  if ((st = check_plan(z, p)) != SSM_OK) return st;
+  if ((st = check_plan(z, p, want_dg ? 2 : 1)) != SSM_OK) return st;
   *bytes = static_cast<size_t>(bwd_layout(z, p, want_dg).total);
   return ok();
 }
@@ -453,7 +469,7 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     if (!aligned(p, 4)) return fail(SSM_ERR_INVALID_ARG, "pointer %p not 4-byte aligned", p);
   const int want_dg = !dg ? 0 : flags & SSM_FLAG_HEAD_DECAY ? 2 : 1;
   ssm::LinPlan plan = make_plan(z, true, want_dg != 0);
-  if ((st = check_plan(z, plan)) != SSM_OK) return st;
+  if ((st = check_plan(z, plan, want_dg ? 2 : 1)) != SSM_OK) return st;
   const BwdLayout l = bwd_layout(z, plan, want_dg);
   if ((st = check_workspace(workspace, workspace_bytes, static_cast<size_t>(l.total))) != SSM_OK)
     return st;
@@ -551,7 +567,8 @@ int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_st
     gk.x = K;
     gk.dots = f32(l.ydots);
   }
-  const ssm::LinPairs pr{plan, Q, K, V, O, g, base.g_kind, scale, want_dg ? f32(l.pairs) : nullptr};
+  const ssm::LinPairs pr{pairs_plan(z, plan), Q, K, V, O, g, base.g_kind, scale,
+                         want_dg ? f32(l.pairs) : nullptr};
   err = bf16 ? ssm::launch_linattn_grads_bf16(gq, gk, gv, want_dg ? &pr : nullptr, stream)
              : ssm::launch_linattn_grads_f32(gq, gk, gv, want_dg ? &pr : nullptr, stream);
   if (err != 0) return hip_failed(err);

@@ -808,12 +808,10 @@ __device__ __forceinline__ void pairs(const LinPairs &p, unsigned block,
   const int li = lane & 15, lq = lane >> 4;
   const unsigned teams = static_cast<unsigned>(p.plan.heads) / kHeads;
   const int h0 = block % teams * kHeads;
-  const unsigned per_seg = static_cast<unsigned>(p.plan.seg_len) / C;
-  const unsigned cs = block / teams;
-  const Segment sg = segment_of(p.plan, cs / per_seg);
-  const int64_t t0 = sg.begin + static_cast<int64_t>(cs % per_seg) * C;
+  const Segment sg = segment_of(p.plan, block / teams);  // one chunk
+  const int64_t t0 = sg.begin;
   if (!sg.real || t0 >= sg.end) return;
-  const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
+  const int rows = static_cast<int>(sg.end - t0);
   auto head = [&](const LinSide &x, int h) __attribute__((always_inline)) {
     return static_cast<const T *>(x.p) + t0 * x.stride + (h / x.div) * x.d;
   };
@@ -1034,9 +1032,7 @@ int launch_grads_t(const LinCore &dq, const LinCore &dk, const LinCore &dv, cons
                    hipStream_t s) {
   const unsigned n = core_blocks<kWaves, 1>(dq), nv = core_blocks<kWaves, kHeads>(dv);
   const unsigned np =
-      pr ? static_cast<unsigned>(pr->plan.slots * (pr->plan.seg_len / Traits<T>::kChunk) *
-                                 (pr->plan.heads / kHeads))
-         : 0;
+      pr ? static_cast<unsigned>(pr->plan.slots * (pr->plan.heads / kHeads)) : 0;
   const dim3 grid(2 * n + nv + np), block(64 * kWaves);
   auto go = [&](auto dots, auto vec) {
     hipLaunchKernelGGL((linattn_grads_kernel<T, kDKv, kDKq, kWaves, kHeads, dots(), vec()>), grid,

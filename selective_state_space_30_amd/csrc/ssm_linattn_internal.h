@@ -75,7 +75,7 @@ struct LinChain {       // running states of the segments, in place
 };
 
 struct LinPairs {       // sums over token pairs inside each chunk
-  LinPlan plan;
+  LinPlan plan;         // its segments are the chunks
   LinSide q, k, v, o;
   const float *g;
   int g_kind;
