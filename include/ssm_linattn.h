@@ -88,10 +88,9 @@ int ssm_linattn_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t
  * bf16: the weighted products of token pairs, and the state where o is read
  * from it, are rounded to bf16 once; what enters the state does so with 24
  * bits (as three bf16 values) and is carried in fp32.  fp32 runs in fp32.
- * An infinity or NaN in a token's q, k, v or g may make every result of its
- * chunk of 64 tokens (fp32: 32), counted from the start of its segment, and
- * of those after it in the sequence NaN, not only those the recurrence
- * reaches; other sequences and heads with other inputs are not touched. */
+ * An infinity or NaN in a token's q, k, v or g reaches the results that the
+ * recurrence lets it reach (no token before it, no other column than its own
+ * if it is in v), but may be NaN there where the recurrence has an infinity. */
 int ssm_linattn_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                     const void *v, int64_t v_stride, const float *g, unsigned flags, float scale,
                     const float *h0, const int32_t *cu_seqlens, void *o, float *h_final,
@@ -118,6 +117,9 @@ int ssm_linattn_bwd_workspace_size(int64_t tokens, int64_t nseq, int packed, int
  *  dg          nullable output, fp32, shape of g; only with g
  *  dh0         nullable output, fp32
  *  workspace   >= ssm_linattn_bwd_workspace_size() bytes, 256-byte aligned
+ * An infinity or NaN in a token's q, k, v or d_o reaches dq of no token before
+ * it and dk and dv of none behind it; dg of its whole sequence, and with a NaN
+ * in g dk and dv of the chunk around it, may be NaN.
  * Sums run in a fixed order: the same call gives the same bits. */
 int ssm_linattn_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                     const void *v, int64_t v_stride, const float *g, unsigned flags, float scale,

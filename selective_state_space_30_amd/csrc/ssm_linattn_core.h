@@ -225,6 +225,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const T *base, int64
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(base), 0, bytes, kBufferWord3);
 }
 
+constexpr float kLargest = 3.4028235e38f;  // finite
+
 constexpr int kNowhere = 0x7ffffff0;  // behind the end of every view
 
 // kRows token rows of one head, kCols elements wide in LDS (the head's d,
@@ -718,6 +720,35 @@ __device__ __forceinline__ void core(const LinCore &p, unsigned block,
     if (more) stage();
     if (kOut) {
       const int lane = anew(tid) & 63, li = lane & 15, lq = lane >> 4;
+      // A pair left out has the weight 0, whose product with an infinity or
+      // NaN is NaN.  So columns that hold one, found by a product with zeros,
+      // are cleared of them first and marked from the first one on (against
+      // token order: up to the last) behind.  (1 to 3 % of a call's time; done
+      // before the barrier, where more registers are in use, 9 more of them
+      // went through scratch memory.)
+      f32x4 none = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ts = 0; ts < kTS; ++ts) none = mma(vf[ts], Frag{}, none);
+      const bool odd =
+          __builtin_amdgcn_ballot_w64(!(none[0] + none[1] + none[2] + none[3] == 0.0f)) != 0;
+      int mark = kRev ? -1 : C;  // of column li
+      if (odd) {
+#pragma unroll
+        for (int ts = 0; ts < kTS; ++ts)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int s = 32 * ts + 4 * lq + e % 4 + e / 4 * 16;
+            if (!(fabsf(static_cast<float>(vf[ts][e])) <= kLargest)) {
+              mark = kRev ? (s > mark ? s : mark) : (s < mark ? s : mark);
+              vf[ts][e] = static_cast<Elem>(0.0f);
+            }
+          }
+#pragma unroll
+        for (int d = 16; d < 64; d *= 2) {
+          const int o = __shfl_xor(mark, d);
+          mark = kRev ? (o > mark ? o : mark) : (o < mark ? o : mark);
+        }
+      }
 #pragma unroll
       for (int ti = 0; ti < kNT; ++ti)
 #pragma unroll
@@ -725,6 +756,14 @@ __device__ __forceinline__ void core(const LinCore &p, unsigned block,
           if (kRev ? 2 * ts + 1 < ti : 2 * ts > ti) continue;  // no pair left
           const Frag b = two_halves(&Ps[mine][(16 * ti + li) * kRowP + 32 * ts + 4 * lq]);
           O[ti] = mma(vf[ts], b, O[ti]);
+        }
+      if (odd)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int from = __shfl(mark, 4 * lq + e);
+#pragma unroll
+          for (int ti = 0; ti < kNT; ++ti)
+            if (kRev ? 16 * ti + li <= from : 16 * ti + li >= from) O[ti][e] = __builtin_nanf("");
         }
       const int64_t t0 = sg.begin + static_cast<int64_t>(c) * C;
       const int rows = sg.end - t0 < C ? static_cast<int>(sg.end - t0) : C;
