@@ -8,6 +8,9 @@
  *   o_t = scale * S_t^T q_t
  * g is a log decay: one a token and head (gated forms; the SSD form of
  * Mamba-2 with q = C, k = B, v = dt x, g = dt A), one a head, or none.
+ * ssm_ssd_fwd (ssm_scan.h) computes that SSD form from channel-major rows with
+ * softplus, D and the gate inside, forward only; its states are (headdim,
+ * dstate), the transpose of those here.
  *
  * Conventions are those of ssm_scan.h (device pointers owned by the caller,
  * nothing allocated, work enqueued on `stream`, statuses, ssm_last_error(),
@@ -74,7 +77,9 @@ int ssm_linattn_workspace_size(int64_t tokens, int64_t nseq, int packed, int64_t
  *  q, k, v     required, activation dtype; may overlap each other
  *  g           nullable fp32; (tokens, heads), or (heads) with
  *              SSM_FLAG_HEAD_DECAY.  Natural logarithm; -inf forgets all that
- *              came before the token
+ *              came before the token; above 0 the state grows, and sums of g
+ *              over runs of tokens have to stay below 88 (e^88 is near the
+ *              end of fp32's range)
  *  scale       factor of o
  *  h0          nullable fp32: state before each sequence (zero if NULL)
  *  cu_seqlens  nullable (see above)
@@ -117,6 +122,8 @@ int ssm_linattn_bwd_workspace_size(int64_t tokens, int64_t nseq, int packed, int
  *  dg          nullable output, fp32, shape of g; only with g
  *  dh0         nullable output, fp32
  *  workspace   >= ssm_linattn_bwd_workspace_size() bytes, 256-byte aligned
+ * Roundings as in the forward pass, except that with dg the state and its
+ * adjoint enter dq and dk, as well as dg, with 24 bits instead of bf16's 8.
  * An infinity or NaN in a token's q, k, v or d_o reaches dq of no token before
  * it and dk and dv of none behind it; dg of its whole sequence, and with a NaN
  * in g dk and dv of the chunk around it, may be NaN.
@@ -169,6 +176,9 @@ int ssm_linattn_step(float *state, const void *q, int64_t q_stride, const void *
  *  dtype        activations;  residual_dtype: residual and r (the
  *               activations' or SSM_DTYPE_F32)
  *  rows >= 0; dim 1..16384, at most 8192 with groups > 1; eps > 0
+ * With z and w_pre but no w_post, y is the norm of the gated row, x silu(z),
+ * as Mamba-2 has it.  Squares are summed in fp32: their mean has to lie within
+ * its range (elements up to about 1e17).
  * y is formed from r before r is rounded.  Outputs may not overlap inputs,
  * except that r may be exactly the residual, in place (dense rows). */
 int ssm_block_norm_fwd(const void *x, int64_t x_stride, const float *w_post, const void *z,

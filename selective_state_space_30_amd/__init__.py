@@ -999,7 +999,8 @@ def ssm_linattn_bwd(q, k, v, g=None, scale=None, h0=None, cu_seqlens=None,
     dk, dv (activation dtype; dq and dk summed over the value heads that share
     a query/key head), dg (fp32, like g; when g is given) and dh0 (fp32).
     ``out`` may supply any of them.  Rows outside packed sequences are 0, those
-    of given tensors left as they are."""
+    of given tensors left as they are.  In bf16, dq and dk read the state with
+    24 bits where dg is formed, else with 8."""
     if do is None:
         raise ValueError("do is required")
     a = _Linattn(q, k, v, g, scale, h0, cu_seqlens)
@@ -1101,7 +1102,8 @@ def ssm_block_norm_fwd(x, w_post=None, z=None, scale=None, residual=None,
     """The end of a block and the start of the next in one pass, per row:
     n = rmsnorm of each of ``groups`` parts of x, times w_post (n = x without
     w_post); r = residual + n * silu(z) * scale (each optional); y =
-    rmsnorm(r) * w_pre (None without w_pre).  x, z: (..., dim), float32 or
+    rmsnorm(r) * w_pre (None without w_pre; with z but no w_post the norm of
+    the gated row).  x, z: (..., dim), float32 or
     bfloat16; residual: the same or float32, and r with it; w_post, scale,
     w_pre: (dim,) fp32.  x, z and residual may be slices of wider rows.
     ``r`` may be the residual itself (in place).  Returns ``(r, y)``."""
