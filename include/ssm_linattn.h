@@ -175,7 +175,7 @@ int ssm_linattn_step(float *state, const void *q, int64_t q_stride, const void *
  *               w_pre, NULL without
  *  dtype        activations;  residual_dtype: residual and r (the
  *               activations' or SSM_DTYPE_F32)
- *  rows >= 0; dim 1..16384, at most 8192 with groups > 1; eps > 0
+ *  0 <= rows < 2^22; dim 1..16384, at most 8192 with groups > 1; eps > 0
  * With z and w_pre but no w_post, y is the norm of the gated row, x silu(z),
  * as Mamba-2 has it.  Squares are summed in fp32: their mean has to lie within
  * its range (elements up to about 1e17).

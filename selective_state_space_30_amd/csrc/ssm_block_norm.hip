@@ -175,7 +175,7 @@ __device__ __forceinline__ void part_means(float (&own)[kP], const NormArgs &p, 
 // Bound by memory.  Measured: 8192 rows of 5120 bf16 in 80 parts with a gate,
 // 252 MB: 41 us on inputs that the caches hold in part, 52 us a call on others
 // (4.9 TB/s; a large copy: 5.2); 8192 rows of 2560 with both norms, gate, scale
-// and an fp32 residual, 57 us (294 MB, 5.1 TB/s); 8 rows of 2560, 3.5 us.
+// and an fp32 residual, 60 us (294 MB, 4.9 TB/s); 8 rows of 2560, 3.5 us.
 template <typename T, typename R, int kN, int kP, int kParts>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p) {
   __shared__ float Buf[2][16][1];
@@ -258,10 +258,13 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p) {
 
 // The row's inputs stay as they are in memory (packed) until they are used,
 // and the next row's are asked for before this row's sums.  Measured: 8192
-// rows of 2560, both norms, gate, scale, fp32 residual, 126 us (462 MB, 3.7
-// TB/s; 175 us without the early loads); bound by the instructions of a
-// workgroup's 5 waves on 4 SIMDs, since the sums for the weights leave room
-// for one workgroup a CU.  (With those sums in LDS, two a CU: 181 to 211 us.)
+// rows of 2560, both norms, gate, scale, fp32 residual, 134 us on inputs that
+// the caches do not hold (462 MB, 3.4 TB/s), 126 us on others (175 us without
+// the early loads).  The sums for the weights leave room for one workgroup a
+// CU, whose 5 waves on 4 SIMDs issue vector instructions 36 % of the time (58 %
+// on the SIMD with two) and wait 46 % of their cycles.  (With those sums in LDS,
+// two a CU: 181 to 211 us.)  1001 rows of 1537 in fp32, both norms and scale: 27
+// us; a row a workgroup, so that 18 of the 31 MB written are partial sums.
 template <typename T, typename R, int kN, int kP, int kParts, int kBound>
 __global__ __launch_bounds__(kBound, sizeof(R) == 2 && kN == 8 ? 3 : 1) void norm_bwd_kernel(NormArgs p) {
   __shared__ float Buf1[16][1];

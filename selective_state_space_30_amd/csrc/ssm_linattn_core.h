@@ -398,15 +398,17 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t v, int off, f32x4 
 // Why so: every operand is read from memory once (q and k once for two heads,
 // or once for each 128 columns), and neither the states inside a segment nor
 // the pairs ever leave the CU.  Two workgroups of 8 waves fill a CU's
-// registers.  What bounds it: the instructions around the matrix ones, about
-// 500 vector instructions (weights, packing, splitting, addresses) against 62
-// to 78 matrix instructions a wave and chunk; the matrix cores are busy a
-// fifth of the time.  Measured, bf16:
+// registers.  What bounds it: no unit alone.  In the output pass the vector
+// units issue 36 % of the time (530 vector instructions -- weights, packing,
+// splitting, addresses -- against 80 matrix ones a wave and chunk), LDS works
+// 37 % (a third of it bank conflicts; the states' pass has none), the matrix
+// cores 18 %, and the waves wait 56 % of their cycles: the phases of a chunk
+// follow one another, with two barriers.  Measured, bf16 (kernel trace, median
+// over inputs in turn):
 //   2 x 4096 tokens, 80 heads of 64 on states of 128, one q and k: output
-//   pass 102 us (180 MB, 1.8 TB/s; 32 GFLOP, 316 TFLOP/s), states 48 us;
-//   65536 tokens, 8 heads of 128 on 128: 138 to 160 us (537 MB, 3.4 to 3.9
-//   TB/s), states 72 us;
-//   24 prompts of 16384 tokens together, 16 heads of 128 on 128: 107 and 41 us.
+//   pass 117 us (180 MB, 1.5 TB/s; 32 GFLOP, 276 TFLOP/s), states 52 us;
+//   65536 tokens, 8 heads of 128 on 128: 163 us (537 MB, 3.3 TB/s), states 80 us;
+//   24 prompts of 16384 tokens together, 16 heads of 128 on 128: 118 and 45 us.
 // Tiles of 4 waves, 2 columns of tiles a wave, or the next chunk's loads
 // behind the products were all slower.
 //
@@ -428,7 +430,7 @@ struct CoreShared {
   static constexpr bool kOut = kMode != kLinState;
   // row strides: 8 banks apart for the transposing reads and those of 16
   // bytes, 4 for those of 8 bytes (cycles a read, measured: 2 and 4, with the
-  // other stride 4 and 8)
+  // other stride 4 and 8); q is read both ways
   static constexpr int kRowQ = kDK + (Tr::kBf16 ? 8 : 4), kRowK = kDK + (Tr::kBf16 ? 16 : 4);
   static constexpr int kRowV = kCols + (Tr::kBf16 ? 16 : 4), kRowP = C + (Tr::kBf16 ? 8 : 4);
   alignas(16) Elem Qs[kOut ? C * kRowQ : 8];
@@ -1043,10 +1045,12 @@ int launch_states(const LinCore &a, const LinCore *back, hipStream_t s) {
 // workgroup size; the pairs' short workgroups come last: they fill what the
 // long ones leave, where the same sums inside dv's pass made it the longest of
 // the three.  Measured, bf16, with the decay's gradient: 2 x 2048 tokens, 16
-// heads of 128 on states of 128, 98 us (187 MB of the step's inputs and
+// heads of 128 on states of 128, 104 us (187 MB of the step's inputs and
 // outputs); 4 x 2000 tokens, 24 heads of 64 on states of 128 and one q and k,
-// 155 us.  Bound as the forward pass, and by 8 registers a lane that do not
-// fit (the dot products' rows) and go through scratch memory once a chunk.
+// 153 us.  Bound as the forward pass (vector issue 34 and 49 % of the time,
+// waves wait 53 and 50 % of their cycles), and for heads of 128 by 16 registers
+// a lane that do not fit (the dot products' rows) and go through scratch memory
+// once a chunk.
 template <typename T, int kDKv, int kDKq, int kWaves, int kHeads, bool kDots, bool kVec>
 __global__ __launch_bounds__(64 * kWaves, waves_per_simd(kDKv > kDKq ? kDKv : kDKq)) void
 linattn_grads_kernel(LinCore dq, LinCore dk, LinCore dv, LinPairs pr, unsigned n, unsigned nv) {
