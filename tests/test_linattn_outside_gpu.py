@@ -98,3 +98,41 @@ def test_zeros_reach_only_the_rows_outside():
         inside = slice(offsets[0], offsets[-1])
         assert torch.equal(rows[inside], want.view(tokens, -1)[inside])
         assert (buf[:at] == 5.0).all() and (buf[at + n:] == 5.0).all()
+
+
+def test_captured_with_its_own_outputs():
+    """Packed calls that allocate what they return, captured once and replayed
+    over other inputs and offsets, with eager work between."""
+    dtype, offsets, tokens, heads, qk_heads, dk, dv, decay = CASES[0]
+    t = list(_inputs(*((dtype,) + CASES[0][2:])))
+    cu = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+
+    def run():
+        q, k, v, g, do = t
+        o, h = ssm.ssm_linattn_fwd(q, k, v, g, cu_seqlens=cu)
+        d = ssm.ssm_linattn_bwd(q, k, v, g, cu_seqlens=cu, do=do)
+        part = ssm.ssm_linattn_bwd(q, k, v, g, cu_seqlens=cu, do=do,
+                                   out={"dv": torch.full_like(v, 3.0)})
+        return [o, h] + [d[n] for n in sorted(d)] + [part[n] for n in sorted(part)]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            got = run()
+    torch.cuda.current_stream().wait_stream(side)
+    for replay, cut in enumerate(([0, 3, 70, 400], [100, 130, 131, 399], [5, 5, 5, 5])):
+        for x in t:
+            x.copy_(x.flip(0) if replay else x * 0.5)
+        cu.copy_(torch.tensor(cut, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), replay
+        for a in (got[0], *got[2:7]):
+            if a.shape[0] == tokens:
+                assert (a[:cut[0]] == 0).all() and (a[cut[-1]:] == 0).all(), replay
