@@ -36,10 +36,11 @@
  * nseq rows; with it (device, int32, nseq + 1 offsets, not falling, within
  * 0..tokens) sequence i is rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1, of
  * any length, 0 included.  Rows before the first and behind the last
- * sequence are not read, and written only with SSM_FLAG_ZERO_OUTSIDE.  The offsets are not checked
- * (that would need a synchronisation): ones outside 0..tokens are brought
- * into that range and a falling one ends its sequence, so that no memory
- * outside the arrays is touched, but results are then unspecified.
+ * sequence are not read, and written only with SSM_FLAG_ZERO_OUTSIDE.  The
+ * offsets are not checked (that would need a synchronisation): ones outside
+ * 0..tokens are brought into that range and a falling one ends its sequence, so
+ * that no memory outside the arrays is touched, but results are then
+ * unspecified.
  */
 #ifndef SSM_LINATTN_H
 #define SSM_LINATTN_H
