@@ -34,6 +34,14 @@ Names follow the C ABI:
 * :func:`ssm_block_norm_fwd`, :func:`ssm_block_norm_bwd` -- the norms after a
   mixer and before the next block fused with gate, scale and residual, and
   their gradients; :func:`ssm_block_norm_bwd_workspace_size`.
+* :func:`ssm_embed_fwd`, :func:`ssm_embed_bwd` -- the embedding and the
+  gradient of its weight (``include/ssm_model.h``);
+  :func:`ssm_embed_bwd_workspace_size`.
+* :func:`ssm_layer_norm_fwd`, :func:`ssm_layer_norm_bwd` -- the residual sum
+  and the layer norm after it, and their gradients;
+  :func:`ssm_layer_norm_bwd_workspace_size`.
+* :func:`ssm_grad_norm`, :func:`ssm_grad_clip` -- the norm of all gradients
+  together, and their clipping; :func:`ssm_grad_workspace_size`.
 * :func:`ssm_scan_plan`, :func:`ssm_scan_workspace_size`,
   :func:`ssm_last_error`, :func:`ssm_abi_version`.
 * :func:`ssm_roofline_hbm`, :func:`ssm_roofline_valu` -- microbenchmarks of
@@ -60,6 +68,9 @@ SSM_FLAG_ZOH_B = 2
 SSM_FLAG_BWD_SAVED = 4
 SSM_FLAG_HEAD_DECAY = 8
 SSM_FLAG_ZERO_OUTSIDE = 32
+SSM_FLAG_ACCUMULATE = 64
+SSM_INDEX_I32 = 0
+SSM_INDEX_I64 = 1
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_INVALID_ARG", 2: "SSM_ERR_UNSUPPORTED",
           3: "SSM_ERR_WORKSPACE", 4: "SSM_ERR_HIP"}
 EXPORTS = ("ssm_abi_version", "ssm_scan_plan", "ssm_scan_workspace_size",
@@ -73,7 +84,11 @@ EXPORTS = ("ssm_abi_version", "ssm_scan_plan", "ssm_scan_workspace_size",
            "ssm_linattn_plan", "ssm_linattn_workspace_size", "ssm_linattn_fwd",
            "ssm_linattn_bwd_workspace_size", "ssm_linattn_bwd", "ssm_linattn_step",
            "ssm_block_norm_fwd", "ssm_block_norm_bwd_workspace_size",
-           "ssm_block_norm_bwd")
+           "ssm_block_norm_bwd",
+           "ssm_embed_fwd", "ssm_embed_bwd_workspace_size", "ssm_embed_bwd",
+           "ssm_layer_norm_fwd", "ssm_layer_norm_bwd_workspace_size",
+           "ssm_layer_norm_bwd",
+           "ssm_grad_workspace_size", "ssm_grad_norm", "ssm_grad_clip")
 SCAN_SCRATCH_BYTES = 16 << 20  # the fixed scratch of ssm_scan_fwd_noalloc
 SSM_ROOFLINE_HBM_QUANTUM = 16384
 SSM_ROOFLINE_VALU_QUANTUM = 256
@@ -189,6 +204,26 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.ssm_block_norm_bwd.argtypes = (norm + [P] * 8 +
                                            [I64, I64, I64, F, I, I, P, SZ, P])
         lib.ssm_block_norm_bwd.restype = I
+        lib.ssm_embed_fwd.argtypes = [P, P, I64, P, I64, I64, I64, F, I, I, I, P]
+        lib.ssm_embed_fwd.restype = I
+        lib.ssm_embed_bwd_workspace_size.argtypes = [I64, I64, I64, ctypes.POINTER(SZ)]
+        lib.ssm_embed_bwd_workspace_size.restype = I
+        lib.ssm_embed_bwd.argtypes = [P, P, I64, P, I64, I64, I64, F, U, I, I, I, P, SZ, P]
+        lib.ssm_embed_bwd.restype = I
+        lib.ssm_layer_norm_fwd.argtypes = (side * 2 + [P] * 4 +
+                                           [I64, I64, F, I, I, I, P])
+        lib.ssm_layer_norm_fwd.restype = I
+        lib.ssm_layer_norm_bwd_workspace_size.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+        lib.ssm_layer_norm_bwd_workspace_size.restype = I
+        lib.ssm_layer_norm_bwd.argtypes = (side * 2 + [P] * 7 +
+                                           [I64, I64, F, I, I, I, P, SZ, P])
+        lib.ssm_layer_norm_bwd.restype = I
+        lib.ssm_grad_workspace_size.argtypes = [ctypes.POINTER(SZ)]
+        lib.ssm_grad_workspace_size.restype = I
+        lib.ssm_grad_norm.argtypes = [P, P, P, I64, P, P, SZ, P]
+        lib.ssm_grad_norm.restype = I
+        lib.ssm_grad_clip.argtypes = [P, P, P, P, P, I64, F, I, P, P, SZ, P]
+        lib.ssm_grad_clip.restype = I
         lib.ssm_last_error.argtypes = []
         lib.ssm_last_error.restype = ctypes.c_char_p
         if path is None:
@@ -770,8 +805,9 @@ def ssm_roofline_valu(kind, out, iters, stream=None):
 
 # ---------------------------------------------------------- linear attention
 def _on_device(fn):
-    """Runs the wrapper with its first argument's device as the current one
-    (kernels are launched on the current device), and with ``stream`` (when
+    """Runs the wrapper with the device of its first argument (or of a list's
+    first tensor) as the current one (kernels are launched on the current
+    device), and with ``stream`` (when
     given) as torch's current stream, as :func:`_on_stream` does."""
     inner = _on_stream(fn)
     names = list(inspect.signature(fn).parameters)
@@ -780,6 +816,8 @@ def _on_device(fn):
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         t = args[0] if args else kwargs.get(first)
+        if t.__class__ is list or t.__class__ is tuple:
+            t = t[0] if t else None
         stream = args[at] if len(args) > at else kwargs.get("stream")
         call = fn if stream is None else inner
         if (isinstance(t, torch.Tensor) and t.is_cuda
@@ -1152,3 +1190,274 @@ def ssm_block_norm_bwd(x, w_post=None, z=None, scale=None, residual=None,
         p.get("dw_pre"), rows, dim, groups, eps, code, rcode, ws, ws_bytes,
         _raw_stream(dev, stream)))
     return {name: out[name] for name in shapes}
+
+
+# ----------------------------------------------------------------- embedding
+def ssm_embed_bwd_workspace_size(tokens, vocab, dim) -> int:
+    return _size(load_library().ssm_embed_bwd_workspace_size, tokens, vocab, dim)
+
+
+def _ids(ids):
+    """Address, type code and number of the ids of a call."""
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype is torch.int64:
+        code = SSM_INDEX_I64
+    elif ids.dtype is torch.int32:
+        code = SSM_INDEX_I32
+    else:
+        raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+    if not ids.is_cuda:
+        raise ValueError("ids must be a device (HIP) tensor")
+    return _dense(ids, "ids", ids.dtype, ids.shape, ids.device), code, ids.numel()
+
+
+@_on_device
+def ssm_embed_fwd(ids, weight, scale=1.0, out=None, dtype=None, stream=None):
+    """Rows of the embedding: out[t] = scale * weight[ids[t]].
+
+    ids: int32 or int64, any shape; an id outside 0..vocab-1 (padding) gives a
+    row of zeros.  weight: (vocab, dim), float32 or bfloat16, rows may be
+    slices of wider ones.  ``dtype``: of the result (weight's by default; the
+    other of the two is allowed).  Returns out, ids.shape + (dim,)."""
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be (vocab, dim)")
+    p_ids, index, tokens = _ids(ids)
+    dev = ids.device
+    vocab, dim = weight.shape
+    w, w_stride = _rows(weight, "weight", weight.dtype, (vocab,), (dim,), dev)
+    shape = ids.shape + (dim,)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or weight.dtype, device=dev)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError("out must be %s, got %s" % (dtype, out.dtype))
+    _check(load_library().ssm_embed_fwd(
+        p_ids, w, w_stride, _dense(out, "out", out.dtype, shape, dev), tokens, vocab, dim,
+        float(scale), index, _code(weight.dtype), _code(out.dtype), _raw_stream(dev, stream)))
+    return out
+
+
+@_on_device
+def ssm_embed_bwd(ids, dy, vocab, scale=1.0, dweight=None, accumulate=False,
+                  dtype=torch.float32, workspace=None, stream=None):
+    """Gradient of :func:`ssm_embed_fwd`'s weight for a gradient ``dy`` of its
+    result (ids.shape + (dim,), float32 or bfloat16, rows may be slices of
+    wider ones): dweight[v] = scale * sum of dy[t] where ids[t] = v, in fp32 in
+    a fixed order.  ``accumulate`` adds it to the given ``dweight`` (vocab, dim)
+    in place, whose rows without a token are not touched.  ``dtype``: of a new
+    dweight, float32 or bfloat16.  Returns dweight."""
+    p_ids, index, tokens = _ids(ids)
+    dev = ids.device
+    if not isinstance(dy, torch.Tensor) or dy.dim() < 1:
+        raise TypeError("dy must be a torch.Tensor (..., dim)")
+    dim = dy.shape[-1]
+    p_dy, dy_stride = _rows(dy, "dy", dy.dtype, ids.shape, (dim,), dev)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs dweight")
+        dweight = torch.empty((vocab, dim), dtype=dtype, device=dev)
+    lib = load_library()
+    keep, ws, ws_bytes = _scratch(
+        workspace, _size(lib.ssm_embed_bwd_workspace_size, tokens, vocab, dim), dev)
+    _check(lib.ssm_embed_bwd(
+        p_ids, p_dy, dy_stride, _dense(dweight, "dweight", dweight.dtype, (vocab, dim), dev),
+        tokens, vocab, dim, float(scale), SSM_FLAG_ACCUMULATE if accumulate else 0, index,
+        _code(dy.dtype), _code(dweight.dtype), ws, ws_bytes, _raw_stream(dev, stream)))
+    return dweight
+
+
+# ---------------------------------------------------------------- layer norm
+def ssm_layer_norm_bwd_workspace_size(rows, dim) -> int:
+    return _size(load_library().ssm_layer_norm_bwd_workspace_size, rows, dim)
+
+
+def _layer_norm_args(x, residual, weight, bias):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor (..., dim)")
+    dev, act, f32 = x.device, x.dtype, torch.float32
+    if dev.type != "cuda":
+        raise ValueError("x must be a device (HIP) tensor")
+    lead, dim = x.shape[:-1], x.shape[-1]
+    rows = 1
+    for n in lead:
+        rows *= n
+    args = _rows(x, "x", act, lead, (dim,), dev)
+    rdt = act
+    if residual is None:
+        args += (None, 0)
+    else:
+        rdt = residual.dtype
+        args += _rows(residual, "residual", rdt, lead, (dim,), dev)
+    return (args, _dense(weight, "weight", f32, (dim,), dev),
+            _dense(bias, "bias", f32, (dim,), dev), rows, dim, _code(act), _code(rdt), rdt)
+
+
+@_on_device
+def ssm_layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5,
+                       r=None, y=None, dtype=None, stream=None):
+    """The residual sum and the layer norm after it, per row:
+    r = x + residual, y = (r - mean(r)) / sqrt(var(r) + eps) * weight + bias.
+
+    x: (..., dim), float32 or bfloat16; residual: the same or float32, and r
+    with it; weight, bias: (dim,) fp32 or None; ``dtype``: of y (x's by
+    default; bfloat16 with a float32 x).  x and residual may be slices of wider
+    rows.  ``r`` may be the residual itself (in place).  Returns ``(r, y)``; r
+    is x itself without a residual."""
+    args, w, b, rows, dim, code, rcode, rdt = _layer_norm_args(x, residual, weight, bias)
+    dev = x.device
+    if residual is None:
+        if r is not None:
+            raise ValueError("r without a residual")
+        p_r = None
+    else:
+        if r is None:
+            r = torch.empty(x.shape, dtype=rdt, device=dev)
+        p_r = _dense(r, "r", rdt, x.shape, dev)
+    if y is None:
+        y = torch.empty(x.shape, dtype=dtype or x.dtype, device=dev)
+    elif dtype is not None and y.dtype != dtype:
+        raise TypeError("y must be %s, got %s" % (dtype, y.dtype))
+    _check(load_library().ssm_layer_norm_fwd(
+        *args, w, b, p_r, _dense(y, "y", y.dtype, x.shape, dev), rows, dim, eps, code, rcode,
+        _code(y.dtype), _raw_stream(dev, stream)))
+    return x if residual is None else r, y
+
+
+@_on_device
+def ssm_layer_norm_bwd(x, weight=None, bias=None, residual=None, eps=1e-5,
+                       dr=None, dy=None, out=None, workspace=None, stream=None):
+    """Gradients of :func:`ssm_layer_norm_fwd`, from its inputs, for gradients
+    ``dr`` of r (r's type, or None) and ``dy`` of y.  Returns a dict: dx, and
+    for each input given dresidual, dweight, dbias.  The gradient of x and that
+    of the residual are the same numbers: where their types are the same too,
+    dresidual is dx itself, one tensor.  A caller that kept r alone gives it
+    as x, without a residual.  ``out`` may supply any of them."""
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch.Tensor")
+    args, w, b, rows, dim, code, rcode, rdt = _layer_norm_args(x, residual, weight, bias)
+    dev, act, f32 = x.device, x.dtype, torch.float32
+    given = out or {}
+    shapes = {"dx": (x.shape, act)}
+    shared = residual is not None and rdt == act and "dresidual" not in given
+    if residual is not None and not shared:
+        shapes["dresidual"] = (x.shape, rdt)
+    if weight is not None:
+        shapes["dweight"] = ((dim,), f32)
+    if bias is not None:
+        shapes["dbias"] = ((dim,), f32)
+    out, p = {}, {}
+    for name, (shape, dtype) in shapes.items():
+        t = given.get(name)
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        out[name] = t
+        p[name] = _dense(t, name, dtype, shape, dev)
+    lib = load_library()
+    keep, ws, ws_bytes = _scratch(
+        workspace, _size(lib.ssm_layer_norm_bwd_workspace_size, rows, dim), dev)
+    _check(lib.ssm_layer_norm_bwd(
+        *args, w, _dense(dr, "dr", rdt, x.shape, dev), _dense(dy, "dy", dy.dtype, x.shape, dev),
+        p["dx"], p.get("dresidual"), p.get("dweight"), p.get("dbias"), rows, dim, eps, code, rcode,
+        _code(dy.dtype), ws, ws_bytes, _raw_stream(dev, stream)))
+    if shared:
+        out["dresidual"] = out["dx"]
+    return out
+
+
+# ------------------------------------------- the gradients' norm and clipping
+def ssm_grad_workspace_size() -> int:
+    return _size(load_library().ssm_grad_workspace_size)
+
+
+_GRAD_CODES = {torch.float32: SSM_DTYPE_F32, torch.bfloat16: SSM_DTYPE_BF16}
+
+
+def _fills_its_memory(t):
+    """Whether the elements of t, in some order of its dimensions, lie one after
+    another without gaps."""
+    want = 1
+    for s, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if s != want:
+            return False
+        want *= n
+    return True
+
+
+def _tensors(ts, name, dev):
+    """Host arrays of the addresses, sizes and types of a list of tensors."""
+    ptrs, sizes, codes = [], [], []
+    for i, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s[%d] must be a torch.Tensor" % (name, i))
+        code = _GRAD_CODES.get(t.dtype)
+        if code is None:
+            raise TypeError("%s[%d] must be float32 or bfloat16, got %s" % (name, i, t.dtype))
+        if t.device != dev:
+            raise ValueError("%s[%d] is on %s, expected %s" % (name, i, t.device, dev))
+        if not t.is_contiguous() and not _fills_its_memory(t):
+            raise ValueError("%s[%d] has gaps between its elements" % (name, i))
+        ptrs.append(t.data_ptr())
+        sizes.append(t.numel())
+        codes.append(code)
+    n = len(ptrs)
+    return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*codes)
+
+
+def _grad_device(grads):
+    if isinstance(grads, torch.Tensor):
+        raise TypeError("grads must be a list of tensors")
+    if not grads:
+        return torch.device("cuda", torch.cuda.current_device())
+    if not isinstance(grads[0], torch.Tensor):
+        raise TypeError("grads[0] must be a torch.Tensor")
+    if grads[0].device.type != "cuda":
+        raise ValueError("grads[0] must be a device (HIP) tensor")
+    return grads[0].device
+
+
+@_on_device
+def ssm_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The 2-norm over all elements of a list of tensors, float32 or bfloat16,
+    of any sizes and types side by side, squares summed in 64 bits.  Returns
+    ``norm``, a float32 tensor of no dimensions on the device."""
+    dev = _grad_device(grads)
+    lists = _tensors(grads, "grads", dev)
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    keep, ws, ws_bytes = _scratch(workspace, ssm_grad_workspace_size(), dev)
+    _check(load_library().ssm_grad_norm(
+        *lists, len(grads), _dense(norm, "norm", torch.float32, (), dev), ws, ws_bytes,
+        _raw_stream(dev, stream)))
+    return norm
+
+
+@_on_device
+def ssm_grad_clip(grads, max_norm, norm=None, out=None, workspace=None,
+                  stream=None):
+    """Clips a list of gradients to a 2-norm of ``max_norm`` over all of them:
+    g * min(1, max_norm / norm), in place, or into the tensors of ``out`` (the
+    gradients' shapes; float32 or bfloat16, whatever the gradients' type).
+    ``norm``: a float32 device scalar to take instead of forming it (one that
+    was summed over several processes).  Where the norm is not finite the
+    gradients stay as they are.  Returns the norm before the clipping, a
+    device scalar."""
+    dev = _grad_device(grads)
+    lists = _tensors(grads, "grads", dev)
+    outs, out_codes = None, None
+    if out is not None:
+        if len(out) != len(grads):
+            raise ValueError("out must have as many tensors as grads")
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if o.shape != g.shape or (o.stride() != g.stride() and not (
+                    o.is_contiguous() and g.is_contiguous())):
+                raise ValueError("out[%d] must have the shape and strides of its gradient" % i)
+        outs, _, out_codes = _tensors(out, "out", dev)
+    have = norm is not None
+    keep, ws, ws_bytes = None, None, 0
+    if not have:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        keep, ws, ws_bytes = _scratch(workspace, ssm_grad_workspace_size(), dev)
+    _check(load_library().ssm_grad_clip(
+        *lists, outs, out_codes, len(grads), float(max_norm), int(have),
+        _dense(norm, "norm", torch.float32, (), dev), ws, ws_bytes, _raw_stream(dev, stream)))
+    return norm

@@ -48,8 +48,9 @@ HIP_SOURCES = ["ssm_kernels.hip", "ssm_step.hip", "ssm_bwd.hip", "ssm_ssd.hip",
                "ssm_roofline.hip", "ssm_conv_bwd.hip", "ssm_linattn.hip",
                "ssm_linattn_out_bf16.hip", "ssm_linattn_out_f32.hip",
                "ssm_linattn_grads_bf16.hip", "ssm_linattn_grads_f32.hip",
-               "ssm_block_norm.hip"]
-CPP_SOURCES = ["ssm_api.cpp", "ssm_linattn_api.cpp"]
+               "ssm_block_norm.hip", "ssm_embed.hip", "ssm_layer_norm.hip",
+               "ssm_grad.hip"]
+CPP_SOURCES = ["ssm_api.cpp", "ssm_linattn_api.cpp", "ssm_model_api.cpp"]
 
 
 def build(verbose: bool = False) -> str:

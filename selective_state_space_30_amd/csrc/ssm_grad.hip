@@ -1,0 +1,200 @@
+// ssm_grad.hip -- gfx950 kernels of the gradients' global norm and clipping.
+//
+//   norm = sqrt(sum g^2),  g' = g min(1, max_norm / norm)
+//
+// Tensors are cut into chunks, which a launch's workgroups take in turn; the
+// table of tensors travels in the launch's arguments.  Each workgroup adds the
+// squares of its chunks in 64 bits to a sum of its own, and every workgroup of
+// the clipping launch adds those sums, all in the same order, so no launch of
+// one workgroup stands between the two.
+#include "ssm_model_internal.h"
+#include "ssm_pieces.h"
+
+namespace ssm {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Sum over the workgroup, the same in every thread.
+__device__ __forceinline__ double block_sum64(double v, double *buf) {
+  v = wave_sum64(v);
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) v += buf[w];
+  return v;
+}
+
+__device__ __forceinline__ double sum_of_squares(const double *sums, int n, double *buf) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) v += sums[i];
+  return block_sum64(v, buf);
+}
+
+// Tensor of a chunk.
+__device__ __forceinline__ int tensor_of(const GradTable &t, uint32_t chunk) {
+  int lo = 0, hi = t.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (t.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T *g, int64_t n) {
+  double acc[2] = {0.0, 0.0};
+  int64_t at = static_cast<int64_t>(threadIdx.x) * 8;
+  auto add = [&](const Piece<T, 8> &x) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double v = static_cast<double>(x[e]);
+      acc[e % 2] = fma(v, v, acc[e % 2]);
+    }
+  };
+  for (; at + 3 * kThreads * 8 + 8 <= n; at += 4 * kThreads * 8) {
+    Piece<T, 8> x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k].load(g + at + k * kThreads * 8);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add(x[k]);
+  }
+  for (; at < n; at += kThreads * 8) {
+    Piece<T, 8> x;
+    if (at + 8 <= n)
+      x.load(g + at);
+    else
+      x.load_some(g + at, static_cast<int>(n - at));
+    add(x);
+  }
+  return acc[0] + acc[1];
+}
+
+__global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradTable t, double *sums,
+                                                               int first) {
+  __shared__ double Buf[kThreads / 64];
+  double acc = 0.0;
+  for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
+    const int k = tensor_of(t, c);
+    const int64_t from = static_cast<int64_t>(c - t.first[k]) * kGradChunk;
+    const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
+    const int64_t n = size < kGradChunk ? size : kGradChunk;
+    if (t.size[k] & kGradBf16)
+      acc += chunk_squares(static_cast<const uint16_t *>(t.grad[k]) + from, n);
+    else
+      acc += chunk_squares(static_cast<const float *>(t.grad[k]) + from, n);
+  }
+  acc = block_sum64(acc, Buf);
+  if (threadIdx.x == 0) sums[blockIdx.x] = first ? acc : sums[blockIdx.x] + acc;
+}
+
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double *sums, int n, float *norm) {
+  __shared__ double Buf[kThreads / 64];
+  const double v = sum_of_squares(sums, n, Buf);
+  if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(v));
+}
+
+template <typename T, typename W>
+__device__ __forceinline__ void scale_chunk(const T *g, W *out, int64_t n, float c) {
+  auto put = [&](const Piece<T, 8> &x, int64_t at) __attribute__((always_inline)) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = x[e] * c;
+    Piece<W, 8> y;
+    y.set(v);
+    if (at + 8 <= n)
+      y.store(out + at);
+    else
+      y.store_some(out + at, static_cast<int>(n - at));
+  };
+  int64_t at = static_cast<int64_t>(threadIdx.x) * 8;
+  for (; at + 3 * kThreads * 8 + 8 <= n; at += 4 * kThreads * 8) {
+    Piece<T, 8> x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k].load(g + at + k * kThreads * 8);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) put(x[k], at + k * kThreads * 8);
+  }
+  for (; at < n; at += kThreads * 8) {
+    Piece<T, 8> x;
+    if (at + 8 <= n)
+      x.load(g + at);
+    else
+      x.load_some(g + at, static_cast<int>(n - at));
+    put(x, at);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable t, GradOuts o, int in_place,
+                                                             const double *sums, int nsums,
+                                                             float max_norm, float *norm,
+                                                             int write_norm) {
+  __shared__ double Buf[kThreads / 64];
+  const double total = sums ? sqrt(sum_of_squares(sums, nsums, Buf)) : static_cast<double>(*norm);
+  const float shown = static_cast<float>(total);
+  if (sums && write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = shown;
+  // a norm that is infinite, NaN, or not above max_norm leaves the gradients
+  const bool finite = shown < __builtin_huge_valf();
+  const double limit = static_cast<double>(max_norm);
+  const float c = finite && total > limit ? static_cast<float>(limit / total) : 1.0f;
+  if (in_place && c == 1.0f) return;
+  for (uint32_t i = blockIdx.x; i < t.first[t.n]; i += gridDim.x) {
+    const int k = tensor_of(t, i);
+    const int64_t from = static_cast<int64_t>(i - t.first[k]) * kGradChunk;
+    const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
+    const int64_t n = size < kGradChunk ? size : kGradChunk;
+    const void *g = t.grad[k];
+    void *out = o.out[k];
+    if (t.size[k] & kGradBf16) {
+      const uint16_t *x = static_cast<const uint16_t *>(g) + from;
+      if (t.size[k] & kGradOutBf16)
+        scale_chunk(x, static_cast<uint16_t *>(out) + from, n, c);
+      else
+        scale_chunk(x, static_cast<float *>(out) + from, n, c);
+    } else {
+      const float *x = static_cast<const float *>(g) + from;
+      if (t.size[k] & kGradOutBf16)
+        scale_chunk(x, static_cast<uint16_t *>(out) + from, n, c);
+      else
+        scale_chunk(x, static_cast<float *>(out) + from, n, c);
+    }
+  }
+}
+
+}  // namespace
+
+int launch_grad_squares(const GradTable &t, double *sums, int nsums, bool first, void *stream) {
+  hipLaunchKernelGGL(grad_squares_kernel, dim3(nsums), dim3(kThreads), 0,
+                     static_cast<hipStream_t>(stream), t, sums, first ? 1 : 0);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_grad_norm(const double *sums, int nsums, float *norm, void *stream) {
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kThreads), 0,
+                     static_cast<hipStream_t>(stream), sums, nsums, norm);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_grad_scale(const GradTable &t, const GradOuts &outs, bool in_place, const double *sums,
+                      int nsums, float max_norm, float *norm, bool write_norm, void *stream) {
+  const uint32_t chunks = t.first[t.n];
+  const unsigned grid = chunks < 1 ? 1 : chunks < 2 * kGradGroups ? chunks : 2 * kGradGroups;
+  hipLaunchKernelGGL(grad_scale_kernel, dim3(grid), dim3(kThreads), 0,
+                     static_cast<hipStream_t>(stream), t, outs, in_place ? 1 : 0, sums, nsums,
+                     max_norm, norm, write_norm ? 1 : 0);
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace ssm

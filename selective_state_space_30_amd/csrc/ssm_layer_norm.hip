@@ -1,0 +1,359 @@
+// ssm_layer_norm.hip -- gfx950 kernels of the layer norm with the residual sum
+// before it, and of its gradient.
+//
+// Per row of dim elements:
+//   r = x + residual,  m = mean(r),  s = 1 / sqrt(mean((r - m)^2) + eps)
+//   y = (r - m) s weight + bias
+// Backward, with h = (r - m) s and g = dy weight:
+//   D = dr + s (g - mean(g) - h mean(g h))      (= dx = dresidual)
+//   dweight = sum_rows dy h,  dbias = sum_rows dy
+//
+// The row is held in registers in fp32 by a group of lanes, kP pieces of kN
+// elements each: 8 to 64 lanes of a wave, whose sums need no barrier, or a
+// workgroup of up to 8 waves, whose sums meet in LDS.  The mean is formed
+// first and the squares from the differences, so that a mean far from 0 costs
+// no digits.
+#include "ssm_model_internal.h"
+#include "ssm_pieces.h"
+
+namespace ssm {
+namespace {
+
+using namespace dev;
+
+// Sums of v over the group, the same in every lane.  `lanes` over 64: the
+// workgroup.  `turn` is another one of the buffers at each call, of which two
+// calls in a row have different ones: a wave writes again only behind a
+// barrier that the readers have passed.
+template <int kK>
+__device__ __forceinline__ void row_sums(float (&v)[kK], int lanes, float (*buf)[8][2], int &turn) {
+#pragma unroll
+  for (int k = 0; k < kK; ++k) v[k] = group_sum(v[k], lanes);
+  if (lanes <= 64) return;
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < kK; ++k) buf[turn][wave][k] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kK; ++k) v[k] = 0.0f;
+  for (int w = 0; w < waves; ++w)
+#pragma unroll
+    for (int k = 0; k < kK; ++k) v[k] += buf[turn][w][k];
+  turn ^= 1;
+}
+
+// r - mean in v (0 behind the row's end), and s.  The mean of the differences,
+// which is what the first mean's rounding left, is taken from both.
+template <int kP, int kN>
+__device__ __forceinline__ float centre(float (&v)[kP][kN], const LayerNormArgs &p, int lanes,
+                                        int at, float (*buf)[8][2], int &turn) {
+  const float n = static_cast<float>(p.dim);
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < kP; ++i)
+#pragma unroll
+    for (int e = 0; e < kN; ++e) s[0] += v[i][e];
+  row_sums<1>(s, lanes, buf, turn);
+  const float mean = s[0] / n;
+  float t[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int left = p.dim - (at + i * lanes) * kN;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      v[i][e] = e < left ? v[i][e] - mean : 0.0f;
+      t[0] += v[i][e];
+      t[1] = fmaf(v[i][e], v[i][e], t[1]);
+    }
+  }
+  row_sums<2>(t, lanes, buf, turn);
+  const float rest = t[0] / n;
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int left = p.dim - (at + i * lanes) * kN;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) v[i][e] = e < left ? v[i][e] - rest : 0.0f;
+  }
+  return 1.0f / sqrtf(fmaf(-rest, rest, t[1] / n) + p.eps);
+}
+
+template <typename T, typename R, typename Y, int kN, int kP>
+__global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, int lanes) {
+  __shared__ float Buf[2][8][2];
+  int turn = 0;
+  const int at = threadIdx.x & (lanes - 1);
+  const int pieces = (p.dim + kN - 1) / kN;
+  const int per = lanes < static_cast<int>(blockDim.x) ? blockDim.x / lanes : 1;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes; row < p.rows;
+       row += step) {
+    float v[kP][kN];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int q = at + i * lanes;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) v[i][e] = 0.0f;
+      if (q < pieces) {
+        get_piece<T, kN>(static_cast<const T *>(p.x) + row * p.x_stride, q, p.dim, v[i]);
+        if (p.residual) {
+          float t[kN];
+          get_piece<R, kN>(static_cast<const R *>(p.residual) + row * p.r_stride, q, p.dim, t);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[i][e] += t[e];
+        }
+      }
+    }
+    if (p.r)
+#pragma unroll
+      for (int i = 0; i < kP; ++i)
+        if (at + i * lanes < pieces)
+          store_piece<R, kN>(static_cast<R *>(p.r) + row * p.dim, at + i * lanes, p.dim, v[i]);
+    const float s = centre<kP, kN>(v, p, lanes, at, Buf, turn);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int q = at + i * lanes;
+      if (q >= pieces) continue;
+      float w[kN], b[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        w[e] = 1.0f;
+        b[e] = 0.0f;
+      }
+      if (p.weight) get_piece<float, kN>(p.weight, q, p.dim, w);
+      if (p.bias) get_piece<float, kN>(p.bias, q, p.dim, b);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) w[e] = fmaf(v[i][e] * s, w[e], b[e]);
+      store_piece<Y, kN>(static_cast<Y *>(p.y) + row * p.dim, q, p.dim, w);
+    }
+  }
+}
+
+// The sums for the weights' gradients of a lane's columns stay in registers
+// over the rows that its group takes; at the end the workgroup's groups are
+// added in LDS in a fixed order and leave one partial row.
+template <typename T, typename R, typename Y, int kN, int kP>
+__global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, int lanes) {
+  __shared__ float Buf[2][8][2];
+  __shared__ float Sums[2 * kN * kP * 64];
+  int turn = 0;
+  const int at = threadIdx.x & (lanes - 1);
+  const int pieces = (p.dim + kN - 1) / kN;
+  const int per = lanes < static_cast<int>(blockDim.x) ? blockDim.x / lanes : 1;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  float w[kP][kN], gw[kP][kN], gb[kP][kN];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int q = at + i * lanes;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      w[i][e] = 1.0f;
+      gw[i][e] = gb[i][e] = 0.0f;
+    }
+    if (p.weight && q < pieces) get_piece<float, kN>(p.weight, q, p.dim, w[i]);
+  }
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes; row < p.rows;
+       row += step) {
+    float v[kP][kN];
+    Piece<Y, kN> dy[kP];
+    Piece<R, kN> dr[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int q = at + i * lanes;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) v[i][e] = 0.0f;
+      dy[i].zero();
+      dr[i].zero();
+      if (q < pieces) {
+        get_piece<T, kN>(static_cast<const T *>(p.x) + row * p.x_stride, q, p.dim, v[i]);
+        if (p.residual) {
+          float t[kN];
+          get_piece<R, kN>(static_cast<const R *>(p.residual) + row * p.r_stride, q, p.dim, t);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[i][e] += t[e];
+        }
+        load_piece(dy[i], static_cast<const Y *>(p.dy) + row * p.dim, q, p.dim);
+        if (p.dr) load_piece(dr[i], static_cast<const R *>(p.dr) + row * p.dim, q, p.dim);
+      }
+    }
+    const float s = centre<kP, kN>(v, p, lanes, at, Buf, turn);
+    float m[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kP; ++i)
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        v[i][e] *= s;
+        const float d = dy[i][e], g = d * w[i][e];
+        gb[i][e] += d;
+        gw[i][e] = fmaf(d, v[i][e], gw[i][e]);
+        m[0] += g;
+        m[1] = fmaf(g, v[i][e], m[1]);
+      }
+    row_sums<2>(m, lanes, Buf, turn);
+    m[0] *= inv;
+    m[1] *= inv;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int q = at + i * lanes;
+      if (q >= pieces) continue;
+      float d[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        d[e] = fmaf(s, fmaf(-m[1], v[i][e], fmaf(dy[i][e], w[i][e], -m[0])), dr[i][e]);
+      store_piece<T, kN>(static_cast<T *>(p.dx) + row * p.dim, q, p.dim, d);
+      if (p.dresidual)
+        store_piece<R, kN>(static_cast<R *>(p.dresidual) + row * p.dim, q, p.dim, d);
+    }
+  }
+  if (!p.dweight && !p.dbias) return;
+  float *part = p.parts + static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
+  if (lanes < static_cast<int>(blockDim.x)) {
+    // groups inside a wave, then the waves one after another
+#pragma unroll
+    for (int i = 0; i < kP; ++i)
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        for (int d = lanes; d < 64; d *= 2) {
+          gw[i][e] += __shfl_xor(gw[i][e], d);
+          gb[i][e] += __shfl_xor(gb[i][e], d);
+        }
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int waves = blockDim.x >> 6;
+    for (int k = 0; k < waves; ++k) {
+      if (wave == k && lane < lanes)
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+#pragma unroll
+          for (int e = 0; e < kN; ++e) {
+            float *c = Sums + (i * kN + e) * 64 + lane;
+            if (k > 0) {
+              gw[i][e] += c[0];
+              gb[i][e] += c[kN * kP * 64];
+            }
+            c[0] = gw[i][e];
+            c[kN * kP * 64] = gb[i][e];
+          }
+      __syncthreads();
+    }
+    if (wave != waves - 1 || lane >= lanes) return;
+  }
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int q = at + i * lanes;
+    if (q < pieces) {
+      store_piece<float, kN>(part, q, p.dim, gw[i]);
+      store_piece<float, kN>(part + p.dim, q, p.dim, gb[i]);
+    }
+  }
+}
+
+// Sum of the workgroups' partial rows, 32 columns and 32 row groups a
+// workgroup, in a fixed order.
+__global__ __launch_bounds__(1024) void layer_norm_parts_kernel(LayerNormArgs p) {
+  __shared__ float Sums[32][33];
+  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  float *out = blockIdx.y == 0 ? p.dweight : p.dbias;
+  if (!out) return;
+  const int c = blockIdx.x * 32 + lane;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < p.dim) {
+    const float *s = p.parts + static_cast<int64_t>(blockIdx.y) * p.dim + c;
+    const int64_t row = 2 * static_cast<int64_t>(p.dim);
+    int w = grp;
+    for (; w + 96 < p.nparts; w += 128)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] += s[(w + 32 * k) * row];
+    for (; w < p.nparts; w += 32) acc[0] += s[w * row];
+  }
+  Sums[grp][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  __syncthreads();
+  if (grp == 0 && c < p.dim) {
+    float s = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 32; ++g) s += Sums[g][lane];
+    out[c] = s;
+  }
+}
+
+// Lanes of a row's group (a power of two, 8..512) and pieces that each holds.
+struct Shape {
+  int lanes, per, threads;
+};
+Shape shape_of(int dim, int n) {
+  const int pieces = (dim + n - 1) / n, most = n == 8 ? 5 : 8;
+  int lanes = 8;
+  while ((pieces + lanes - 1) / lanes > most) lanes *= 2;
+  return {lanes, (pieces + lanes - 1) / lanes, lanes <= 64 ? 256 : lanes};
+}
+
+template <typename T, typename R, typename Y, int kN, int kP, bool kBack>
+int launch_p(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
+  const int per = sh.threads / sh.lanes;
+  const int64_t groups = (a.rows + per - 1) / per;
+  if constexpr (kBack) {
+    hipLaunchKernelGGL((layer_norm_bwd_kernel<T, R, Y, kN, kP>), dim3(a.nparts), dim3(sh.threads),
+                       0, s, a, sh.lanes);
+  } else {
+    const unsigned grid = static_cast<unsigned>(groups < 65536 ? groups : 65536);
+    hipLaunchKernelGGL((layer_norm_fwd_kernel<T, R, Y, kN, kP>), dim3(grid), dim3(sh.threads), 0,
+                       s, a, sh.lanes);
+  }
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename T, typename R, typename Y, int kN, bool kBack>
+int launch_n(const LayerNormArgs &a, hipStream_t s) {
+  const Shape sh = shape_of(a.dim, kN);
+  switch (sh.per) {
+    case 1: return launch_p<T, R, Y, kN, 1, kBack>(a, sh, s);
+    case 2: return launch_p<T, R, Y, kN, 2, kBack>(a, sh, s);
+    case 3: return launch_p<T, R, Y, kN, 3, kBack>(a, sh, s);
+    case 4: return launch_p<T, R, Y, kN, 4, kBack>(a, sh, s);
+    case 5: return launch_p<T, R, Y, kN, 5, kBack>(a, sh, s);
+  }
+  if constexpr (kN == 4) {
+    switch (sh.per) {
+      case 6: return launch_p<T, R, Y, kN, 6, kBack>(a, sh, s);
+      case 7: return launch_p<T, R, Y, kN, 7, kBack>(a, sh, s);
+      case 8: return launch_p<T, R, Y, kN, 8, kBack>(a, sh, s);
+    }
+  }
+  return static_cast<int>(hipErrorInvalidValue);
+}
+
+template <bool kBack>
+int launch(const LayerNormArgs &a, LayerNormTypes types, hipStream_t s) {
+  switch (types) {
+    case kLnBf16: return launch_n<uint16_t, uint16_t, uint16_t, 8, kBack>(a, s);
+    case kLnBf16Wide: return launch_n<uint16_t, float, uint16_t, 8, kBack>(a, s);
+    case kLnF32: return launch_n<float, float, float, 4, kBack>(a, s);
+    default: return launch_n<float, float, uint16_t, 8, kBack>(a, s);
+  }
+}
+
+}  // namespace
+
+int launch_layer_norm_fwd(const LayerNormArgs &a, LayerNormTypes types, void *stream) {
+  return launch<false>(a, types, static_cast<hipStream_t>(stream));
+}
+
+int launch_layer_norm_bwd(const LayerNormArgs &args, LayerNormTypes types, void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LayerNormArgs a = args;
+  a.nparts = 0;
+  if (a.rows > 0) {
+    const Shape sh = shape_of(a.dim, types == kLnF32 ? 4 : 8);
+    const int per = sh.threads / sh.lanes;
+    const int64_t groups = (a.rows + per - 1) / per;
+    a.nparts = static_cast<int>(groups < kLayerNormMaxParts ? groups : kLayerNormMaxParts);
+    const int err = launch<true>(a, types, s);
+    if (err != 0) return err;
+  }
+  if (!a.dweight && !a.dbias) return 0;
+  hipLaunchKernelGGL(layer_norm_parts_kernel, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2),
+                     dim3(1024), 0, s, a);
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace ssm

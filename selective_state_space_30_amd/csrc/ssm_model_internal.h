@@ -1,0 +1,91 @@
+// ssm_model_internal.h -- launch interface of the embedding, the layer norm
+// and the gradients' norm (ssm_embed.hip, ssm_layer_norm.hip, ssm_grad.hip).
+// Not installed.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace ssm {
+
+// ------------------------------------------------------------- embedding --
+constexpr int kEmbedMaxDim = 65536;
+
+struct EmbedArgs {
+  const void *ids;
+  int wide_ids;  // int64
+  int64_t tokens, vocab;
+  int dim;
+  float scale;
+  // forward
+  const void *weight;
+  int64_t w_stride;
+  void *out;
+  // backward
+  const void *dy;
+  int64_t dy_stride;
+  void *dweight;
+  int accumulate;
+  void *workspace;
+};
+
+int64_t embed_bwd_workspace(int64_t tokens, int64_t vocab, int64_t dim);
+// wdtype_bf16: of weight or dweight; bf16: of out or dy
+int launch_embed_fwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream);
+int launch_embed_bwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream);
+
+// ------------------------------------------------------------ layer norm --
+constexpr int kLayerNormMaxDim = 16384;
+constexpr int kLayerNormMaxParts = 512;  // workgroups that leave partial weight gradients
+
+struct LayerNormArgs {
+  const void *x, *residual;
+  int64_t x_stride, r_stride;
+  const float *weight, *bias;
+  int64_t rows;
+  int dim;
+  float eps;
+  // forward
+  void *r, *y;
+  // backward
+  const void *dr, *dy;
+  void *dx, *dresidual;
+  float *dweight, *dbias;
+  float *parts;  // (workgroups, 2, dim)
+  int nparts;
+};
+
+enum LayerNormTypes { kLnBf16 = 0, kLnBf16Wide = 1, kLnF32 = 2, kLnF32Bf16 = 3 };
+
+int launch_layer_norm_fwd(const LayerNormArgs &a, LayerNormTypes types, void *stream);
+int launch_layer_norm_bwd(const LayerNormArgs &a, LayerNormTypes types, void *stream);
+
+// -------------------------------------------------------- gradients' norm --
+constexpr int kGradTensors = 128;   // tensors a launch takes, in its arguments
+constexpr int kGradGroups = 1024;   // workgroups of a launch, and partial sums
+constexpr int kGradChunk = 16384;   // elements that a workgroup takes at a time
+
+struct GradTable {
+  const void *grad[kGradTensors];
+  uint32_t first[kGradTensors + 1];  // chunks before each tensor
+  int32_t n;
+  // elements of each tensor, its gradient's type in bit 62, its output's in 63
+  uint64_t size[kGradTensors];
+};
+constexpr uint64_t kGradBf16 = uint64_t(1) << 62, kGradOutBf16 = uint64_t(1) << 63;
+constexpr uint64_t kGradSize = kGradBf16 - 1;
+
+struct GradOuts {
+  void *out[kGradTensors];
+};
+
+// Adds the squares of a table's tensors to nsums (at most kGradGroups) sums,
+// or writes them where it is the first.
+int launch_grad_squares(const GradTable &t, double *sums, int nsums, bool first, void *stream);
+int launch_grad_norm(const double *sums, int nsums, float *norm, void *stream);
+// sums: null where norm is given
+int launch_grad_scale(const GradTable &t, const GradOuts &outs, bool in_place,
+                      const double *sums, int nsums, float max_norm, float *norm, bool write_norm,
+                      void *stream);
+
+}  // namespace ssm
