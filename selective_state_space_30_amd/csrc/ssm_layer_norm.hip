@@ -21,6 +21,8 @@ namespace {
 
 using namespace dev;
 
+constexpr int kForwardGroups = 1024;  // of 256 threads: what the GPU holds at once
+
 // Sums of v over the group, the same in every lane.  `lanes` over 64: the
 // workgroup.  `turn` is another one of the buffers at each call, of which two
 // calls in a row have different ones: a wave writes again only behind a
@@ -43,9 +45,35 @@ __device__ __forceinline__ void row_sums(float (&v)[kK], int lanes, float (*buf)
   turn ^= 1;
 }
 
+// Elements e of a lane's piece i that lie in the row: all of them where the
+// row fills every lane's pieces (kWhole).
+template <bool kWhole, int kN>
+__device__ __forceinline__ bool inside(const LayerNormArgs &p, int lanes, int at, int i, int e) {
+  return kWhole || (at + i * lanes) * kN + e < p.dim;
+}
+template <bool kWhole, typename T, int kN>
+__device__ __forceinline__ void load_at(Piece<T, kN> &x, const T *row, int q, int dim) {
+  if constexpr (kWhole) {
+    x.load(row + q * kN);
+  } else {
+    x.zero();
+    if (q * kN < dim) load_piece(x, row, q, dim);
+  }
+}
+template <bool kWhole, typename T, int kN>
+__device__ __forceinline__ void store_at(T *row, int q, int dim, const float (&v)[kN]) {
+  if constexpr (kWhole) {
+    Piece<T, kN> x;
+    x.set(v);
+    x.store(row + q * kN);
+  } else {
+    if (q * kN < dim) store_piece<T, kN>(row, q, dim, v);
+  }
+}
+
 // r - mean in v (0 behind the row's end), and s.  The mean of the differences,
 // which is what the first mean's rounding left, is taken from both.
-template <int kP, int kN>
+template <int kP, int kN, bool kWhole>
 __device__ __forceinline__ float centre(float (&v)[kP][kN], const LayerNormArgs &p, int lanes,
                                         int at, float (*buf)[8][2], int &turn) {
   const float n = static_cast<float>(p.dim);
@@ -58,157 +86,195 @@ __device__ __forceinline__ float centre(float (&v)[kP][kN], const LayerNormArgs 
   const float mean = s[0] / n;
   float t[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < kP; ++i) {
-    const int left = p.dim - (at + i * lanes) * kN;
+  for (int i = 0; i < kP; ++i)
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
-      v[i][e] = e < left ? v[i][e] - mean : 0.0f;
+      v[i][e] = inside<kWhole, kN>(p, lanes, at, i, e) ? v[i][e] - mean : 0.0f;
       t[0] += v[i][e];
       t[1] = fmaf(v[i][e], v[i][e], t[1]);
     }
-  }
   row_sums<2>(t, lanes, buf, turn);
   const float rest = t[0] / n;
 #pragma unroll
-  for (int i = 0; i < kP; ++i) {
-    const int left = p.dim - (at + i * lanes) * kN;
+  for (int i = 0; i < kP; ++i)
 #pragma unroll
-    for (int e = 0; e < kN; ++e) v[i][e] = e < left ? v[i][e] - rest : 0.0f;
-  }
+    for (int e = 0; e < kN; ++e)
+      v[i][e] = inside<kWhole, kN>(p, lanes, at, i, e) ? v[i][e] - rest : 0.0f;
   return 1.0f / sqrtf(fmaf(-rest, rest, t[1] / n) + p.eps);
 }
 
-template <typename T, typename R, typename Y, int kN, int kP>
+template <typename T, typename R, typename Y, int kN, int kP, bool kWhole>
 __global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, int lanes) {
   __shared__ float Buf[2][8][2];
   int turn = 0;
   const int at = threadIdx.x & (lanes - 1);
-  const int pieces = (p.dim + kN - 1) / kN;
-  const int per = lanes < static_cast<int>(blockDim.x) ? blockDim.x / lanes : 1;
+  const int per = blockDim.x / lanes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes; row < p.rows;
-       row += step) {
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes;
+  Piece<float, kN> w[kP], b[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int q = at + i * lanes;
+    if (p.weight) load_at<kWhole>(w[i], p.weight, q, p.dim);
+    if (p.bias) load_at<kWhole>(b[i], p.bias, q, p.dim);
+  }
+  for (; row < p.rows; row += step) {
     float v[kP][kN];
+    {
+      Piece<T, kN> x[kP];
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      const int q = at + i * lanes;
+      for (int i = 0; i < kP; ++i)
+        load_at<kWhole>(x[i], static_cast<const T *>(p.x) + row * p.x_stride, at + i * lanes, p.dim);
+      if (p.residual) {
+        Piece<R, kN> res[kP];
 #pragma unroll
-      for (int e = 0; e < kN; ++e) v[i][e] = 0.0f;
-      if (q < pieces) {
-        get_piece<T, kN>(static_cast<const T *>(p.x) + row * p.x_stride, q, p.dim, v[i]);
-        if (p.residual) {
-          float t[kN];
-          get_piece<R, kN>(static_cast<const R *>(p.residual) + row * p.r_stride, q, p.dim, t);
+        for (int i = 0; i < kP; ++i)
+          load_at<kWhole>(res[i], static_cast<const R *>(p.residual) + row * p.r_stride,
+                          at + i * lanes, p.dim);
 #pragma unroll
-          for (int e = 0; e < kN; ++e) v[i][e] += t[e];
-        }
+        for (int i = 0; i < kP; ++i)
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[i][e] = x[i][e] + res[i][e];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[i][e] = x[i][e];
       }
     }
     if (p.r)
 #pragma unroll
       for (int i = 0; i < kP; ++i)
-        if (at + i * lanes < pieces)
-          store_piece<R, kN>(static_cast<R *>(p.r) + row * p.dim, at + i * lanes, p.dim, v[i]);
-    const float s = centre<kP, kN>(v, p, lanes, at, Buf, turn);
+        store_at<kWhole, R, kN>(static_cast<R *>(p.r) + row * p.dim, at + i * lanes, p.dim, v[i]);
+    const float s = centre<kP, kN, kWhole>(v, p, lanes, at, Buf, turn);
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-      const int q = at + i * lanes;
-      if (q >= pieces) continue;
-      float w[kN], b[kN];
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
-        w[e] = 1.0f;
-        b[e] = 0.0f;
+        v[i][e] *= s;
+        if (p.weight) v[i][e] *= w[i][e];
+        if (p.bias) v[i][e] += b[i][e];
       }
-      if (p.weight) get_piece<float, kN>(p.weight, q, p.dim, w);
-      if (p.bias) get_piece<float, kN>(p.bias, q, p.dim, b);
-#pragma unroll
-      for (int e = 0; e < kN; ++e) w[e] = fmaf(v[i][e] * s, w[e], b[e]);
-      store_piece<Y, kN>(static_cast<Y *>(p.y) + row * p.dim, q, p.dim, w);
+      store_at<kWhole, Y, kN>(static_cast<Y *>(p.y) + row * p.dim, at + i * lanes, p.dim, v[i]);
     }
   }
+}
+
+// The weight, in LDS by pieces' quarters so that neighbouring lanes read
+// neighbouring 16 bytes.
+template <int kN>
+__device__ __forceinline__ void stage_weight(const LayerNormArgs &p, float *W, int pieces) {
+  for (int j = threadIdx.x; j < pieces * kN; j += blockDim.x) {
+    const int q = j / kN, e = j % kN;
+    W[((e / 4) * pieces + q) * 4 + e % 4] = j < p.dim ? (p.weight ? p.weight[j] : 1.0f) : 0.0f;
+  }
+  __syncthreads();
 }
 
 // The sums for the weights' gradients of a lane's columns stay in registers
 // over the rows that its group takes; at the end the workgroup's groups are
 // added in LDS in a fixed order and leave one partial row.
-template <typename T, typename R, typename Y, int kN, int kP>
+template <typename T, typename R, typename Y, int kN, int kP, bool kWhole>
 __global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, int lanes) {
   __shared__ float Buf[2][8][2];
-  __shared__ float Sums[2 * kN * kP * 64];
+  extern __shared__ float Dyn[];  // the weight; at the end the groups' sums
   int turn = 0;
   const int at = threadIdx.x & (lanes - 1);
-  const int pieces = (p.dim + kN - 1) / kN;
-  const int per = lanes < static_cast<int>(blockDim.x) ? blockDim.x / lanes : 1;
+  const int per = blockDim.x / lanes;
+  const int pieces = kP * lanes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  const float inv = 1.0f / static_cast<float>(p.dim);
-  float w[kP][kN], gw[kP][kN], gb[kP][kN];
+  const float n = static_cast<float>(p.dim);
+  stage_weight<kN>(p, Dyn, pieces);
+  float gw[kP][kN], gb[kP][kN];
 #pragma unroll
-  for (int i = 0; i < kP; ++i) {
-    const int q = at + i * lanes;
+  for (int i = 0; i < kP; ++i)
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      w[i][e] = 1.0f;
-      gw[i][e] = gb[i][e] = 0.0f;
+    for (int e = 0; e < kN; ++e) gw[i][e] = gb[i][e] = 0.0f;
+  auto weight = [&](int i, float (&w)[kN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < kN / 4; ++h) {
+      const float4 x = reinterpret_cast<const float4 *>(Dyn)[h * pieces + at + i * lanes];
+      w[4 * h] = x.x;
+      w[4 * h + 1] = x.y;
+      w[4 * h + 2] = x.z;
+      w[4 * h + 3] = x.w;
     }
-    if (p.weight && q < pieces) get_piece<float, kN>(p.weight, q, p.dim, w[i]);
-  }
+  };
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes; row < p.rows;
        row += step) {
     float v[kP][kN];
     Piece<Y, kN> dy[kP];
     Piece<R, kN> dr[kP];
+    {
+      Piece<T, kN> x[kP];
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      const int q = at + i * lanes;
+      for (int i = 0; i < kP; ++i)
+        load_at<kWhole>(x[i], static_cast<const T *>(p.x) + row * p.x_stride, at + i * lanes, p.dim);
+      if (p.residual) {
+        Piece<R, kN> res[kP];
 #pragma unroll
-      for (int e = 0; e < kN; ++e) v[i][e] = 0.0f;
-      dy[i].zero();
-      dr[i].zero();
-      if (q < pieces) {
-        get_piece<T, kN>(static_cast<const T *>(p.x) + row * p.x_stride, q, p.dim, v[i]);
-        if (p.residual) {
-          float t[kN];
-          get_piece<R, kN>(static_cast<const R *>(p.residual) + row * p.r_stride, q, p.dim, t);
+        for (int i = 0; i < kP; ++i)
+          load_at<kWhole>(res[i], static_cast<const R *>(p.residual) + row * p.r_stride,
+                          at + i * lanes, p.dim);
 #pragma unroll
-          for (int e = 0; e < kN; ++e) v[i][e] += t[e];
-        }
-        load_piece(dy[i], static_cast<const Y *>(p.dy) + row * p.dim, q, p.dim);
-        if (p.dr) load_piece(dr[i], static_cast<const R *>(p.dr) + row * p.dim, q, p.dim);
+        for (int i = 0; i < kP; ++i)
+          load_at<kWhole>(dy[i], static_cast<const Y *>(p.dy) + row * p.dim, at + i * lanes, p.dim);
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[i][e] = x[i][e] + res[i][e];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+          load_at<kWhole>(dy[i], static_cast<const Y *>(p.dy) + row * p.dim, at + i * lanes, p.dim);
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[i][e] = x[i][e];
       }
     }
-    const float s = centre<kP, kN>(v, p, lanes, at, Buf, turn);
+    if (p.dr) {
+#pragma unroll
+      for (int i = 0; i < kP; ++i)
+        load_at<kWhole>(dr[i], static_cast<const R *>(p.dr) + row * p.dim, at + i * lanes, p.dim);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kP; ++i) dr[i].zero();
+    }
+    const float s = centre<kP, kN, kWhole>(v, p, lanes, at, Buf, turn);
     float m[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kP; ++i)
+    for (int i = 0; i < kP; ++i) {
+      float w[kN];
+      weight(i, w);
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
         v[i][e] *= s;
-        const float d = dy[i][e], g = d * w[i][e];
+        const float d = dy[i][e], g = d * w[e];
         gb[i][e] += d;
         gw[i][e] = fmaf(d, v[i][e], gw[i][e]);
         m[0] += g;
         m[1] = fmaf(g, v[i][e], m[1]);
       }
+    }
     row_sums<2>(m, lanes, Buf, turn);
-    m[0] *= inv;
-    m[1] *= inv;
+    m[0] /= n;
+    m[1] /= n;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-      const int q = at + i * lanes;
-      if (q >= pieces) continue;
-      float d[kN];
+      float w[kN], d[kN];
+      weight(i, w);
 #pragma unroll
       for (int e = 0; e < kN; ++e)
-        d[e] = fmaf(s, fmaf(-m[1], v[i][e], fmaf(dy[i][e], w[i][e], -m[0])), dr[i][e]);
-      store_piece<T, kN>(static_cast<T *>(p.dx) + row * p.dim, q, p.dim, d);
+        d[e] = fmaf(s, fmaf(-m[1], v[i][e], fmaf(dy[i][e], w[e], -m[0])), dr[i][e]);
+      store_at<kWhole, T, kN>(static_cast<T *>(p.dx) + row * p.dim, at + i * lanes, p.dim, d);
       if (p.dresidual)
-        store_piece<R, kN>(static_cast<R *>(p.dresidual) + row * p.dim, q, p.dim, d);
+        store_at<kWhole, R, kN>(static_cast<R *>(p.dresidual) + row * p.dim, at + i * lanes, p.dim, d);
     }
   }
   if (!p.dweight && !p.dbias) return;
   float *part = p.parts + static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
-  if (lanes < static_cast<int>(blockDim.x)) {
+  if (per > 1) {
     // groups inside a wave, then the waves one after another
 #pragma unroll
     for (int i = 0; i < kP; ++i)
@@ -220,13 +286,14 @@ __global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, in
         }
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int waves = blockDim.x >> 6;
+    __syncthreads();  // the weight is read
     for (int k = 0; k < waves; ++k) {
       if (wave == k && lane < lanes)
 #pragma unroll
         for (int i = 0; i < kP; ++i)
 #pragma unroll
           for (int e = 0; e < kN; ++e) {
-            float *c = Sums + (i * kN + e) * 64 + lane;
+            float *c = Dyn + (i * kN + e) * 64 + lane;
             if (k > 0) {
               gw[i][e] += c[0];
               gb[i][e] += c[kN * kP * 64];
@@ -240,11 +307,8 @@ __global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, in
   }
 #pragma unroll
   for (int i = 0; i < kP; ++i) {
-    const int q = at + i * lanes;
-    if (q < pieces) {
-      store_piece<float, kN>(part, q, p.dim, gw[i]);
-      store_piece<float, kN>(part + p.dim, q, p.dim, gb[i]);
-    }
+    store_at<kWhole, float, kN>(part, at + i * lanes, p.dim, gw[i]);
+    store_at<kWhole, float, kN>(part + p.dim, at + i * lanes, p.dim, gb[i]);
   }
 }
 
@@ -276,50 +340,73 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(LayerNormArgs p)
   }
 }
 
-// Lanes of a row's group (a power of two, 8..512) and pieces that each holds.
+// Lanes of a row's group (a power of two, 8..512), pieces that each holds, and
+// whether they fill the row.  Rows that do not round the pieces up to one of
+// fewer instances.
 struct Shape {
   int lanes, per, threads;
+  bool whole;
 };
 Shape shape_of(int dim, int n) {
   const int pieces = (dim + n - 1) / n, most = n == 8 ? 5 : 8;
   int lanes = 8;
   while ((pieces + lanes - 1) / lanes > most) lanes *= 2;
-  return {lanes, (pieces + lanes - 1) / lanes, lanes <= 64 ? 256 : lanes};
+  int per = (pieces + lanes - 1) / lanes;
+  const bool whole = per * lanes * n == dim;
+  if (!whole && n == 8 && per == 5) {
+    lanes *= 2;
+    per = (pieces + lanes - 1) / lanes;
+  }
+  if (!whole && per > 4) per = per <= 6 ? 6 : 8;
+  return {lanes, per, lanes <= 64 ? 256 : lanes, whole};
 }
 
-template <typename T, typename R, typename Y, int kN, int kP, bool kBack>
-int launch_p(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
+// Workgroups of a pass over `rows` rows: at most `most`.
+int groups_of(int64_t rows, const Shape &sh, int most) {
   const int per = sh.threads / sh.lanes;
-  const int64_t groups = (a.rows + per - 1) / per;
+  const int64_t groups = (rows + per - 1) / per;
+  return static_cast<int>(groups < most ? groups : most);
+}
+
+template <typename T, typename R, typename Y, int kN, int kP, bool kWhole, bool kBack>
+int launch_p(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
   if constexpr (kBack) {
-    hipLaunchKernelGGL((layer_norm_bwd_kernel<T, R, Y, kN, kP>), dim3(a.nparts), dim3(sh.threads),
-                       0, s, a, sh.lanes);
+    const size_t weight = static_cast<size_t>(kN) * kP * sh.lanes * 4;
+    const size_t sums = sh.lanes <= 64 ? 2 * kN * kP * 64 * 4 : 0;
+    hipLaunchKernelGGL((layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole>), dim3(a.nparts),
+                       dim3(sh.threads), weight > sums ? weight : sums, s, a, sh.lanes);
   } else {
-    const unsigned grid = static_cast<unsigned>(groups < 65536 ? groups : 65536);
-    hipLaunchKernelGGL((layer_norm_fwd_kernel<T, R, Y, kN, kP>), dim3(grid), dim3(sh.threads), 0,
-                       s, a, sh.lanes);
+    hipLaunchKernelGGL((layer_norm_fwd_kernel<T, R, Y, kN, kP, kWhole>),
+                       dim3(groups_of(a.rows, sh, kForwardGroups * 256 / sh.threads)),
+                       dim3(sh.threads), 0, s, a, sh.lanes);
   }
   return static_cast<int>(hipGetLastError());
+}
+
+template <typename T, typename R, typename Y, int kN, bool kWhole, bool kBack>
+int launch_w(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
+  switch (sh.per) {
+    case 1: return launch_p<T, R, Y, kN, 1, kWhole, kBack>(a, sh, s);
+    case 2: return launch_p<T, R, Y, kN, 2, kWhole, kBack>(a, sh, s);
+    case 3: return launch_p<T, R, Y, kN, 3, kWhole, kBack>(a, sh, s);
+    case 4: return launch_p<T, R, Y, kN, 4, kWhole, kBack>(a, sh, s);
+  }
+  if constexpr (kWhole)
+    if (sh.per == 5) return launch_p<T, R, Y, kN, 5, kWhole, kBack>(a, sh, s);
+  if constexpr (kN == 4) {
+    if (sh.per == 6) return launch_p<T, R, Y, kN, 6, kWhole, kBack>(a, sh, s);
+    if (sh.per == 8) return launch_p<T, R, Y, kN, 8, kWhole, kBack>(a, sh, s);
+    if constexpr (kWhole)
+      if (sh.per == 7) return launch_p<T, R, Y, kN, 7, kWhole, kBack>(a, sh, s);
+  }
+  return static_cast<int>(hipErrorInvalidValue);
 }
 
 template <typename T, typename R, typename Y, int kN, bool kBack>
 int launch_n(const LayerNormArgs &a, hipStream_t s) {
   const Shape sh = shape_of(a.dim, kN);
-  switch (sh.per) {
-    case 1: return launch_p<T, R, Y, kN, 1, kBack>(a, sh, s);
-    case 2: return launch_p<T, R, Y, kN, 2, kBack>(a, sh, s);
-    case 3: return launch_p<T, R, Y, kN, 3, kBack>(a, sh, s);
-    case 4: return launch_p<T, R, Y, kN, 4, kBack>(a, sh, s);
-    case 5: return launch_p<T, R, Y, kN, 5, kBack>(a, sh, s);
-  }
-  if constexpr (kN == 4) {
-    switch (sh.per) {
-      case 6: return launch_p<T, R, Y, kN, 6, kBack>(a, sh, s);
-      case 7: return launch_p<T, R, Y, kN, 7, kBack>(a, sh, s);
-      case 8: return launch_p<T, R, Y, kN, 8, kBack>(a, sh, s);
-    }
-  }
-  return static_cast<int>(hipErrorInvalidValue);
+  return sh.whole ? launch_w<T, R, Y, kN, true, kBack>(a, sh, s)
+                  : launch_w<T, R, Y, kN, false, kBack>(a, sh, s);
 }
 
 template <bool kBack>
@@ -344,9 +431,7 @@ int launch_layer_norm_bwd(const LayerNormArgs &args, LayerNormTypes types, void 
   a.nparts = 0;
   if (a.rows > 0) {
     const Shape sh = shape_of(a.dim, types == kLnF32 ? 4 : 8);
-    const int per = sh.threads / sh.lanes;
-    const int64_t groups = (a.rows + per - 1) / per;
-    a.nparts = static_cast<int>(groups < kLayerNormMaxParts ? groups : kLayerNormMaxParts);
+    a.nparts = groups_of(a.rows, sh, kLayerNormMaxParts);
     const int err = launch<true>(a, types, s);
     if (err != 0) return err;
   }
