@@ -50,6 +50,7 @@ Names follow the C ABI:
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import inspect
@@ -1193,23 +1194,43 @@ def ssm_block_norm_bwd(x, w_post=None, z=None, scale=None, residual=None,
 
 
 # ----------------------------------------------------------------- embedding
+@functools.lru_cache(maxsize=1024)
 def ssm_embed_bwd_workspace_size(tokens, vocab, dim) -> int:
     return _size(load_library().ssm_embed_bwd_workspace_size, tokens, vocab, dim)
 
 
+_INDEX_CODES = {torch.int32: SSM_INDEX_I32, torch.int64: SSM_INDEX_I64}
+_CODES = {torch.float32: SSM_DTYPE_F32, torch.bfloat16: SSM_DTYPE_BF16}
+
+
 def _ids(ids):
-    """Address, type code and number of the ids of a call."""
+    """Address and type code of the ids of a call."""
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch.Tensor")
-    if ids.dtype is torch.int64:
-        code = SSM_INDEX_I64
-    elif ids.dtype is torch.int32:
-        code = SSM_INDEX_I32
-    else:
+    code = _INDEX_CODES.get(ids.dtype)
+    if code is None:
         raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
     if not ids.is_cuda:
         raise ValueError("ids must be a device (HIP) tensor")
-    return _dense(ids, "ids", ids.dtype, ids.shape, ids.device), code, ids.numel()
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    return ids.data_ptr(), code
+
+
+def _rows_at(t, name, dtype, shape, dev):
+    """Address and row stride of a tensor of this shape whose last dimension is
+    the row (see :func:`_rows`)."""
+    if (t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape
+            and t.device == dev and t.is_contiguous()):
+        return t.data_ptr(), shape[-1]
+    return _rows(t, name, dtype, shape[:-1], shape[-1:], dev)
+
+
+def _new(like, shape, dtype):
+    """A dense tensor on the device of ``like``, a tensor of the same shape."""
+    if like.dtype is dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 @_on_device
@@ -1220,20 +1241,24 @@ def ssm_embed_fwd(ids, weight, scale=1.0, out=None, dtype=None, stream=None):
     row of zeros.  weight: (vocab, dim), float32 or bfloat16, rows may be
     slices of wider ones.  ``dtype``: of the result (weight's by default; the
     other of the two is allowed).  Returns out, ids.shape + (dim,)."""
+    p_ids, index = _ids(ids)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be (vocab, dim)")
-    p_ids, index, tokens = _ids(ids)
-    dev = ids.device
+    dev, wt = ids.device, weight.dtype
     vocab, dim = weight.shape
-    w, w_stride = _rows(weight, "weight", weight.dtype, (vocab,), (dim,), dev)
-    shape = ids.shape + (dim,)
+    w, w_stride = _rows_at(weight, "weight", wt, weight.shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype or weight.dtype, device=dev)
-    elif dtype is not None and out.dtype != dtype:
-        raise TypeError("out must be %s, got %s" % (dtype, out.dtype))
+        ot = dtype or wt
+        out = torch.empty((*ids.shape, dim), dtype=ot, device=dev)
+        p_out = out.data_ptr()
+    else:
+        ot = out.dtype
+        if dtype is not None and ot != dtype:
+            raise TypeError("out must be %s, got %s" % (dtype, ot))
+        p_out = _dense(out, "out", ot, ids.shape + (dim,), dev)
     _check(load_library().ssm_embed_fwd(
-        p_ids, w, w_stride, _dense(out, "out", out.dtype, shape, dev), tokens, vocab, dim,
-        float(scale), index, _code(weight.dtype), _code(out.dtype), _raw_stream(dev, stream)))
+        p_ids, w, w_stride, p_out, ids.numel(), vocab, dim, scale, index, _code(wt), _code(ot),
+        _raw_stream(dev, stream)))
     return out
 
 
@@ -1246,27 +1271,28 @@ def ssm_embed_bwd(ids, dy, vocab, scale=1.0, dweight=None, accumulate=False,
     a fixed order.  ``accumulate`` adds it to the given ``dweight`` (vocab, dim)
     in place, whose rows without a token are not touched.  ``dtype``: of a new
     dweight, float32 or bfloat16.  Returns dweight."""
-    p_ids, index, tokens = _ids(ids)
-    dev = ids.device
+    p_ids, index = _ids(ids)
+    dev, tokens = ids.device, ids.numel()
     if not isinstance(dy, torch.Tensor) or dy.dim() < 1:
         raise TypeError("dy must be a torch.Tensor (..., dim)")
+    at = dy.dtype
     dim = dy.shape[-1]
-    p_dy, dy_stride = _rows(dy, "dy", dy.dtype, ids.shape, (dim,), dev)
+    p_dy, dy_stride = _rows_at(dy, "dy", at, ids.shape + (dim,), dev)
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate needs dweight")
         dweight = torch.empty((vocab, dim), dtype=dtype, device=dev)
-    lib = load_library()
-    keep, ws, ws_bytes = _scratch(
-        workspace, _size(lib.ssm_embed_bwd_workspace_size, tokens, vocab, dim), dev)
-    _check(lib.ssm_embed_bwd(
-        p_ids, p_dy, dy_stride, _dense(dweight, "dweight", dweight.dtype, (vocab, dim), dev),
-        tokens, vocab, dim, float(scale), SSM_FLAG_ACCUMULATE if accumulate else 0, index,
-        _code(dy.dtype), _code(dweight.dtype), ws, ws_bytes, _raw_stream(dev, stream)))
+    p_dw = _dense(dweight, "dweight", dweight.dtype, (vocab, dim), dev)
+    keep, ws, ws_bytes = _scratch(workspace, ssm_embed_bwd_workspace_size(tokens, vocab, dim), dev)
+    _check(load_library().ssm_embed_bwd(
+        p_ids, p_dy, dy_stride, p_dw, tokens, vocab, dim, scale,
+        SSM_FLAG_ACCUMULATE if accumulate else 0, index, _code(at), _code(dweight.dtype), ws,
+        ws_bytes, _raw_stream(dev, stream)))
     return dweight
 
 
 # ---------------------------------------------------------------- layer norm
+@functools.lru_cache(maxsize=1024)
 def ssm_layer_norm_bwd_workspace_size(rows, dim) -> int:
     return _size(load_library().ssm_layer_norm_bwd_workspace_size, rows, dim)
 
@@ -1274,22 +1300,21 @@ def ssm_layer_norm_bwd_workspace_size(rows, dim) -> int:
 def _layer_norm_args(x, residual, weight, bias):
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a torch.Tensor (..., dim)")
-    dev, act, f32 = x.device, x.dtype, torch.float32
-    if dev.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("x must be a device (HIP) tensor")
-    lead, dim = x.shape[:-1], x.shape[-1]
-    rows = 1
-    for n in lead:
-        rows *= n
-    args = _rows(x, "x", act, lead, (dim,), dev)
-    rdt = act
+    dev, act, shape = x.device, x.dtype, x.shape
+    dim = shape[-1]
+    px, sx = _rows_at(x, "x", act, shape, dev)
+    code = rcode = _code(act)
     if residual is None:
-        args += (None, 0)
+        pr, sr, rdt = None, 0, act
     else:
         rdt = residual.dtype
-        args += _rows(residual, "residual", rdt, lead, (dim,), dev)
-    return (args, _dense(weight, "weight", f32, (dim,), dev),
-            _dense(bias, "bias", f32, (dim,), dev), rows, dim, _code(act), _code(rdt), rdt)
+        rcode = _code(rdt)
+        pr, sr = _rows_at(residual, "residual", rdt, shape, dev)
+    f32 = torch.float32
+    return ((px, sx, pr, sr), _dense(weight, "weight", f32, (dim,), dev),
+            _dense(bias, "bias", f32, (dim,), dev), x.numel() // max(dim, 1), dim, code, rcode, rdt)
 
 
 @_on_device
@@ -1304,23 +1329,28 @@ def ssm_layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5,
     rows.  ``r`` may be the residual itself (in place).  Returns ``(r, y)``; r
     is x itself without a residual."""
     args, w, b, rows, dim, code, rcode, rdt = _layer_norm_args(x, residual, weight, bias)
-    dev = x.device
+    dev, shape = x.device, x.shape
     if residual is None:
         if r is not None:
             raise ValueError("r without a residual")
-        p_r = None
+        r, p_r = x, None
+    elif r is None:
+        r = _new(residual, shape, rdt)
+        p_r = r.data_ptr()
     else:
-        if r is None:
-            r = torch.empty(x.shape, dtype=rdt, device=dev)
-        p_r = _dense(r, "r", rdt, x.shape, dev)
+        p_r = _dense(r, "r", rdt, shape, dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=dtype or x.dtype, device=dev)
-    elif dtype is not None and y.dtype != dtype:
-        raise TypeError("y must be %s, got %s" % (dtype, y.dtype))
+        yt = dtype or x.dtype
+        y = _new(x, shape, yt)
+        p_y = y.data_ptr()
+    else:
+        yt = y.dtype
+        if dtype is not None and yt != dtype:
+            raise TypeError("y must be %s, got %s" % (dtype, yt))
+        p_y = _dense(y, "y", yt, shape, dev)
     _check(load_library().ssm_layer_norm_fwd(
-        *args, w, b, p_r, _dense(y, "y", y.dtype, x.shape, dev), rows, dim, eps, code, rcode,
-        _code(y.dtype), _raw_stream(dev, stream)))
-    return x if residual is None else r, y
+        *args, w, b, p_r, p_y, rows, dim, eps, code, rcode, _code(yt), _raw_stream(dev, stream)))
+    return r, y
 
 
 @_on_device
@@ -1335,28 +1365,28 @@ def ssm_layer_norm_bwd(x, weight=None, bias=None, residual=None, eps=1e-5,
     if not isinstance(dy, torch.Tensor):
         raise TypeError("dy must be a torch.Tensor")
     args, w, b, rows, dim, code, rcode, rdt = _layer_norm_args(x, residual, weight, bias)
-    dev, act, f32 = x.device, x.dtype, torch.float32
+    dev, act, f32, shape = x.device, x.dtype, torch.float32, x.shape
     given = out or {}
-    shapes = {"dx": (x.shape, act)}
-    shared = residual is not None and rdt == act and "dresidual" not in given
+    shared = residual is not None and rdt is act and "dresidual" not in given
+    want = [("dx", x, shape, act)]
     if residual is not None and not shared:
-        shapes["dresidual"] = (x.shape, rdt)
+        want.append(("dresidual", residual, shape, rdt))
     if weight is not None:
-        shapes["dweight"] = ((dim,), f32)
+        want.append(("dweight", weight, (dim,), f32))
     if bias is not None:
-        shapes["dbias"] = ((dim,), f32)
+        want.append(("dbias", bias, (dim,), f32))
     out, p = {}, {}
-    for name, (shape, dtype) in shapes.items():
+    for name, like, size, dtype in want:
         t = given.get(name)
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t = _new(like, size, dtype)
+            p[name] = t.data_ptr()
+        else:
+            p[name] = _dense(t, name, dtype, size, dev)
         out[name] = t
-        p[name] = _dense(t, name, dtype, shape, dev)
-    lib = load_library()
-    keep, ws, ws_bytes = _scratch(
-        workspace, _size(lib.ssm_layer_norm_bwd_workspace_size, rows, dim), dev)
-    _check(lib.ssm_layer_norm_bwd(
-        *args, w, _dense(dr, "dr", rdt, x.shape, dev), _dense(dy, "dy", dy.dtype, x.shape, dev),
+    keep, ws, ws_bytes = _scratch(workspace, ssm_layer_norm_bwd_workspace_size(rows, dim), dev)
+    _check(load_library().ssm_layer_norm_bwd(
+        *args, w, _dense(dr, "dr", rdt, shape, dev), _dense(dy, "dy", dy.dtype, shape, dev),
         p["dx"], p.get("dresidual"), p.get("dweight"), p.get("dbias"), rows, dim, eps, code, rcode,
         _code(dy.dtype), ws, ws_bytes, _raw_stream(dev, stream)))
     if shared:
@@ -1365,11 +1395,9 @@ def ssm_layer_norm_bwd(x, weight=None, bias=None, residual=None, eps=1e-5,
 
 
 # ------------------------------------------- the gradients' norm and clipping
+@functools.lru_cache(maxsize=1)
 def ssm_grad_workspace_size() -> int:
     return _size(load_library().ssm_grad_workspace_size)
-
-
-_GRAD_CODES = {torch.float32: SSM_DTYPE_F32, torch.bfloat16: SSM_DTYPE_BF16}
 
 
 def _fills_its_memory(t):
@@ -1384,33 +1412,40 @@ def _fills_its_memory(t):
 
 
 def _tensors(ts, name, dev):
-    """Host arrays of the addresses, sizes and types of a list of tensors."""
-    ptrs, sizes, codes = [], [], []
+    """Host arrays of the addresses, sizes and types of a list of tensors, and
+    whether all are contiguous."""
+    index, dense = dev.index, True
+    ptrs, sizes, codes = array.array("Q"), array.array("q"), array.array("i")
     for i, t in enumerate(ts):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s[%d] must be a torch.Tensor" % (name, i))
-        code = _GRAD_CODES.get(t.dtype)
+        code = _CODES.get(t.dtype)
         if code is None:
             raise TypeError("%s[%d] must be float32 or bfloat16, got %s" % (name, i, t.dtype))
-        if t.device != dev:
+        if t.get_device() != index or not t.is_cuda:
             raise ValueError("%s[%d] is on %s, expected %s" % (name, i, t.device, dev))
-        if not t.is_contiguous() and not _fills_its_memory(t):
-            raise ValueError("%s[%d] has gaps between its elements" % (name, i))
+        if not t.is_contiguous():
+            dense = False
+            if not _fills_its_memory(t):
+                raise ValueError("%s[%d] has gaps between its elements" % (name, i))
         ptrs.append(t.data_ptr())
         sizes.append(t.numel())
         codes.append(code)
-    n = len(ptrs)
-    return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*codes)
+    return ptrs, sizes, codes, dense
+
+
+def _at(a):
+    return a.buffer_info()[0]
 
 
 def _grad_device(grads):
-    if isinstance(grads, torch.Tensor):
+    if not isinstance(grads, (list, tuple)):
         raise TypeError("grads must be a list of tensors")
     if not grads:
         return torch.device("cuda", torch.cuda.current_device())
     if not isinstance(grads[0], torch.Tensor):
         raise TypeError("grads[0] must be a torch.Tensor")
-    if grads[0].device.type != "cuda":
+    if not grads[0].is_cuda:
         raise ValueError("grads[0] must be a device (HIP) tensor")
     return grads[0].device
 
@@ -1421,13 +1456,13 @@ def ssm_grad_norm(grads, norm=None, workspace=None, stream=None):
     of any sizes and types side by side, squares summed in 64 bits.  Returns
     ``norm``, a float32 tensor of no dimensions on the device."""
     dev = _grad_device(grads)
-    lists = _tensors(grads, "grads", dev)
+    ptrs, sizes, codes, _ = _tensors(grads, "grads", dev)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=dev)
     keep, ws, ws_bytes = _scratch(workspace, ssm_grad_workspace_size(), dev)
     _check(load_library().ssm_grad_norm(
-        *lists, len(grads), _dense(norm, "norm", torch.float32, (), dev), ws, ws_bytes,
-        _raw_stream(dev, stream)))
+        _at(ptrs), _at(sizes), _at(codes), len(grads),
+        _dense(norm, "norm", torch.float32, (), dev), ws, ws_bytes, _raw_stream(dev, stream)))
     return norm
 
 
@@ -1435,29 +1470,34 @@ def ssm_grad_norm(grads, norm=None, workspace=None, stream=None):
 def ssm_grad_clip(grads, max_norm, norm=None, out=None, workspace=None,
                   stream=None):
     """Clips a list of gradients to a 2-norm of ``max_norm`` over all of them:
-    g * min(1, max_norm / norm), in place, or into the tensors of ``out`` (the
-    gradients' shapes; float32 or bfloat16, whatever the gradients' type).
-    ``norm``: a float32 device scalar to take instead of forming it (one that
-    was summed over several processes).  Where the norm is not finite the
-    gradients stay as they are.  Returns the norm before the clipping, a
-    device scalar."""
+    g * min(1, max_norm / norm), in place, or into the tensors of ``out`` (one
+    for each, of its shape and element order; float32 or bfloat16, whatever the
+    gradient's type).  ``norm``: a float32 device scalar to take instead of
+    forming it (one that was summed over several processes).  Where the norm is
+    not finite the gradients stay as they are.  Returns the norm before the
+    clipping, a device scalar."""
     dev = _grad_device(grads)
-    lists = _tensors(grads, "grads", dev)
-    outs, out_codes = None, None
+    ptrs, sizes, codes, dense = _tensors(grads, "grads", dev)
+    p_out = p_out_codes = None
     if out is not None:
-        if len(out) != len(grads):
-            raise ValueError("out must have as many tensors as grads")
-        for i, (g, o) in enumerate(zip(grads, out)):
-            if o.shape != g.shape or (o.stride() != g.stride() and not (
-                    o.is_contiguous() and g.is_contiguous())):
-                raise ValueError("out[%d] must have the shape and strides of its gradient" % i)
-        outs, _, out_codes = _tensors(out, "out", dev)
+        outs, out_sizes, out_codes, out_dense = _tensors(out, "out", dev)
+        if out_sizes != sizes:
+            raise ValueError("out must have a tensor of its size for each gradient")
+        if not (dense and out_dense):
+            for i, (g, o) in enumerate(zip(grads, out)):
+                if not (g.is_contiguous() and o.is_contiguous()) and (
+                        o.shape != g.shape or o.stride() != g.stride()):
+                    raise ValueError("out[%d] must have the strides of its gradient" % i)
+        p_out, p_out_codes = _at(outs), _at(out_codes)
     have = norm is not None
     keep, ws, ws_bytes = None, None, 0
-    if not have:
+    if have:
+        p_norm = _dense(norm, "norm", torch.float32, (), dev)
+    else:
         norm = torch.empty((), dtype=torch.float32, device=dev)
+        p_norm = norm.data_ptr()
         keep, ws, ws_bytes = _scratch(workspace, ssm_grad_workspace_size(), dev)
     _check(load_library().ssm_grad_clip(
-        *lists, outs, out_codes, len(grads), float(max_norm), int(have),
-        _dense(norm, "norm", torch.float32, (), dev), ws, ws_bytes, _raw_stream(dev, stream)))
+        _at(ptrs), _at(sizes), _at(codes), p_out, p_out_codes, len(grads), max_norm, have, p_norm,
+        ws, ws_bytes, _raw_stream(dev, stream)))
     return norm

@@ -14,6 +14,7 @@
 // first and the squares from the differences, so that a mean far from 0 costs
 // no digits.
 #include "ssm_model_internal.h"
+#include <cstdlib>
 #include "ssm_pieces.h"
 
 namespace ssm {
@@ -21,7 +22,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kForwardGroups = 1024;  // of 256 threads: what the GPU holds at once
+constexpr int kForwardGroups = 1024, kBackwardGroups = 256;  // of 256 threads: what the GPU holds
 
 // Sums of v over the group, the same in every lane.  `lanes` over 64: the
 // workgroup.  `turn` is another one of the buffers at each call, of which two
@@ -45,24 +46,24 @@ __device__ __forceinline__ void row_sums(float (&v)[kK], int lanes, float (*buf)
   turn ^= 1;
 }
 
-// Elements e of a lane's piece i that lie in the row: all of them where the
-// row fills every lane's pieces (kWhole).
-template <bool kWhole, int kN>
+// The row fills every lane's pieces (kWhole), or all but the last of each.
+// Whether element e of a lane's piece i lies in the row:
+template <bool kWhole, int kP, int kN>
 __device__ __forceinline__ bool inside(const LayerNormArgs &p, int lanes, int at, int i, int e) {
-  return kWhole || (at + i * lanes) * kN + e < p.dim;
+  return kWhole || i < kP - 1 || (at + i * lanes) * kN + e < p.dim;
 }
-template <bool kWhole, typename T, int kN>
-__device__ __forceinline__ void load_at(Piece<T, kN> &x, const T *row, int q, int dim) {
-  if constexpr (kWhole) {
+template <typename T, int kN>
+__device__ __forceinline__ void load_at(bool whole, Piece<T, kN> &x, const T *row, int q, int dim) {
+  if (whole) {
     x.load(row + q * kN);
   } else {
     x.zero();
     if (q * kN < dim) load_piece(x, row, q, dim);
   }
 }
-template <bool kWhole, typename T, int kN>
-__device__ __forceinline__ void store_at(T *row, int q, int dim, const float (&v)[kN]) {
-  if constexpr (kWhole) {
+template <typename T, int kN>
+__device__ __forceinline__ void store_at(bool whole, T *row, int q, int dim, const float (&v)[kN]) {
+  if (whole) {
     Piece<T, kN> x;
     x.set(v);
     x.store(row + q * kN);
@@ -89,7 +90,7 @@ __device__ __forceinline__ float centre(float (&v)[kP][kN], const LayerNormArgs 
   for (int i = 0; i < kP; ++i)
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
-      v[i][e] = inside<kWhole, kN>(p, lanes, at, i, e) ? v[i][e] - mean : 0.0f;
+      v[i][e] = inside<kWhole, kP, kN>(p, lanes, at, i, e) ? v[i][e] - mean : 0.0f;
       t[0] += v[i][e];
       t[1] = fmaf(v[i][e], v[i][e], t[1]);
     }
@@ -99,7 +100,7 @@ __device__ __forceinline__ float centre(float (&v)[kP][kN], const LayerNormArgs 
   for (int i = 0; i < kP; ++i)
 #pragma unroll
     for (int e = 0; e < kN; ++e)
-      v[i][e] = inside<kWhole, kN>(p, lanes, at, i, e) ? v[i][e] - rest : 0.0f;
+      v[i][e] = inside<kWhole, kP, kN>(p, lanes, at, i, e) ? v[i][e] - rest : 0.0f;
   return 1.0f / sqrtf(fmaf(-rest, rest, t[1] / n) + p.eps);
 }
 
@@ -115,8 +116,8 @@ __global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, in
 #pragma unroll
   for (int i = 0; i < kP; ++i) {
     const int q = at + i * lanes;
-    if (p.weight) load_at<kWhole>(w[i], p.weight, q, p.dim);
-    if (p.bias) load_at<kWhole>(b[i], p.bias, q, p.dim);
+    if (p.weight) load_at(kWhole || i < kP - 1, w[i], p.weight, q, p.dim);
+    if (p.bias) load_at(kWhole || i < kP - 1, b[i], p.bias, q, p.dim);
   }
   for (; row < p.rows; row += step) {
     float v[kP][kN];
@@ -124,12 +125,12 @@ __global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, in
       Piece<T, kN> x[kP];
 #pragma unroll
       for (int i = 0; i < kP; ++i)
-        load_at<kWhole>(x[i], static_cast<const T *>(p.x) + row * p.x_stride, at + i * lanes, p.dim);
+        load_at(kWhole || i < kP - 1, x[i], static_cast<const T *>(p.x) + row * p.x_stride, at + i * lanes, p.dim);
       if (p.residual) {
         Piece<R, kN> res[kP];
 #pragma unroll
         for (int i = 0; i < kP; ++i)
-          load_at<kWhole>(res[i], static_cast<const R *>(p.residual) + row * p.r_stride,
+          load_at(kWhole || i < kP - 1, res[i], static_cast<const R *>(p.residual) + row * p.r_stride,
                           at + i * lanes, p.dim);
 #pragma unroll
         for (int i = 0; i < kP; ++i)
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, in
     if (p.r)
 #pragma unroll
       for (int i = 0; i < kP; ++i)
-        store_at<kWhole, R, kN>(static_cast<R *>(p.r) + row * p.dim, at + i * lanes, p.dim, v[i]);
+        store_at<R, kN>(kWhole || i < kP - 1, static_cast<R *>(p.r) + row * p.dim, at + i * lanes, p.dim, v[i]);
     const float s = centre<kP, kN, kWhole>(v, p, lanes, at, Buf, turn);
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, in
         if (p.weight) v[i][e] *= w[i][e];
         if (p.bias) v[i][e] += b[i][e];
       }
-      store_at<kWhole, Y, kN>(static_cast<Y *>(p.y) + row * p.dim, at + i * lanes, p.dim, v[i]);
+      store_at<Y, kN>(kWhole || i < kP - 1, static_cast<Y *>(p.y) + row * p.dim, at + i * lanes, p.dim, v[i]);
     }
   }
 }
@@ -174,8 +175,8 @@ __device__ __forceinline__ void stage_weight(const LayerNormArgs &p, float *W, i
 // The sums for the weights' gradients of a lane's columns stay in registers
 // over the rows that its group takes; at the end the workgroup's groups are
 // added in LDS in a fixed order and leave one partial row.
-template <typename T, typename R, typename Y, int kN, int kP, bool kWhole>
-__global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, int lanes) {
+template <typename T, typename R, typename Y, int kN, int kP, bool kWhole, int kBound>
+__global__ __launch_bounds__(kBound) void layer_norm_bwd_kernel(LayerNormArgs p, int lanes) {
   __shared__ float Buf[2][8][2];
   extern __shared__ float Dyn[];  // the weight; at the end the groups' sums
   int turn = 0;
@@ -200,47 +201,43 @@ __global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, in
       w[4 * h + 3] = x.w;
     }
   };
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes; row < p.rows;
-       row += step) {
+  // a row's inputs as they are in memory: the next row's are asked for before
+  // this one's are worked on, unless 8 waves share the registers
+  constexpr bool kAhead = kBound <= 256;
+  Piece<T, kN> nx[kP];
+  Piece<R, kN> nres[kP], ndr[kP];
+  Piece<Y, kN> ndy[kP];
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int q = at + i * lanes;
+      load_at(kWhole || i < kP - 1, nx[i], static_cast<const T *>(p.x) + row * p.x_stride, q, p.dim);
+      if (p.residual)
+        load_at(kWhole || i < kP - 1, nres[i], static_cast<const R *>(p.residual) + row * p.r_stride, q, p.dim);
+      load_at(kWhole || i < kP - 1, ndy[i], static_cast<const Y *>(p.dy) + row * p.dim, q, p.dim);
+      if (p.dr) load_at(kWhole || i < kP - 1, ndr[i], static_cast<const R *>(p.dr) + row * p.dim, q, p.dim);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    nres[i].zero();
+    ndr[i].zero();
+  }
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes;
+  if (kAhead && row < p.rows) load(row);
+  for (; row < p.rows; row += step) {
+    if (!kAhead) load(row);
     float v[kP][kN];
     Piece<Y, kN> dy[kP];
     Piece<R, kN> dr[kP];
-    {
-      Piece<T, kN> x[kP];
 #pragma unroll
-      for (int i = 0; i < kP; ++i)
-        load_at<kWhole>(x[i], static_cast<const T *>(p.x) + row * p.x_stride, at + i * lanes, p.dim);
-      if (p.residual) {
-        Piece<R, kN> res[kP];
+    for (int i = 0; i < kP; ++i) {
+      dy[i] = ndy[i];
+      dr[i] = ndr[i];
 #pragma unroll
-        for (int i = 0; i < kP; ++i)
-          load_at<kWhole>(res[i], static_cast<const R *>(p.residual) + row * p.r_stride,
-                          at + i * lanes, p.dim);
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-          load_at<kWhole>(dy[i], static_cast<const Y *>(p.dy) + row * p.dim, at + i * lanes, p.dim);
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-#pragma unroll
-          for (int e = 0; e < kN; ++e) v[i][e] = x[i][e] + res[i][e];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-          load_at<kWhole>(dy[i], static_cast<const Y *>(p.dy) + row * p.dim, at + i * lanes, p.dim);
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-#pragma unroll
-          for (int e = 0; e < kN; ++e) v[i][e] = x[i][e];
-      }
+      for (int e = 0; e < kN; ++e) v[i][e] = nx[i][e] + nres[i][e];
     }
-    if (p.dr) {
-#pragma unroll
-      for (int i = 0; i < kP; ++i)
-        load_at<kWhole>(dr[i], static_cast<const R *>(p.dr) + row * p.dim, at + i * lanes, p.dim);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kP; ++i) dr[i].zero();
-    }
+    if (kAhead && row + step < p.rows) load(row + step);
     const float s = centre<kP, kN, kWhole>(v, p, lanes, at, Buf, turn);
     float m[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -267,9 +264,9 @@ __global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, in
 #pragma unroll
       for (int e = 0; e < kN; ++e)
         d[e] = fmaf(s, fmaf(-m[1], v[i][e], fmaf(dy[i][e], w[e], -m[0])), dr[i][e]);
-      store_at<kWhole, T, kN>(static_cast<T *>(p.dx) + row * p.dim, at + i * lanes, p.dim, d);
+      store_at<T, kN>(kWhole || i < kP - 1, static_cast<T *>(p.dx) + row * p.dim, at + i * lanes, p.dim, d);
       if (p.dresidual)
-        store_at<kWhole, R, kN>(static_cast<R *>(p.dresidual) + row * p.dim, at + i * lanes, p.dim, d);
+        store_at<R, kN>(kWhole || i < kP - 1, static_cast<R *>(p.dresidual) + row * p.dim, at + i * lanes, p.dim, d);
     }
   }
   if (!p.dweight && !p.dbias) return;
@@ -307,8 +304,8 @@ __global__ __launch_bounds__(512) void layer_norm_bwd_kernel(LayerNormArgs p, in
   }
 #pragma unroll
   for (int i = 0; i < kP; ++i) {
-    store_at<kWhole, float, kN>(part, at + i * lanes, p.dim, gw[i]);
-    store_at<kWhole, float, kN>(part + p.dim, at + i * lanes, p.dim, gb[i]);
+    store_at<float, kN>(kWhole || i < kP - 1, part, at + i * lanes, p.dim, gw[i]);
+    store_at<float, kN>(kWhole || i < kP - 1, part + p.dim, at + i * lanes, p.dim, gb[i]);
   }
 }
 
@@ -341,30 +338,30 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(LayerNormArgs p)
 }
 
 // Lanes of a row's group (a power of two, 8..512), pieces that each holds, and
-// whether they fill the row.  Rows that do not round the pieces up to one of
-// fewer instances.
+// whether they fill the row.
 struct Shape {
   int lanes, per, threads;
   bool whole;
 };
-Shape shape_of(int dim, int n) {
-  const int pieces = (dim + n - 1) / n, most = n == 8 ? 5 : 8;
+Shape shape_of(int64_t rows, int dim, int n) {
+  const int pieces = (dim + n - 1) / n, most = getenv("LN_MOST") ? atoi(getenv("LN_MOST")) : n == 8 ? 5 : 8;
   int lanes = 8;
-  while ((pieces + lanes - 1) / lanes > most) lanes *= 2;
+  while (lanes < 512 && (pieces + lanes - 1) / lanes > most) lanes *= 2;
   int per = (pieces + lanes - 1) / lanes;
   const bool whole = per * lanes * n == dim;
   if (!whole && n == 8 && per == 5) {
     lanes *= 2;
     per = (pieces + lanes - 1) / lanes;
   }
-  if (!whole && per > 4) per = per <= 6 ? 6 : 8;
+  (void)rows;
   return {lanes, per, lanes <= 64 ? 256 : lanes, whole};
 }
 
-// Workgroups of a pass over `rows` rows: at most `most`.
+// Workgroups of a pass over the rows: at most `most` times 256 threads.
 int groups_of(int64_t rows, const Shape &sh, int most) {
   const int per = sh.threads / sh.lanes;
   const int64_t groups = (rows + per - 1) / per;
+  most = most * 256 / (sh.threads < 256 ? sh.threads : 256);
   return static_cast<int>(groups < most ? groups : most);
 }
 
@@ -373,11 +370,20 @@ int launch_p(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
   if constexpr (kBack) {
     const size_t weight = static_cast<size_t>(kN) * kP * sh.lanes * 4;
     const size_t sums = sh.lanes <= 64 ? 2 * kN * kP * 64 * 4 : 0;
-    hipLaunchKernelGGL((layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole>), dim3(a.nparts),
-                       dim3(sh.threads), weight > sums ? weight : sums, s, a, sh.lanes);
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(a.nparts), dim3(sh.threads), weight > sums ? weight : sums, s,
+                         a, sh.lanes);
+    };
+    if (sh.threads <= 256) {
+      go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 256>);
+    } else if constexpr (kN * kP >= 8) {
+      go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 512>);
+    } else {
+      return static_cast<int>(hipErrorInvalidValue);
+    }
   } else {
     hipLaunchKernelGGL((layer_norm_fwd_kernel<T, R, Y, kN, kP, kWhole>),
-                       dim3(groups_of(a.rows, sh, kForwardGroups * 256 / sh.threads)),
+                       dim3(groups_of(a.rows, sh, kForwardGroups)),
                        dim3(sh.threads), 0, s, a, sh.lanes);
   }
   return static_cast<int>(hipGetLastError());
@@ -391,20 +397,19 @@ int launch_w(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
     case 3: return launch_p<T, R, Y, kN, 3, kWhole, kBack>(a, sh, s);
     case 4: return launch_p<T, R, Y, kN, 4, kWhole, kBack>(a, sh, s);
   }
-  if constexpr (kWhole)
+  if constexpr (kWhole || kN == 4)
     if (sh.per == 5) return launch_p<T, R, Y, kN, 5, kWhole, kBack>(a, sh, s);
   if constexpr (kN == 4) {
     if (sh.per == 6) return launch_p<T, R, Y, kN, 6, kWhole, kBack>(a, sh, s);
+    if (sh.per == 7) return launch_p<T, R, Y, kN, 7, kWhole, kBack>(a, sh, s);
     if (sh.per == 8) return launch_p<T, R, Y, kN, 8, kWhole, kBack>(a, sh, s);
-    if constexpr (kWhole)
-      if (sh.per == 7) return launch_p<T, R, Y, kN, 7, kWhole, kBack>(a, sh, s);
   }
   return static_cast<int>(hipErrorInvalidValue);
 }
 
 template <typename T, typename R, typename Y, int kN, bool kBack>
 int launch_n(const LayerNormArgs &a, hipStream_t s) {
-  const Shape sh = shape_of(a.dim, kN);
+  const Shape sh = shape_of(a.rows, a.dim, kN);
   return sh.whole ? launch_w<T, R, Y, kN, true, kBack>(a, sh, s)
                   : launch_w<T, R, Y, kN, false, kBack>(a, sh, s);
 }
@@ -430,8 +435,8 @@ int launch_layer_norm_bwd(const LayerNormArgs &args, LayerNormTypes types, void 
   LayerNormArgs a = args;
   a.nparts = 0;
   if (a.rows > 0) {
-    const Shape sh = shape_of(a.dim, types == kLnF32 ? 4 : 8);
-    a.nparts = groups_of(a.rows, sh, kLayerNormMaxParts);
+    const Shape sh = shape_of(a.rows, a.dim, types == kLnF32 ? 4 : 8);
+    a.nparts = groups_of(a.rows, sh, kBackwardGroups);
     const int err = launch<true>(a, types, s);
     if (err != 0) return err;
   }
