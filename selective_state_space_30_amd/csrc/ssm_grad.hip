@@ -73,11 +73,13 @@ __device__ __forceinline__ double chunk_squares(const T *g, int64_t n) {
   }
   for (; at < n; at += kThreads * 8) {
     Piece<T, 8> x;
-    if (at + 8 <= n)
-      x.load(g + at);
-    else
-      x.load_some(g + at, static_cast<int>(n - at));
-    add(x);
+    const int q = static_cast<int>(at / 8), size = static_cast<int>(n);
+    load_piece(x, g, q, size);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double v = in_piece<8>(q, e, size) ? static_cast<double>(x[e]) : 0.0;
+      acc[e % 2] = fma(v, v, acc[e % 2]);
+    }
   }
   return acc[0] + acc[1];
 }
@@ -108,16 +110,12 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double *sums,
 
 template <typename T, typename W>
 __device__ __forceinline__ void scale_chunk(const T *g, W *out, int64_t n, float c) {
+  const int size = static_cast<int>(n);
   auto put = [&](const Piece<T, 8> &x, int64_t at) __attribute__((always_inline)) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = x[e] * c;
-    Piece<W, 8> y;
-    y.set(v);
-    if (at + 8 <= n)
-      y.store(out + at);
-    else
-      y.store_some(out + at, static_cast<int>(n - at));
+    store_piece<W, 8>(out, static_cast<int>(at / 8), size, v);
   };
   int64_t at = static_cast<int64_t>(threadIdx.x) * 8;
   for (; at + 3 * kThreads * 8 + 8 <= n; at += 4 * kThreads * 8) {
@@ -129,10 +127,7 @@ __device__ __forceinline__ void scale_chunk(const T *g, W *out, int64_t n, float
   }
   for (; at < n; at += kThreads * 8) {
     Piece<T, 8> x;
-    if (at + 8 <= n)
-      x.load(g + at);
-    else
-      x.load_some(g + at, static_cast<int>(n - at));
+    load_piece(x, g, static_cast<int>(at / 8), size);
     put(x, at);
   }
 }

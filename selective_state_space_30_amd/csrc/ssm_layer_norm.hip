@@ -14,7 +14,6 @@
 // first and the squares from the differences, so that a mean far from 0 costs
 // no digits.
 #include "ssm_model_internal.h"
-#include <cstdlib>
 #include "ssm_pieces.h"
 
 namespace ssm {
@@ -22,7 +21,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kForwardGroups = 1024, kBackwardGroups = 256;  // of 256 threads: what the GPU holds
+constexpr int kCus = 256;
 
 // Sums of v over the group, the same in every lane.  `lanes` over 64: the
 // workgroup.  `turn` is another one of the buffers at each call, of which two
@@ -50,7 +49,7 @@ __device__ __forceinline__ void row_sums(float (&v)[kK], int lanes, float (*buf)
 // Whether element e of a lane's piece i lies in the row:
 template <bool kWhole, int kP, int kN>
 __device__ __forceinline__ bool inside(const LayerNormArgs &p, int lanes, int at, int i, int e) {
-  return kWhole || i < kP - 1 || (at + i * lanes) * kN + e < p.dim;
+  return kWhole || i < kP - 1 || in_piece<kN>(at + i * lanes, e, p.dim);
 }
 template <typename T, int kN>
 __device__ __forceinline__ void load_at(bool whole, Piece<T, kN> &x, const T *row, int q, int dim) {
@@ -82,7 +81,8 @@ __device__ __forceinline__ float centre(float (&v)[kP][kN], const LayerNormArgs 
 #pragma unroll
   for (int i = 0; i < kP; ++i)
 #pragma unroll
-    for (int e = 0; e < kN; ++e) s[0] += v[i][e];
+    for (int e = 0; e < kN; ++e)
+      s[0] += inside<kWhole, kP, kN>(p, lanes, at, i, e) ? v[i][e] : 0.0f;
   row_sums<1>(s, lanes, buf, turn);
   const float mean = s[0] / n;
   float t[2] = {0.0f, 0.0f};
@@ -163,11 +163,13 @@ __global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, in
 
 // The weight, in LDS by pieces' quarters so that neighbouring lanes read
 // neighbouring 16 bytes.
-template <int kN>
+template <bool kWhole, int kN>
 __device__ __forceinline__ void stage_weight(const LayerNormArgs &p, float *W, int pieces) {
   for (int j = threadIdx.x; j < pieces * kN; j += blockDim.x) {
     const int q = j / kN, e = j % kN;
-    W[((e / 4) * pieces + q) * 4 + e % 4] = j < p.dim ? (p.weight ? p.weight[j] : 1.0f) : 0.0f;
+    const int c = kWhole || (q + 1) * kN <= p.dim ? j : p.dim - kN + e;
+    const bool in = kWhole || (q * kN < p.dim && in_piece<kN>(q, e, p.dim));
+    W[((e / 4) * pieces + q) * 4 + e % 4] = in ? (p.weight ? p.weight[c] : 1.0f) : 0.0f;
   }
   __syncthreads();
 }
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(kBound) void layer_norm_bwd_kernel(LayerNormArgs p,
   const int pieces = kP * lanes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * per;
   const float n = static_cast<float>(p.dim);
-  stage_weight<kN>(p, Dyn, pieces);
+  stage_weight<kWhole, kN>(p, Dyn, pieces);
   float gw[kP][kN], gb[kP][kN];
 #pragma unroll
   for (int i = 0; i < kP; ++i)
@@ -203,7 +205,7 @@ __global__ __launch_bounds__(kBound) void layer_norm_bwd_kernel(LayerNormArgs p,
   };
   // a row's inputs as they are in memory: the next row's are asked for before
   // this one's are worked on, unless 8 waves share the registers
-  constexpr bool kAhead = kBound <= 256;
+  constexpr bool kAhead = kBound <= 256 || kP * kN <= 16;
   Piece<T, kN> nx[kP];
   Piece<R, kN> nres[kP], ndr[kP];
   Piece<Y, kN> ndy[kP];
@@ -247,7 +249,8 @@ __global__ __launch_bounds__(kBound) void layer_norm_bwd_kernel(LayerNormArgs p,
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
         v[i][e] *= s;
-        const float d = dy[i][e], g = d * w[e];
+        const float d = inside<kWhole, kP, kN>(p, lanes, at, i, e) ? dy[i][e] : 0.0f;
+        const float g = d * w[e];
         gb[i][e] += d;
         gw[i][e] = fmaf(d, v[i][e], gw[i][e]);
         m[0] += g;
@@ -343,26 +346,56 @@ struct Shape {
   int lanes, per, threads;
   bool whole;
 };
-Shape shape_of(int64_t rows, int dim, int n) {
-  const int pieces = (dim + n - 1) / n, most = getenv("LN_MOST") ? atoi(getenv("LN_MOST")) : n == 8 ? 5 : 8;
-  int lanes = 8;
-  while (lanes < 512 && (pieces + lanes - 1) / lanes > most) lanes *= 2;
-  int per = (pieces + lanes - 1) / lanes;
-  const bool whole = per * lanes * n == dim;
-  if (!whole && n == 8 && per == 5) {
-    lanes *= 2;
-    per = (pieces + lanes - 1) / lanes;
+
+// One wave or a part of it where its lanes hold the row in at most `alone`
+// pieces each (no barrier), else as many waves as leave `shared` pieces.  Among
+// up to 64 lanes the most that fill the row, since short rows want many lanes
+// (forward pass, bf16: 100000 x 256 with 8, 16 and 32 lanes 43, 40 and 39 us)
+// and filled ones no checks (65536 x 768 with 32 filled lanes 75 us, with 64
+// not filled 78).  Long rows want fewer pieces a lane than the registers hold
+// (forward, bf16: 8192 x 5120 with 128 and 256 lanes 77 and 65 us, 4096 x 8192
+// with 256 and 512 lanes 57 and 52 us; backward: 8192 x 4096 with 128 and 256
+// lanes 85 and 78 us, 8192 x 2560 with an fp32 residual with 64, 128 and 256
+// lanes 86, 87 and 82 us).
+Shape shape_of(int dim, int n, int alone, int shared) {
+  const int pieces = (dim + n - 1) / n;
+  auto per = [&](int lanes) { return (pieces + lanes - 1) / lanes; };
+  int lanes = 0;
+  for (int k = 64; k >= 8; k /= 2)
+    if (!lanes && pieces % k == 0 && dim % n == 0 && per(k) <= alone) lanes = k;
+  if (!lanes) {
+    lanes = 8;
+    while (lanes < 64 && per(lanes) > 1) lanes *= 2;
+    if (per(lanes) > alone)
+      while (lanes < 512 && per(lanes) > shared) lanes *= 2;
   }
-  (void)rows;
-  return {lanes, per, lanes <= 64 ? 256 : lanes, whole};
+  return {lanes, per(lanes), lanes <= 64 ? 256 : lanes, per(lanes) * lanes * n == dim};
 }
 
-// Workgroups of a pass over the rows: at most `most` times 256 threads.
+// types: of elements per piece n, and whether rows are read as fp32 beside bf16
+Shape shape_of(int dim, LayerNormTypes types, bool backward) {
+  if (types == kLnF32) return backward ? shape_of(dim, 4, 7, 5) : shape_of(dim, 4, 8, 6);
+  return shape_of(dim, 8, 4, backward && types != kLnBf16 ? 2 : 3);
+}
+
+// Workgroups of a pass over the rows: at most `most` for each CU and 256 threads.
 int groups_of(int64_t rows, const Shape &sh, int most) {
   const int per = sh.threads / sh.lanes;
   const int64_t groups = (rows + per - 1) / per;
-  most = most * 256 / (sh.threads < 256 ? sh.threads : 256);
+  most = most * kCus * 256 / (sh.threads < 256 ? sh.threads : 256);
   return static_cast<int>(groups < most ? groups : most);
+}
+
+// Workgroups a CU of the backward pass: one that asks for its rows ahead keeps
+// the memory busy by itself where its lanes are filled and wait for no other
+// wave; two where they fit into the registers and it does not.  (bf16, one and
+// two: 32768 x 1024 69 and 73 us, 65536 x 768 105 and 109; 8192 x 4096 94 and
+// 78, 30000 x 1100 95 and 76, 8192 x 2560 76 and 58; with an fp32 residual 8192
+// x 2560 103 and 83.)
+int back_groups(int64_t rows, const Shape &sh, LayerNormTypes types) {
+  const int held = sh.per * (types == kLnF32 ? 4 : 8);
+  const bool fit = held <= (types == kLnBf16 ? 24 : 16) && sh.threads <= 256;
+  return groups_of(rows, sh, fit && (!sh.whole || sh.lanes > 64) ? 2 : 1);
 }
 
 template <typename T, typename R, typename Y, int kN, int kP, bool kWhole, bool kBack>
@@ -374,16 +407,13 @@ int launch_p(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
       hipLaunchKernelGGL(kernel, dim3(a.nparts), dim3(sh.threads), weight > sums ? weight : sums, s,
                          a, sh.lanes);
     };
-    if (sh.threads <= 256) {
+    if (sh.threads <= 256)
       go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 256>);
-    } else if constexpr (kN * kP >= 8) {
+    else
       go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 512>);
-    } else {
-      return static_cast<int>(hipErrorInvalidValue);
-    }
   } else {
     hipLaunchKernelGGL((layer_norm_fwd_kernel<T, R, Y, kN, kP, kWhole>),
-                       dim3(groups_of(a.rows, sh, kForwardGroups)),
+                       dim3(groups_of(a.rows, sh, 4)),
                        dim3(sh.threads), 0, s, a, sh.lanes);
   }
   return static_cast<int>(hipGetLastError());
@@ -397,7 +427,7 @@ int launch_w(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
     case 3: return launch_p<T, R, Y, kN, 3, kWhole, kBack>(a, sh, s);
     case 4: return launch_p<T, R, Y, kN, 4, kWhole, kBack>(a, sh, s);
   }
-  if constexpr (kWhole || kN == 4)
+  if constexpr (kN == 4)
     if (sh.per == 5) return launch_p<T, R, Y, kN, 5, kWhole, kBack>(a, sh, s);
   if constexpr (kN == 4) {
     if (sh.per == 6) return launch_p<T, R, Y, kN, 6, kWhole, kBack>(a, sh, s);
@@ -408,26 +438,34 @@ int launch_w(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
 }
 
 template <typename T, typename R, typename Y, int kN, bool kBack>
-int launch_n(const LayerNormArgs &a, hipStream_t s) {
-  const Shape sh = shape_of(a.rows, a.dim, kN);
+int launch_n(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
   return sh.whole ? launch_w<T, R, Y, kN, true, kBack>(a, sh, s)
                   : launch_w<T, R, Y, kN, false, kBack>(a, sh, s);
 }
 
 template <bool kBack>
-int launch(const LayerNormArgs &a, LayerNormTypes types, hipStream_t s) {
+int launch(const LayerNormArgs &a, const Shape &sh, LayerNormTypes types, hipStream_t s) {
   switch (types) {
-    case kLnBf16: return launch_n<uint16_t, uint16_t, uint16_t, 8, kBack>(a, s);
-    case kLnBf16Wide: return launch_n<uint16_t, float, uint16_t, 8, kBack>(a, s);
-    case kLnF32: return launch_n<float, float, float, 4, kBack>(a, s);
-    default: return launch_n<float, float, uint16_t, 8, kBack>(a, s);
+    case kLnBf16: return launch_n<uint16_t, uint16_t, uint16_t, 8, kBack>(a, sh, s);
+    case kLnBf16Wide: return launch_n<uint16_t, float, uint16_t, 8, kBack>(a, sh, s);
+    case kLnF32: return launch_n<float, float, float, 4, kBack>(a, sh, s);
+    default: return launch_n<float, float, uint16_t, 8, kBack>(a, sh, s);
   }
 }
 
 }  // namespace
 
+int layer_norm_bwd_parts(int64_t rows, int dim) {
+  int most = 0;
+  for (LayerNormTypes t : {kLnBf16, kLnBf16Wide, kLnF32, kLnF32Bf16}) {
+    const int n = back_groups(rows, shape_of(dim, t, true), t);
+    if (n > most) most = n;
+  }
+  return most;
+}
+
 int launch_layer_norm_fwd(const LayerNormArgs &a, LayerNormTypes types, void *stream) {
-  return launch<false>(a, types, static_cast<hipStream_t>(stream));
+  return launch<false>(a, shape_of(a.dim, types, false), types, static_cast<hipStream_t>(stream));
 }
 
 int launch_layer_norm_bwd(const LayerNormArgs &args, LayerNormTypes types, void *stream) {
@@ -435,9 +473,9 @@ int launch_layer_norm_bwd(const LayerNormArgs &args, LayerNormTypes types, void 
   LayerNormArgs a = args;
   a.nparts = 0;
   if (a.rows > 0) {
-    const Shape sh = shape_of(a.rows, a.dim, types == kLnF32 ? 4 : 8);
-    a.nparts = groups_of(a.rows, sh, kBackwardGroups);
-    const int err = launch<true>(a, types, s);
+    const Shape sh = shape_of(a.dim, types, true);
+    a.nparts = back_groups(a.rows, sh, types);
+    const int err = launch<true>(a, sh, types, s);
     if (err != 0) return err;
   }
   if (!a.dweight && !a.dbias) return 0;

@@ -183,7 +183,7 @@ ssm::LayerNormArgs norm_args(const NormCall &c) {
 }
 
 int64_t norm_workspace(int64_t rows, int64_t dim) {
-  return std::min<int64_t>(rows, ssm::kLayerNormMaxParts) * 2 * dim * 4;
+  return int64_t(ssm::layer_norm_bwd_parts(rows, static_cast<int>(dim))) * 2 * dim * 4;
 }
 
 // -------------------------------------------------------- gradients' norm --

@@ -36,7 +36,6 @@ int launch_embed_bwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream);
 
 // ------------------------------------------------------------ layer norm --
 constexpr int kLayerNormMaxDim = 16384;
-constexpr int kLayerNormMaxParts = 512;  // workgroups that leave partial weight gradients
 
 struct LayerNormArgs {
   const void *x, *residual;
@@ -57,6 +56,9 @@ struct LayerNormArgs {
 
 enum LayerNormTypes { kLnBf16 = 0, kLnBf16Wide = 1, kLnF32 = 2, kLnF32Bf16 = 3 };
 
+// Workgroups of the backward pass, and partial rows of the weights' gradients,
+// at most, for any types.
+int layer_norm_bwd_parts(int64_t rows, int dim);
 int launch_layer_norm_fwd(const LayerNormArgs &a, LayerNormTypes types, void *stream);
 int launch_layer_norm_bwd(const LayerNormArgs &a, LayerNormTypes types, void *stream);
 

@@ -1,7 +1,13 @@
 // ssm_pieces.h -- pieces of a row: kN neighbouring elements that are moved
 // with 16-byte loads and stores wherever they start (gfx950 takes global
-// accesses at any element's address), the row's last piece element by element
-// where it is not whole, and sums over lanes.  Included by .hip sources only.
+// accesses at any element's address; 200 million elements copied from and to
+// addresses that are no multiple of 4 took 3 % longer), and sums over lanes.
+// Included by .hip sources only.
+//
+// A row's last piece, where the row does not fill it, ends with the row: its
+// first elements belong to the piece before.  It is read whole, those elements
+// are left out of sums, and only the others are written.  (Reading it element
+// by element, one wait after another, cost rows of 8191 half of their time.)
 #pragma once
 
 #include "ssm_device.h"
@@ -34,17 +40,21 @@ struct Piece {
       for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
     }
   }
-  // the first n of kN elements, 0 behind them
+  // a row of n < kN elements, in the last n places; the others repeat its first
   __device__ __forceinline__ void load_some(const T *p, int n) {
-    zero();
+    T x[kN];
 #pragma unroll
-    for (int e = 0; e < kN; ++e)
-      if (e < n) {
-        if constexpr (sizeof(T) == 2)
-          w[e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e % 2));
-        else
-          w[e] = __float_as_uint(p[e]);
-      }
+    for (int e = 0; e < kN; ++e) {
+      const int at = e - (kN - n);
+      x[e] = p[at < 0 ? 0 : at];
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 2)
+        w[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
+      else
+        w[i] = __float_as_uint(x[i]);
+    }
   }
   __device__ __forceinline__ float operator[](int e) const {
     if constexpr (sizeof(T) == 2)
@@ -71,26 +81,35 @@ struct Piece {
         *reinterpret_cast<u32x4_a4 *>(p + 4 * i) = x;
     }
   }
+  // the last n places, to p[0] and on
   __device__ __forceinline__ void store_some(T *p, int n) const {
 #pragma unroll
     for (int e = 0; e < kN; ++e)
-      if (e < n) {
+      if (e >= kN - n) {
         if constexpr (sizeof(T) == 2)
-          p[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e % 2)));
+          p[e - (kN - n)] = static_cast<uint16_t>(w[e / 2] >> (16 * (e % 2)));
         else
-          p[e] = __uint_as_float(w[e]);
+          p[e - (kN - n)] = __uint_as_float(w[e]);
       }
   }
 };
 
-// Piece at element q * kN of a row of dim elements (q * kN < dim).
+// Whether place e of piece q belongs to it (and not to the one before, or to
+// none): of a row of dim elements.
+template <int kN>
+__device__ __forceinline__ bool in_piece(int q, int e, int dim) {
+  return e >= kN - (dim - q * kN);
+}
+
+// Piece q of a row of dim elements (q * kN < dim).
 template <typename T, int kN>
 __device__ __forceinline__ void load_piece(Piece<T, kN> &x, const T *row, int q, int dim) {
-  const int left = dim - q * kN;
-  if (left >= kN)
-    x.load(row + q * kN);
-  else
-    x.load_some(row + q * kN, left);
+  if (dim >= kN) {
+    const int at = q * kN;
+    x.load(row + (at + kN <= dim ? at : dim - kN));
+  } else {
+    x.load_some(row, dim);
+  }
 }
 template <typename T, int kN>
 __device__ __forceinline__ void store_piece(T *row, int q, int dim, const float (&v)[kN]) {

@@ -169,7 +169,7 @@ def test_sizes(lib):
     assert ssm.ssm_grad_workspace_size() % 256 == 0
     # the partial sums stay a fraction of what is summed
     assert ssm.ssm_embed_bwd_workspace_size(65536, 50000, 1024) < 65536 * 1024 * 2 // 2
-    assert ssm.ssm_layer_norm_bwd_workspace_size(1 << 20, 1024) <= 1 << 22
+    assert ssm.ssm_layer_norm_bwd_workspace_size(1 << 20, 1024) <= 1 << 23
 
 
 CPU = torch.zeros(4, 8)
