@@ -13,6 +13,7 @@
 // spread over as many waves as there are runs of it.
 #include "ssm_model_internal.h"
 #include "ssm_pieces.h"
+#include <cstdlib>
 
 namespace ssm {
 namespace {
@@ -30,159 +31,335 @@ __device__ __forceinline__ uint32_t key_of(const EmbedArgs &p, int64_t t) {
 }
 
 // ---------------------------------------------------------------- forward --
-// A workgroup takes rows_per rows at a time, their pieces flat over its lanes.
+// A workgroup takes rows_per rows at a time, their pieces flat over its lanes,
+// kAhead of them in flight.
 template <typename W, typename T, int kN>
 __global__ __launch_bounds__(kThreads) void embed_fwd_kernel(EmbedArgs p, int rows_per) {
+  constexpr int kAhead = 4;
   const uint32_t pieces = (p.dim + kN - 1) / kN;
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_per; row0 < p.tokens;
        row0 += static_cast<int64_t>(gridDim.x) * rows_per) {
     const int64_t left = p.tokens - row0;
     const uint32_t all = pieces * static_cast<uint32_t>(left < rows_per ? left : rows_per);
-    for (uint32_t l = threadIdx.x; l < all; l += kThreads) {
-      const uint32_t r = l / pieces, q = l - r * pieces;
-      const uint32_t key = key_of(p, row0 + r);
-      float v[kN];
+    for (uint32_t l0 = threadIdx.x; l0 < all; l0 += kAhead * kThreads) {
+      uint32_t row[kAhead], q[kAhead], key[kAhead];
+      Piece<W, kN> w[kAhead];
 #pragma unroll
-      for (int e = 0; e < kN; ++e) v[e] = 0.0f;
-      if (key < p.vocab) {
-        get_piece<W, kN>(static_cast<const W *>(p.weight) + key * p.w_stride, q, p.dim, v);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) v[e] *= p.scale;
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t l = l0 + k * kThreads;
+        row[k] = l / pieces;
+        q[k] = l - row[k] * pieces;
+        key[k] = l < all ? key_of(p, row0 + row[k]) : static_cast<uint32_t>(p.vocab);
       }
-      store_piece<T, kN>(static_cast<T *>(p.out) + (row0 + r) * p.dim, q, p.dim, v);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        w[k].zero();
+        if (key[k] < p.vocab)
+          load_piece(w[k], static_cast<const W *>(p.weight) + key[k] * p.w_stride, q[k], p.dim);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (l0 + k * kThreads >= all) break;
+        float v[kN];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) v[e] = key[k] < p.vocab ? w[k][e] * p.scale : 0.0f;
+        store_piece<T, kN>(static_cast<T *>(p.out) + (row0 + row[k]) * p.dim, q[k], p.dim, v);
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------- sort --
-constexpr int kTile = 4096;             // tokens a workgroup sorts in a pass
-constexpr int kPer = kTile / kThreads;  // keys a thread holds
-constexpr int kBins = 256;
+// Pairs of id and token, a digit of up to kMaxBits bits a pass.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kMaxBits = 9, kBins = 1 << kMaxBits;
+constexpr int kShort = 16384;       // most tokens of the short sort: one workgroup, in LDS
+constexpr int kOwnTiles = 256;      // tiles up to which the scatter sums the counts itself
 
 struct SortPass {
   const uint32_t *keys, *pos;  // null in the first pass: the ids themselves
   uint32_t *keys_out, *pos_out;
-  uint32_t *counts;            // (bins, tiles)
+  uint32_t *counts;            // (bins, tiles): of each tile, or the places before it
   int64_t tiles;
-  int shift;
+  int shift, bits;
 };
 
-// Keys of the pass that the thread holds: a wave's are neighbours, 64 at a time.
+// Lanes of the wave whose digit is this lane's, among those in `in`.
+__device__ __forceinline__ uint64_t same_digit(uint32_t digit, uint64_t in, int bits) {
+#pragma unroll
+  for (int b = 0; b < kMaxBits; ++b) {
+    if (b < bits) {
+      const bool bit = digit >> b & 1u;
+      const uint64_t set = __ballot(bit);
+      in &= bit ? set : ~set;
+    }
+  }
+  return in;
+}
+
+// Rank of the lane's key among the wave's with the same digit so far, whose
+// numbers are in `count`.
+__device__ __forceinline__ uint32_t rank_of(uint32_t digit, bool in, int bits, uint32_t *count) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t same = same_digit(digit, __ballot(in), bits);
+  const int first = __ffsll(static_cast<unsigned long long>(same)) - 1;
+  uint32_t old = 0u;
+  if (in && lane == first)
+    old = atomicAdd(&count[digit], static_cast<uint32_t>(__popcll(same)));
+  old = __shfl(old, first < 0 ? 0 : first);
+  return old + __popcll(same & ((uint64_t(1) << lane) - 1));
+}
+
+// Sum of v over the threads before this one, of kBins neighbouring threads
+// that start at thread 0 (all threads of the workgroup call it).
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t *buf) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t up = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_up(up, d);
+    if (lane >= d) up += o;
+  }
+  if (lane == 63) buf[wave] = up;
+  __syncthreads();
+  up -= v;
+  for (int w = 0; w < wave; ++w) up += buf[w];
+  __syncthreads();
+  return up;
+}
+
+// Zeros in the rows row0 .. row1 - 1 of dweight whose bit in `there` (of row
+// row0 on) is not set, by the whole workgroup.
+template <typename W>
+__device__ __forceinline__ void clear_rows(const EmbedArgs &p, int64_t row0, int64_t row1,
+                                           const uint32_t *there) {
+  constexpr int kN = 16 / sizeof(W);
+  const int pieces = (p.dim + kN - 1) / kN, threads = blockDim.x;
+  const int rows = static_cast<int>(row1 - row0), rs = threads / pieces, qs = threads % pieces;
+  float zero[kN];
+#pragma unroll
+  for (int e = 0; e < kN; ++e) zero[e] = 0.0f;
+  int r = threadIdx.x / pieces, q = threadIdx.x % pieces;
+  while (r < rows) {
+    if (!(there[r / 32] >> (r % 32) & 1u))
+      store_piece<W, kN>(static_cast<W *>(p.dweight) + (row0 + r) * p.dim, q, p.dim, zero);
+    r += rs;
+    q += qs;
+    if (q >= pieces) {
+      q -= pieces;
+      ++r;
+    }
+  }
+}
+
+// The short sort, by workgroup 0, and beside it, by the others, zeros in the
+// rows of ids that do not come: each finds those of its rows among the ids.
+constexpr int kClearRows = 8192;  // rows a workgroup looks for at a time
+template <typename W>
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedArgs p, uint32_t *keys_out,
+                                                                 uint32_t *pos_out, int passes,
+                                                                 int bits, int64_t rows_per) {
+  constexpr int kPer = kShort / kSortThreads;
+  __shared__ uint32_t Key[kShort];
+  __shared__ uint16_t Pos[kShort];
+  __shared__ uint32_t Count[kSortWaves][kBins];
+  __shared__ uint32_t Buf[kSortWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int n = static_cast<int>(p.tokens);
+  if (blockIdx.x > 0) {
+    const int64_t begin = (blockIdx.x - 1) * rows_per;
+    const int64_t stop = begin + rows_per < p.vocab ? begin + rows_per : p.vocab;
+    for (int64_t row0 = begin; row0 < stop; row0 += kClearRows) {
+      const int64_t row1 = row0 + kClearRows < stop ? row0 + kClearRows : stop;
+      for (int i = tid; i < kClearRows / 32; i += kSortThreads) Key[i] = 0u;
+      __syncthreads();
+      for (int t = tid; t < n; t += kSortThreads) {
+        const int64_t key = key_of(p, t);
+        if (key >= row0 && key < row1)
+          atomicOr(&Key[(key - row0) / 32], 1u << ((key - row0) % 32));
+      }
+      __syncthreads();
+      clear_rows<W>(p, row0, row1, Key);
+      __syncthreads();
+    }
+    return;
+  }
+  // a wave holds neighbours, 64 at a time
+  const int per = (n + kSortThreads - 1) / kSortThreads;
+  uint32_t key[kPer], pos[kPer], rank[kPer];
+  auto index = [&](int i) __attribute__((always_inline)) { return (wave * per + i) * 64 + lane; };
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i < per) {
+      pos[i] = index(i);
+      key[i] = index(i) < n ? key_of(p, index(i)) : 0u;
+    }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * bits;
+    const uint32_t mask = (1u << bits) - 1u;
+    for (int i = tid; i < kSortWaves * kBins; i += kSortThreads) (&Count[0][0])[i] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < per) rank[i] = rank_of(key[i] >> shift & mask, index(i) < n, bits, Count[wave]);
+    __syncthreads();
+    uint32_t sum = 0u;
+    if (tid < kBins)
+      for (int w = 0; w < kSortWaves; ++w) sum += Count[w][tid];
+    uint32_t at = sum_before(tid < kBins ? sum : 0u, Buf);
+    if (tid < kBins)
+      for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = Count[w][tid];
+        Count[w][tid] = at;
+        at += c;
+      }
+    __syncthreads();
+    const bool last = pass == passes - 1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < per && index(i) < n) {
+        const uint32_t to = Count[wave][key[i] >> shift & mask] + rank[i];
+        if (last) {
+          keys_out[to] = key[i];
+          pos_out[to] = pos[i];
+        } else {
+          Key[to] = key[i];
+          Pos[to] = static_cast<uint16_t>(pos[i]);
+        }
+      }
+    if (last) return;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < per && index(i) < n) {
+        key[i] = Key[index(i)];
+        pos[i] = Pos[index(i)];
+      }
+    __syncthreads();
+  }
+}
+
+// The long sort: a tile of kPer keys a thread, a wave's 64 neighbours each.
+template <int kPer>
 __device__ __forceinline__ int64_t sort_index(int64_t tile, int i) {
-  return tile * kTile + (threadIdx.x >> 6) * (64 * kPer) + i * 64 + (threadIdx.x & 63);
+  return tile * (kPer * kSortThreads) + (threadIdx.x >> 6) * (64 * kPer) + i * 64 +
+         (threadIdx.x & 63);
 }
 __device__ __forceinline__ uint32_t sort_key(const EmbedArgs &p, const SortPass &s, int64_t at) {
   return s.keys ? s.keys[at] : key_of(p, at);
 }
 
-__global__ __launch_bounds__(kThreads) void embed_count_kernel(EmbedArgs p, SortPass s) {
+template <int kPer>
+__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedArgs p, SortPass s) {
   __shared__ uint32_t Count[kBins];
+  const uint32_t mask = (1u << s.bits) - 1u;
   for (int64_t tile = blockIdx.x; tile < s.tiles; tile += gridDim.x) {
-    Count[threadIdx.x] = 0u;
+    if (threadIdx.x < kBins) Count[threadIdx.x] = 0u;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int64_t at = sort_index(tile, i);
-      if (at < p.tokens) atomicAdd(&Count[sort_key(p, s, at) >> s.shift & 255u], 1u);
+      const int64_t at = sort_index<kPer>(tile, i);
+      if (at < p.tokens) atomicAdd(&Count[sort_key(p, s, at) >> s.shift & mask], 1u);
     }
     __syncthreads();
-    s.counts[threadIdx.x * s.tiles + tile] = Count[threadIdx.x];
-    __syncthreads();
-  }
-}
-
-// Counts before each (bin, tile), in that order: one workgroup.
-__global__ __launch_bounds__(1024) void embed_offsets_kernel(SortPass s) {
-  __shared__ uint32_t Sums[16];
-  const int64_t n = kBins * s.tiles;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t before = 0u;
-  for (int64_t base = 0; base < n; base += 4096) {
-    uint32_t c[4], sum = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = base + 4 * threadIdx.x + i;
-      c[i] = at < n ? s.counts[at] : 0u;
-      sum += c[i];
-    }
-    uint32_t up = sum;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const uint32_t o = __shfl_up(up, d);
-      if (lane >= d) up += o;
-    }
-    if (lane == 63) Sums[wave] = up;
-    __syncthreads();
-    uint32_t mine = before + up - sum, all = 0u;
-    for (int w = 0; w < 16; ++w) {
-      if (w < wave) mine += Sums[w];
-      all += Sums[w];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = base + 4 * threadIdx.x + i;
-      if (at < n) s.counts[at] = mine;
-      mine += c[i];
-    }
-    before += all;
+    if (threadIdx.x < kBins) s.counts[tile * kBins + threadIdx.x] = Count[threadIdx.x];
     __syncthreads();
   }
 }
 
-// Lanes of the wave whose 8-bit digit is this lane's, among those in `in`.
-__device__ __forceinline__ uint64_t same_digit(uint32_t digit, uint64_t in) {
+// Places before each (tile, bin), in the order of the bins and in each that of
+// the tiles: a workgroup's threads take a bin each, two for every other tile.
+constexpr int kHalves = kSortThreads / kBins;
+__device__ __forceinline__ uint32_t places_before(const SortPass &s, int64_t tile,
+                                                  uint32_t (*half)[kBins], uint32_t *buf) {
+  const int bin = threadIdx.x % kBins, h = threadIdx.x / kBins;
+  uint32_t before = 0u, all = 0u;
+  for (int64_t t0 = h; t0 < s.tiles; t0 += 16 * kHalves) {
+    uint32_t v[16];
 #pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    const bool bit = digit >> b & 1u;
-    const uint64_t set = __ballot(bit);
-    in &= bit ? set : ~set;
+    for (int k = 0; k < 16; ++k) {
+      const int64_t t = t0 + k * kHalves;
+      v[k] = s.counts[(t < s.tiles ? t : t0) * kBins + bin];
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int64_t t = t0 + k * kHalves;
+      before += t < tile ? v[k] : 0u;
+      all += t < s.tiles ? v[k] : 0u;
+    }
   }
-  return in;
+  half[h][bin] = before;
+  half[kHalves + h][bin] = all;
+  __syncthreads();
+  before = all = 0u;
+  if (h == 0)
+    for (int k = 0; k < kHalves; ++k) {
+      before += half[k][bin];
+      all += half[kHalves + k][bin];
+    }
+  return before + sum_before(all, buf);
 }
 
-__global__ __launch_bounds__(kThreads) void embed_scatter_kernel(EmbedArgs p, SortPass s) {
-  __shared__ uint32_t Count[kWavesPer][kBins];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The same for more tiles, in place, by one workgroup in a launch of its own.
+__global__ __launch_bounds__(kSortThreads) void embed_offsets_kernel(SortPass s) {
+  __shared__ uint32_t Half[2 * kHalves][kBins];
+  __shared__ uint32_t Buf[kSortWaves];
+  uint32_t at = places_before(s, 0, Half, Buf);
+  if (threadIdx.x >= kBins) return;
+  for (int64_t t = 0; t < s.tiles; ++t) {
+    const uint32_t c = s.counts[t * kBins + threadIdx.x];
+    s.counts[t * kBins + threadIdx.x] = at;
+    at += c;
+  }
+}
+
+// kOwn: the counts are those of each tile, and each workgroup forms the places
+// of its own.
+template <int kPer, bool kOwn>
+__global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(EmbedArgs p, SortPass s) {
+  __shared__ uint32_t Count[kSortWaves][kBins];
+  __shared__ uint32_t Half[2 * kHalves][kBins];
+  __shared__ uint32_t Buf[kSortWaves];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const uint32_t mask = (1u << s.bits) - 1u;
   for (int64_t tile = blockIdx.x; tile < s.tiles; tile += gridDim.x) {
-#pragma unroll
-    for (int w = 0; w < kWavesPer; ++w) Count[w][threadIdx.x] = 0u;
-    __syncthreads();
-    uint32_t key[kPer], rank[kPer];
+    uint32_t key[kPer], rank[kPer], pos[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int64_t at = sort_index(tile, i);
-      const bool in = at < p.tokens;
-      key[i] = in ? sort_key(p, s, at) : 0u;
-      const uint32_t digit = key[i] >> s.shift & 255u;
-      const uint64_t same = same_digit(digit, __ballot(in));
-      const int first = __ffsll(static_cast<unsigned long long>(same)) - 1;
-      uint32_t old = 0u;
-      if (in && lane == first)
-        old = atomicAdd(&Count[wave][digit], static_cast<uint32_t>(__popcll(same)));
-      old = __shfl(old, first < 0 ? 0 : first);
-      rank[i] = old + __popcll(same & ((uint64_t(1) << lane) - 1));
+      const int64_t at = sort_index<kPer>(tile, i);
+      key[i] = at < p.tokens ? sort_key(p, s, at) : 0u;
+      pos[i] = s.pos && at < p.tokens ? s.pos[at] : static_cast<uint32_t>(at);
     }
+    for (int i = tid; i < kSortWaves * kBins; i += kSortThreads) (&Count[0][0])[i] = 0u;
+    uint32_t before = 0u;
+    if constexpr (kOwn)
+      before = places_before(s, tile, Half, Buf);
+    else if (tid < kBins)
+      before = s.counts[tile * kBins + tid];
     __syncthreads();
-    {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      rank[i] = rank_of(key[i] >> s.shift & mask, sort_index<kPer>(tile, i) < p.tokens, s.bits,
+                        Count[wave]);
+    __syncthreads();
+    if (tid < kBins) {
       // places of the tile's keys with this thread's digit, wave after wave
-      uint32_t at = s.counts[threadIdx.x * s.tiles + tile];
 #pragma unroll
-      for (int w = 0; w < kWavesPer; ++w) {
-        const uint32_t c = Count[w][threadIdx.x];
-        Count[w][threadIdx.x] = at;
-        at += c;
+      for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = Count[w][tid];
+        Count[w][tid] = before;
+        before += c;
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int64_t at = sort_index(tile, i);
-      if (at < p.tokens) {
-        const uint32_t to = Count[wave][key[i] >> s.shift & 255u] + rank[i];
+    for (int i = 0; i < kPer; ++i)
+      if (sort_index<kPer>(tile, i) < p.tokens) {
+        const uint32_t to = Count[wave][key[i] >> s.shift & mask] + rank[i];
         s.keys_out[to] = key[i];
-        s.pos_out[to] = s.pos ? s.pos[at] : static_cast<uint32_t>(at);
+        s.pos_out[to] = pos[i];
       }
-    }
     __syncthreads();
   }
 }
@@ -194,11 +371,6 @@ struct Runs {
   int64_t runs, row;           // elements of a partial row
   int len;                     // sorted tokens a run has, at most 64
 };
-
-// Whether the ids of sorted tokens i and i + 1 differ or the list ends there.
-__device__ __forceinline__ bool ends_at(const EmbedArgs &p, const Runs &r, int64_t i) {
-  return i + 1 >= p.tokens || r.keys[i + 1] != r.keys[i];
-}
 
 template <typename W, int kN>
 __device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q, float (&v)[kN]) {
@@ -217,25 +389,24 @@ __device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q,
 // A wave takes one run and 64 pieces of the columns.
 template <typename T, typename W, int kN>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r) {
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t run = static_cast<int64_t>(blockIdx.x) * kWavesPer + wave;
-  if (run >= r.runs) return;
   const int pieces = (p.dim + kN - 1) / kN;
-  const int q = blockIdx.y * 64 + lane;
+  const int cols = (pieces + 63) / 64;
+  const uint32_t at = blockIdx.x * kWavesPer + wave;
+  const int64_t run = at / cols;
+  if (run >= r.runs) return;
+  const int q = static_cast<int>(at % cols) * 64 + lane;
   const int64_t from = run * r.len;
   const int n = static_cast<int>(p.tokens - from < r.len ? p.tokens - from : r.len);
-  uint32_t key = 0u, pos = 0u;
-  bool end = false;
-  if (lane < n) {
-    key = r.keys[from + lane];
-    pos = r.pos[from + lane];
-    end = ends_at(p, r, from + lane);
-  }
-  const uint64_t ends = __ballot(end);
+  const int64_t mine = from + (lane < n ? lane : n - 1);
+  const uint32_t key = r.keys[mine], pos = r.pos[mine];
+  const uint32_t next = r.keys[mine + 1 < p.tokens ? mine + 1 : mine];
   // the first id may have begun in a run before
-  bool came = from > 0 && r.keys[from - 1] == __shfl(key, 0);
+  bool came = from > 0 && r.keys[from > 0 ? from - 1 : 0] ==
+                              static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(key));
+  const uint64_t ends = __ballot(next != key || mine + 1 >= p.tokens);
   float acc[kN];
 #pragma unroll
   for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
@@ -246,8 +417,8 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r
     for (int k = 0; k < kAhead; ++k) {
       const int at = j + k < n ? j + k : n - 1;
       const int64_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(pos, at));
-      dy[k].zero();
-      if (q < pieces) load_piece(dy[k], static_cast<const T *>(p.dy) + t * p.dy_stride, q, p.dim);
+      load_piece(dy[k], static_cast<const T *>(p.dy) + t * p.dy_stride, q < pieces ? q : pieces - 1,
+                 p.dim);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -271,51 +442,88 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r
 }
 
 // The run in which an id begins that goes on behind it adds the partial rows
-// of that id.  A workgroup a run and 64 pieces of the columns; its waves take
-// the partial rows in turn.
+// of that id, for 64 pieces of the columns: a wave by itself up to kAlone of
+// them, more by the workgroup's waves together.
+constexpr int kJoinWaves = 16, kAlone = 8;
 template <typename W, int kN>
-__global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedArgs p, Runs r) {
-  __shared__ float Sums[kWavesPer][kN][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t run = blockIdx.x;
-  const int64_t last = (run + 1) * r.len - 1;
-  if (last >= p.tokens - 1) return;
-  const uint32_t key = r.keys[last];
-  if (key >= p.vocab || r.keys[last + 1] != key) return;
-  const int64_t from = run * r.len;
-  if (r.keys[from] == key && from > 0 && r.keys[from - 1] == key) return;
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs p, Runs r) {
+  __shared__ float Sums[kJoinWaves][kN][64];
+  __shared__ int64_t Behind[kJoinWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t run0 = static_cast<int64_t>(blockIdx.x) * kJoinWaves, run = run0 + wave;
   const int pieces = (p.dim + kN - 1) / kN;
   const int q = blockIdx.y * 64 + lane;
   float acc[kN];
+  // the first partial row of the id that begins in a run, and every `step`-th
+  // behind it
+  auto sum = [&](int64_t of, int64_t first, int64_t n, int64_t step) __attribute__((always_inline)) {
 #pragma unroll
-  for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
-  if (q < pieces) {
-    if (wave == 0) get_piece<float, kN>(r.parts + (run * 2 + 1) * r.row, q, p.dim, acc);
-    for (int64_t c = run + 1 + wave; c < r.runs && r.keys[c * r.len] == key; c += kWavesPer) {
-      float v[kN];
-      get_piece<float, kN>(r.parts + c * 2 * r.row, q, p.dim, v);
+    for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
+    const int at = q < pieces ? q : pieces - 1;
+    const float *part = r.parts + (of + 1) * 2 * r.row;
+    if (first == 0) get_piece<float, kN>(part - r.row, at, p.dim, acc);
+    for (int64_t c = first; c < n; c += kAlone * step) {
+      Piece<float, kN> v[kAlone];
 #pragma unroll
-      for (int e = 0; e < kN; ++e) acc[e] += v[e];
+      for (int k = 0; k < kAlone; ++k) {
+        const int64_t row = c + k * step < n ? c + k * step : c;
+        load_piece(v[k], part + row * 2 * r.row, at, p.dim);
+      }
+#pragma unroll
+      for (int k = 0; k < kAlone; ++k)
+#pragma unroll
+        for (int e = 0; e < kN; ++e) acc[e] += c + k * step < n ? v[k][e] : 0.0f;
+    }
+  };
+  const int64_t from = run * r.len, last = from + r.len - 1;
+  int64_t behind = 0;
+  if (last < p.tokens - 1) {
+    const uint32_t key = r.keys[last], next = r.keys[last + 1], begin = r.keys[from];
+    const uint32_t before = r.keys[from > 0 ? from - 1 : 0];
+    if (key < p.vocab && next == key && !(from > 0 && begin == key && before == key)) {
+      // the runs behind that begin with the id, 64 looked at at once
+      for (;;) {
+        const int64_t c = run + 1 + behind + lane;
+        const bool on = c < r.runs && r.keys[c < r.runs ? c * r.len : 0] == key;
+        const int more = __popcll(__ballot(on));
+        behind += more;
+        if (more < 64) break;
+      }
+      if (behind <= kAlone) {
+        sum(run, 0, behind, 1);
+        if (q < pieces) put_sum<W, kN>(p, key, q, acc);
+        behind = 0;
+      }
     }
   }
-#pragma unroll
-  for (int e = 0; e < kN; ++e) Sums[wave][e][lane] = acc[e];
+  if (lane == 0) Behind[wave] = behind;
   __syncthreads();
-  if (wave == 0 && q < pieces) {
+  for (int w = 0; w < kJoinWaves; ++w) {
+    const int64_t n = Behind[w];
+    if (n == 0) continue;
+    sum(run0 + w, wave, n, kJoinWaves);
 #pragma unroll
-    for (int e = 0; e < kN; ++e)
-      acc[e] = (Sums[0][e][lane] + Sums[1][e][lane]) + (Sums[2][e][lane] + Sums[3][e][lane]);
-    put_sum<W, kN>(p, key, q, acc);
+    for (int e = 0; e < kN; ++e) Sums[wave][e][lane] = acc[e];
+    __syncthreads();
+    if (wave == 0 && q < pieces) {
+      for (int k = 1; k < kJoinWaves; ++k)
+#pragma unroll
+        for (int e = 0; e < kN; ++e) acc[e] += Sums[k][e][lane];
+      put_sum<W, kN>(p, r.keys[(run0 + w + 1) * r.len - 1], q, acc);
+    }
+    __syncthreads();
   }
 }
 
-// Zeros in the rows of ids that do not come.  A wave takes 32 rows; lane l
-// finds where id l of them begins in the sorted list.
+// Zeros in the rows of ids that do not come, behind the long sort.  A wave
+// looks for 32 rows; lane l finds where id l of them begins in the sorted list.
 template <typename W>
 __global__ __launch_bounds__(kThreads) void embed_clear_kernel(EmbedArgs p, const uint32_t *keys) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWavesPer + (threadIdx.x >> 6)) * 32;
-  const int64_t want = row0 + (lane < 32 ? lane : 32);
+  __shared__ uint32_t There[kWavesPer];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (32 * kWavesPer);
+  const int64_t want = row0 + wave * 32 + (lane < 32 ? lane : 32);
   int64_t lo = 0, hi = p.tokens;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
@@ -326,93 +534,121 @@ __global__ __launch_bounds__(kThreads) void embed_clear_kernel(EmbedArgs p, cons
   }
   const int64_t next = __shfl_down(lo, 1);
   const uint64_t there = __ballot(lane < 32 && next > lo);
-  constexpr int kN = 16 / sizeof(W);
-  const int pieces = (p.dim + kN - 1) / kN;
-  float zero[kN];
-#pragma unroll
-  for (int e = 0; e < kN; ++e) zero[e] = 0.0f;
-  for (int k = 0; k < 32 && row0 + k < p.vocab; ++k) {
-    if (there >> k & 1) continue;
-    W *row = static_cast<W *>(p.dweight) + (row0 + k) * p.dim;
-    for (int q = lane; q < pieces; q += 64) store_piece<W, kN>(row, q, p.dim, zero);
-  }
+  if (lane == 0) There[wave] = static_cast<uint32_t>(there);
+  __syncthreads();
+  const int64_t row1 = row0 + 32 * kWavesPer < p.vocab ? row0 + 32 * kWavesPer : p.vocab;
+  clear_rows<W>(p, row0, row1, There);
 }
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Sorted tokens a run has.
 constexpr int kRunLen = 32;
 
 // Workspace: two lists of keys and positions, the counts, the partial rows.
 struct Layout {
   int64_t tiles, runs, row;
-  int len;
+  int len, per;  // sorted tokens a run has; keys a thread of the long sort has
   int64_t keys[2], pos[2], counts, parts, bytes;
 };
 Layout layout_of(int64_t tokens, int64_t dim) {
   Layout l;
-  l.tiles = (tokens + kTile - 1) / kTile;
-  l.len = kRunLen;
+  l.per = tokens <= kOwnTiles / 2 * kSortThreads ? 1 : 4;
+  l.tiles = (tokens + l.per * kSortThreads - 1) / (l.per * kSortThreads);
+  l.len = getenv("E_RUN") ? atoi(getenv("E_RUN")) : kRunLen;
   l.runs = (tokens + l.len - 1) / l.len;
   l.row = up(dim, 4);
+  const int lists = tokens > kShort ? 2 : 1;
   int64_t at = 0;
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < lists; ++i) {
     l.keys[i] = at;
     at += up(tokens * 4, 256);
     l.pos[i] = at;
     at += up(tokens * 4, 256);
   }
   l.counts = at;
-  at += up(l.tiles * kBins * 4, 256);
+  if (lists > 1) at += up(l.tiles * kBins * 4, 256);
   l.parts = at;
   at += l.runs > 1 ? l.runs * 2 * l.row * 4 : 0;
   l.bytes = at;
   return l;
 }
 
+// Passes and bits a pass for keys 0..vocab.
+void digits_of(int64_t vocab, int &passes, int &bits) {
+  int all = 1;
+  while (vocab >> all) ++all;
+  passes = (all + kMaxBits - 1) / kMaxBits;
+  bits = (all + passes - 1) / passes;
+}
+
 template <typename T, typename W, int kN>
 int launch_bwd(const EmbedArgs &a, hipStream_t s) {
+  const unsigned clears = static_cast<unsigned>((a.vocab + 32 * kWavesPer - 1) / (32 * kWavesPer));
   if (a.tokens == 0) {
     if (a.accumulate) return 0;
-    hipLaunchKernelGGL(embed_clear_kernel<W>, dim3((a.vocab + 127) / 128), dim3(kThreads), 0, s, a,
-                       nullptr);
+    hipLaunchKernelGGL(embed_clear_kernel<W>, dim3(clears), dim3(kThreads), 0, s, a, nullptr);
     return static_cast<int>(hipGetLastError());
   }
   const Layout l = layout_of(a.tokens, a.dim);
   char *ws = static_cast<char *>(a.workspace);
   auto words = [&](int64_t at) { return reinterpret_cast<uint32_t *>(ws + at); };
-  SortPass sort{nullptr, nullptr, words(l.keys[0]), words(l.pos[0]), words(l.counts), l.tiles, 0};
-  const dim3 grid(static_cast<unsigned>(l.tiles < 65536 ? l.tiles : 65536));
-  int to = 0;
-  for (int shift = 0; shift == 0 || a.vocab >> shift != 0; shift += 8) {
-    sort.shift = shift;
-    sort.keys_out = words(l.keys[to]);
-    sort.pos_out = words(l.pos[to]);
-    hipLaunchKernelGGL(embed_count_kernel, grid, dim3(kThreads), 0, s, a, sort);
-    hipLaunchKernelGGL(embed_offsets_kernel, dim3(1), dim3(1024), 0, s, sort);
-    hipLaunchKernelGGL(embed_scatter_kernel, grid, dim3(kThreads), 0, s, a, sort);
-    sort.keys = sort.keys_out;
-    sort.pos = sort.pos_out;
+  int passes, bits, to = 0;
+  digits_of(a.vocab, passes, bits);
+  if (a.tokens <= kShort) {
+    int64_t groups = 0, rows_per = 1;
+    if (!a.accumulate) {
+      groups = a.vocab < 255 ? a.vocab : 255;
+      rows_per = (a.vocab + groups - 1) / groups;
+    }
+    hipLaunchKernelGGL(embed_sort_kernel<W>, dim3(static_cast<unsigned>(1 + groups)),
+                       dim3(kSortThreads), 0, s, a, words(l.keys[0]), words(l.pos[0]), passes, bits,
+                       rows_per);
+  } else {
+    SortPass sort{nullptr, nullptr, nullptr, nullptr, words(l.counts), l.tiles, 0, bits};
+    const unsigned grid = static_cast<unsigned>(l.tiles < 65536 ? l.tiles : 65536);
+    for (int pass = 0; pass < passes; ++pass) {
+      sort.shift = pass * bits;
+      sort.keys_out = words(l.keys[to]);
+      sort.pos_out = words(l.pos[to]);
+      auto go = [&](auto kernel, unsigned groups) {
+        hipLaunchKernelGGL(kernel, dim3(groups), dim3(kSortThreads), 0, s, a, sort);
+      };
+      if (l.per == 1) {
+        go(embed_count_kernel<1>, grid);
+        go(embed_scatter_kernel<1, true>, grid);
+      } else if (l.tiles <= kOwnTiles) {
+        go(embed_count_kernel<4>, grid);
+        go(embed_scatter_kernel<4, true>, grid);
+      } else {
+        go(embed_count_kernel<4>, grid);
+        hipLaunchKernelGGL(embed_offsets_kernel, dim3(1), dim3(kSortThreads), 0, s, sort);
+        go(embed_scatter_kernel<4, false>, grid);
+      }
+      sort.keys = sort.keys_out;
+      sort.pos = sort.pos_out;
+      to ^= 1;
+    }
     to ^= 1;
   }
-  const Runs r{sort.keys, sort.pos, reinterpret_cast<float *>(ws + l.parts), l.runs, l.row, l.len};
+  const Runs r{words(l.keys[to]), words(l.pos[to]), reinterpret_cast<float *>(ws + l.parts), l.runs,
+               l.row, l.len};
   const unsigned cols = static_cast<unsigned>(((a.dim + kN - 1) / kN + 63) / 64);
   hipLaunchKernelGGL((embed_sum_kernel<T, W, kN>),
-                     dim3(static_cast<unsigned>((l.runs + kWavesPer - 1) / kWavesPer), cols),
+                     dim3(static_cast<unsigned>((l.runs * cols + kWavesPer - 1) / kWavesPer)),
                      dim3(kThreads), 0, s, a, r);
   if (l.runs > 1)
-    hipLaunchKernelGGL((embed_join_kernel<W, kN>), dim3(static_cast<unsigned>(l.runs), cols),
-                       dim3(kThreads), 0, s, a, r);
-  if (!a.accumulate)
-    hipLaunchKernelGGL(embed_clear_kernel<W>, dim3(static_cast<unsigned>((a.vocab + 127) / 128)),
-                       dim3(kThreads), 0, s, a, r.keys);
+    hipLaunchKernelGGL((embed_join_kernel<W, kN>),
+                       dim3(static_cast<unsigned>((l.runs + kJoinWaves - 1) / kJoinWaves), cols),
+                       dim3(64 * kJoinWaves), 0, s, a, r);
+  if (!a.accumulate && a.tokens > kShort)
+    hipLaunchKernelGGL(embed_clear_kernel<W>, dim3(clears), dim3(kThreads), 0, s, a, r.keys);
   return static_cast<int>(hipGetLastError());
 }
 
 template <typename W, typename T, int kN>
 int launch_fwd(const EmbedArgs &a, hipStream_t s) {
   const int pieces = (a.dim + kN - 1) / kN;
-  const int rows_per = pieces >= 512 ? 1 : 512 / pieces;
+  const int rows_per = pieces >= 1024 ? 1 : 1024 / pieces;
   const int64_t groups = (a.tokens + rows_per - 1) / rows_per;
   hipLaunchKernelGGL((embed_fwd_kernel<W, T, kN>),
                      dim3(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20)),
@@ -423,21 +659,21 @@ int launch_fwd(const EmbedArgs &a, hipStream_t s) {
 }  // namespace
 
 int64_t embed_bwd_workspace(int64_t tokens, int64_t, int64_t dim) {
-  return layout_of(tokens, dim).bytes;
+  return tokens == 0 ? 0 : layout_of(tokens, dim).bytes;
 }
 
 int launch_embed_fwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (w_bf16)
-    return bf16 ? launch_fwd<uint16_t, uint16_t, 8>(a, s) : launch_fwd<uint16_t, float, 8>(a, s);
+    return bf16 ? launch_fwd<uint16_t, uint16_t, 8>(a, s) : launch_fwd<uint16_t, float, 4>(a, s);
   return bf16 ? launch_fwd<float, uint16_t, 8>(a, s) : launch_fwd<float, float, 4>(a, s);
 }
 
 int launch_embed_bwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (bf16)
-    return w_bf16 ? launch_bwd<uint16_t, uint16_t, 8>(a, s) : launch_bwd<uint16_t, float, 8>(a, s);
-  return w_bf16 ? launch_bwd<float, uint16_t, 8>(a, s) : launch_bwd<float, float, 4>(a, s);
+    return w_bf16 ? launch_bwd<uint16_t, uint16_t, 4>(a, s) : launch_bwd<uint16_t, float, 4>(a, s);
+  return w_bf16 ? launch_bwd<float, uint16_t, 4>(a, s) : launch_bwd<float, float, 4>(a, s);
 }
 
 }  // namespace ssm

@@ -16,10 +16,12 @@ namespace ssm {
 namespace dev {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
 typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
 
-// kN (a multiple of 8 for bf16, of 4 for fp32) elements as they are in memory.
+// kN (a multiple of 4) elements as they are in memory.
 template <typename T, int kN>
 struct Piece {
   static constexpr int kWords = kN * static_cast<int>(sizeof(T)) / 4;
@@ -29,6 +31,11 @@ struct Piece {
     for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
   __device__ __forceinline__ void load(const T *p) {
+    if constexpr (kWords == 2) {
+      const u32x2_t x = *reinterpret_cast<const u32x2_a2 *>(p);
+      w[0] = x[0];
+      w[1] = x[1];
+    }
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
       u32x4_t x;
@@ -72,6 +79,7 @@ struct Piece {
     }
   }
   __device__ __forceinline__ void store(T *p) const {
+    if constexpr (kWords == 2) *reinterpret_cast<u32x2_a2 *>(p) = u32x2_t{w[0], w[1]};
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
       const u32x4_t x{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
