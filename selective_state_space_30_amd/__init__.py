@@ -54,6 +54,7 @@ import array
 import ctypes
 import functools
 import inspect
+import operator
 import os
 import threading
 
@@ -1411,27 +1412,41 @@ def _fills_its_memory(t):
     return True
 
 
+_data_ptr, _numel, _is_contiguous, _get_device = (
+    torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.get_device)
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _tensors(ts, name, dev):
     """Host arrays of the addresses, sizes and types of a list of tensors, and
     whether all are contiguous."""
-    index, dense = dev.index, True
-    ptrs, sizes, codes = array.array("Q"), array.array("q"), array.array("i")
+    try:
+        codes = array.array("i", map(_CODES.__getitem__, map(_dtype_of, ts)))
+        ptrs = array.array("Q", map(_data_ptr, ts))
+        dense = all(map(_is_contiguous, ts))
+        fine = set(map(_get_device, ts)) <= {dev.index}
+    except (AttributeError, KeyError, TypeError):
+        fine = False
+    if not (fine and dense):
+        dense = _check_tensors(ts, name, dev)
+    return ptrs, array.array("q", map(_numel, ts)), codes, dense
+
+
+def _check_tensors(ts, name, dev):
+    """Says what is wrong with a list of tensors, or whether all are contiguous."""
+    dense = True
     for i, t in enumerate(ts):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s[%d] must be a torch.Tensor" % (name, i))
-        code = _CODES.get(t.dtype)
-        if code is None:
+        if t.dtype not in _CODES:
             raise TypeError("%s[%d] must be float32 or bfloat16, got %s" % (name, i, t.dtype))
-        if t.get_device() != index or not t.is_cuda:
+        if t.device != dev:
             raise ValueError("%s[%d] is on %s, expected %s" % (name, i, t.device, dev))
         if not t.is_contiguous():
             dense = False
             if not _fills_its_memory(t):
                 raise ValueError("%s[%d] has gaps between its elements" % (name, i))
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel())
-        codes.append(code)
-    return ptrs, sizes, codes, dense
+    return dense
 
 
 def _at(a):

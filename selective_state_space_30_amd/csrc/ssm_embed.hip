@@ -13,7 +13,6 @@
 // spread over as many waves as there are runs of it.
 #include "ssm_model_internal.h"
 #include "ssm_pieces.h"
-#include <cstdlib>
 
 namespace ssm {
 namespace {
@@ -372,22 +371,31 @@ struct Runs {
   int len;                     // sorted tokens a run has, at most 64
 };
 
+template <typename W>
+__device__ __forceinline__ W *row_of(const EmbedArgs &p, uint32_t key) {
+  return static_cast<W *>(p.dweight) + static_cast<int64_t>(key) * p.dim;
+}
+// old: what is there, 0 where the sum is written instead of added
 template <typename W, int kN>
-__device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q, float (&v)[kN]) {
-  W *row = static_cast<W *>(p.dweight) + static_cast<int64_t>(key) * p.dim;
+__device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q,
+                                        const float (&sum)[kN], const Piece<W, kN> &old) {
+  float v[kN];
 #pragma unroll
-  for (int e = 0; e < kN; ++e) v[e] *= p.scale;
-  if (p.accumulate) {
-    float old[kN];
-    get_piece<W, kN>(row, q, p.dim, old);
-#pragma unroll
-    for (int e = 0; e < kN; ++e) v[e] += old[e];
-  }
-  store_piece<W, kN>(row, q, p.dim, v);
+  for (int e = 0; e < kN; ++e) v[e] = fmaf(sum[e], p.scale, old[e]);
+  store_piece<W, kN>(row_of<W>(p, key), q, p.dim, v);
+}
+template <typename W, int kN>
+__device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q,
+                                        const float (&sum)[kN]) {
+  Piece<W, kN> old;
+  old.zero();
+  if (p.accumulate) load_piece(old, row_of<W>(p, key), q, p.dim);
+  put_sum<W, kN>(p, key, q, sum, old);
 }
 
-// A wave takes one run and 64 pieces of the columns.
-template <typename T, typename W, int kN>
+// A wave takes one run and 64 pieces of the columns.  kAdd: the rows to add to
+// are asked for together with those of dy.
+template <typename T, typename W, int kN, bool kAdd>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r) {
   constexpr int kAhead = 8;
   const int lane = threadIdx.x & 63;
@@ -411,14 +419,21 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r
 #pragma unroll
   for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
   float *part = r.parts + run * 2 * r.row;
+  const int safe = q < pieces ? q : pieces - 1;
   for (int j = 0; j < n; j += kAhead) {
     Piece<T, kN> dy[kAhead];
+    Piece<W, kN> old[kAdd ? kAhead : 1];
+    old[0].zero();
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int at = j + k < n ? j + k : n - 1;
       const int64_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(pos, at));
-      load_piece(dy[k], static_cast<const T *>(p.dy) + t * p.dy_stride, q < pieces ? q : pieces - 1,
-                 p.dim);
+      load_piece(dy[k], static_cast<const T *>(p.dy) + t * p.dy_stride, safe, p.dim);
+      if constexpr (kAdd) {
+        const uint32_t id = __builtin_amdgcn_readlane(key, at);
+        if (j + k < n && (ends >> at & 1) && id < p.vocab)
+          load_piece(old[k], row_of<W>(p, id), safe, p.dim);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -430,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r
       if (!stop && j + k < n - 1) continue;
       if (id < p.vocab && q < pieces) {
         if (stop && !came)
-          put_sum<W, kN>(p, id, q, acc);
+          put_sum<W, kN>(p, id, q, acc, old[kAdd ? k : 0]);
         else
           store_piece<float, kN>(part + (came ? 0 : r.row), q, p.dim, acc);
       }
@@ -554,7 +569,7 @@ Layout layout_of(int64_t tokens, int64_t dim) {
   Layout l;
   l.per = tokens <= kOwnTiles / 2 * kSortThreads ? 1 : 4;
   l.tiles = (tokens + l.per * kSortThreads - 1) / (l.per * kSortThreads);
-  l.len = getenv("E_RUN") ? atoi(getenv("E_RUN")) : kRunLen;
+  l.len = kRunLen;
   l.runs = (tokens + l.len - 1) / l.len;
   l.row = up(dim, 4);
   const int lists = tokens > kShort ? 2 : 1;
@@ -633,9 +648,11 @@ int launch_bwd(const EmbedArgs &a, hipStream_t s) {
   const Runs r{words(l.keys[to]), words(l.pos[to]), reinterpret_cast<float *>(ws + l.parts), l.runs,
                l.row, l.len};
   const unsigned cols = static_cast<unsigned>(((a.dim + kN - 1) / kN + 63) / 64);
-  hipLaunchKernelGGL((embed_sum_kernel<T, W, kN>),
-                     dim3(static_cast<unsigned>((l.runs * cols + kWavesPer - 1) / kWavesPer)),
-                     dim3(kThreads), 0, s, a, r);
+  const dim3 waves(static_cast<unsigned>((l.runs * cols + kWavesPer - 1) / kWavesPer));
+  if (a.accumulate)
+    hipLaunchKernelGGL((embed_sum_kernel<T, W, kN, true>), waves, dim3(kThreads), 0, s, a, r);
+  else
+    hipLaunchKernelGGL((embed_sum_kernel<T, W, kN, false>), waves, dim3(kThreads), 0, s, a, r);
   if (l.runs > 1)
     hipLaunchKernelGGL((embed_join_kernel<W, kN>),
                        dim3(static_cast<unsigned>((l.runs + kJoinWaves - 1) / kJoinWaves), cols),

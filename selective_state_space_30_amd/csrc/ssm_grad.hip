@@ -54,9 +54,9 @@ __device__ __forceinline__ int tensor_of(const GradTable &t, uint32_t chunk) {
 }
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T *g, int64_t n) {
+__device__ __forceinline__ double chunk_squares(const T *g, int n) {
   double acc[2] = {0.0, 0.0};
-  int64_t at = static_cast<int64_t>(threadIdx.x) * 8;
+  int at = threadIdx.x * 8;
   auto add = [&](const Piece<T, 8> &x) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -73,11 +73,11 @@ __device__ __forceinline__ double chunk_squares(const T *g, int64_t n) {
   }
   for (; at < n; at += kThreads * 8) {
     Piece<T, 8> x;
-    const int q = static_cast<int>(at / 8), size = static_cast<int>(n);
-    load_piece(x, g, q, size);
+    const int q = at / 8;
+    load_piece(x, g, q, n);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const double v = in_piece<8>(q, e, size) ? static_cast<double>(x[e]) : 0.0;
+      const double v = in_piece<8>(q, e, n) ? static_cast<double>(x[e]) : 0.0;
       acc[e % 2] = fma(v, v, acc[e % 2]);
     }
   }
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradTable t, dou
     const int k = tensor_of(t, c);
     const int64_t from = static_cast<int64_t>(c - t.first[k]) * kGradChunk;
     const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
-    const int64_t n = size < kGradChunk ? size : kGradChunk;
+    const int n = static_cast<int>(size < kGradChunk ? size : kGradChunk);
     if (t.size[k] & kGradBf16)
       acc += chunk_squares(static_cast<const uint16_t *>(t.grad[k]) + from, n);
     else
@@ -109,15 +109,14 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double *sums,
 }
 
 template <typename T, typename W>
-__device__ __forceinline__ void scale_chunk(const T *g, W *out, int64_t n, float c) {
-  const int size = static_cast<int>(n);
-  auto put = [&](const Piece<T, 8> &x, int64_t at) __attribute__((always_inline)) {
+__device__ __forceinline__ void scale_chunk(const T *g, W *out, int n, float c) {
+  auto put = [&](const Piece<T, 8> &x, int at) __attribute__((always_inline)) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = x[e] * c;
-    store_piece<W, 8>(out, static_cast<int>(at / 8), size, v);
+    store_piece<W, 8>(out, at / 8, n, v);
   };
-  int64_t at = static_cast<int64_t>(threadIdx.x) * 8;
+  int at = threadIdx.x * 8;
   for (; at + 3 * kThreads * 8 + 8 <= n; at += 4 * kThreads * 8) {
     Piece<T, 8> x[4];
 #pragma unroll
@@ -127,7 +126,7 @@ __device__ __forceinline__ void scale_chunk(const T *g, W *out, int64_t n, float
   }
   for (; at < n; at += kThreads * 8) {
     Piece<T, 8> x;
-    load_piece(x, g, static_cast<int>(at / 8), size);
+    load_piece(x, g, at / 8, n);
     put(x, at);
   }
 }
@@ -145,11 +144,13 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable t, GradO
   const double limit = static_cast<double>(max_norm);
   const float c = finite && total > limit ? static_cast<float>(limit / total) : 1.0f;
   if (in_place && c == 1.0f) return;
-  for (uint32_t i = blockIdx.x; i < t.first[t.n]; i += gridDim.x) {
+  // from the end, which was read last and may still be in the last-level cache
+  for (uint32_t j = blockIdx.x; j < t.first[t.n]; j += gridDim.x) {
+    const uint32_t i = t.first[t.n] - 1 - j;
     const int k = tensor_of(t, i);
     const int64_t from = static_cast<int64_t>(i - t.first[k]) * kGradChunk;
     const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
-    const int64_t n = size < kGradChunk ? size : kGradChunk;
+    const int n = static_cast<int>(size < kGradChunk ? size : kGradChunk);
     const void *g = t.grad[k];
     void *out = o.out[k];
     if (t.size[k] & kGradBf16) {

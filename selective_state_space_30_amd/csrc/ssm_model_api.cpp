@@ -284,54 +284,52 @@ int check_grad_overlaps(const Grads &c, bool clip, const Span *more, int nmore) 
 
 int64_t chunks_of(int64_t size) { return (size + ssm::kGradChunk - 1) / ssm::kGradChunk; }
 
-// Tables of up to kGradTensors tensors, one after another: run(table, outs, last).
-template <typename F>
-int for_tables(const Grads &c, F &&run) {
-  ssm::GradTable t;
-  ssm::GradOuts o;
-  int64_t i = 0;
-  bool any = false;
-  while (i < c.n || !any) {
-    any = true;
-    t.n = 0;
-    t.first[0] = 0;
-    for (; i < c.n && t.n < ssm::kGradTensors; ++i) {
-      if (c.sizes[i] == 0) continue;
-      const int64_t chunks = chunks_of(c.sizes[i]);
-      if (t.n > 0 && t.first[t.n] + chunks > (int64_t(1) << 31)) break;
-      const int out_dtype = c.outs ? c.out_dtypes[i] : c.dtypes[i];
-      t.grad[t.n] = c.grads[i];
-      o.out[t.n] = c.outs ? c.outs[i] : const_cast<void *>(c.grads[i]);
-      t.size[t.n] = static_cast<uint64_t>(c.sizes[i]) |
-                    (c.dtypes[i] == SSM_DTYPE_BF16 ? ssm::kGradBf16 : 0) |
-                    (out_dtype == SSM_DTYPE_BF16 ? ssm::kGradOutBf16 : 0);
-      t.first[t.n + 1] = t.first[t.n] + static_cast<uint32_t>(chunks);
-      ++t.n;
+// The tensors of a call as entries of at most kGradPiece elements, in tables of
+// equal numbers of entries.
+struct Tables {
+  std::vector<ssm::GradTable> t;
+  std::vector<ssm::GradOuts> o;
+  int groups = 1;  // workgroups, and sums, of a launch
+
+  explicit Tables(const Grads &c) {
+    int64_t entries = 0;
+    for (int64_t i = 0; i < c.n; ++i)
+      entries += (c.sizes[i] + ssm::kGradPiece - 1) / ssm::kGradPiece;
+    const int64_t tables = std::max<int64_t>(1, (entries + ssm::kGradTensors - 1) / ssm::kGradTensors);
+    const int64_t each = (entries + tables - 1) / tables;
+    t.resize(tables);
+    o.resize(tables);
+    int64_t k = 0;
+    for (auto &table : t) table.n = 0, table.first[0] = 0;
+    for (int64_t i = 0; i < c.n; ++i) {
+      const int in = c.dtypes[i], out = c.outs ? c.out_dtypes[i] : in;
+      const char *g = static_cast<const char *>(c.grads[i]);
+      char *w = static_cast<char *>(c.outs ? c.outs[i] : const_cast<void *>(c.grads[i]));
+      for (int64_t at = 0; at < c.sizes[i]; at += ssm::kGradPiece) {
+        if (t[k].n == each) ++k;
+        ssm::GradTable &table = t[k];
+        const int64_t size = std::min(c.sizes[i] - at, ssm::kGradPiece);
+        table.grad[table.n] = g + at * size_of(in);
+        o[k].out[table.n] = w + at * size_of(out);
+        table.size[table.n] = static_cast<uint32_t>(size) |
+                              (in == SSM_DTYPE_BF16 ? ssm::kGradBf16 : 0u) |
+                              (out == SSM_DTYPE_BF16 ? ssm::kGradOutBf16 : 0u);
+        table.first[table.n + 1] = table.first[table.n] + static_cast<uint32_t>(chunks_of(size));
+        ++table.n;
+      }
     }
-    while (i < c.n && c.sizes[i] == 0) ++i;
-    const int err = run(t, o, i == c.n);
+    uint32_t most = 1;
+    for (const auto &table : t) most = std::max(most, table.first[table.n]);
+    groups = static_cast<int>(std::min<uint32_t>(most, ssm::kGradGroups));
+  }
+};
+
+int form_squares(const Tables &t, double *sums, void *stream) {
+  for (size_t i = 0; i < t.t.size(); ++i) {
+    const int err = ssm::launch_grad_squares(t.t[i], sums, t.groups, i == 0, stream);
     if (err != 0) return err;
   }
   return 0;
-}
-
-// Workgroups, and sums, of the launches of one call.
-int sums_of(const Grads &c) {
-  uint32_t most = 1;
-  for_tables(c, [&](const ssm::GradTable &t, const ssm::GradOuts &, bool) {
-    most = std::max(most, t.first[t.n]);
-    return 0;
-  });
-  return static_cast<int>(std::min<uint32_t>(most, ssm::kGradGroups));
-}
-
-int form_squares(const Grads &c, double *sums, int nsums, void *stream) {
-  bool first = true;
-  return for_tables(c, [&](const ssm::GradTable &t, const ssm::GradOuts &, bool) {
-    const int err = ssm::launch_grad_squares(t, sums, nsums, first, stream);
-    first = false;
-    return err;
-  });
 }
 
 }  // namespace
@@ -498,9 +496,9 @@ int ssm_grad_norm(const void *const *grads, const int64_t *sizes, const int *dty
   const Span more[] = {{norm, 4, "norm"}, {workspace, kGradWorkspace, "workspace"}};
   if ((st = check_grad_overlaps(c, false, more, 2)) != SSM_OK) return st;
   double *sums = static_cast<double *>(workspace);
-  const int nsums = sums_of(c);
-  const int err = form_squares(c, sums, nsums, stream);
-  return done(err != 0 ? err : ssm::launch_grad_norm(sums, nsums, norm, stream));
+  const Tables t(c);
+  const int err = form_squares(t, sums, stream);
+  return done(err != 0 ? err : ssm::launch_grad_norm(sums, t.groups, norm, stream));
 } catch (const std::bad_alloc &) {
   return fail(SSM_ERR_INVALID_ARG, "out of host memory");
 }
@@ -521,13 +519,12 @@ int ssm_grad_clip(const void *const *grads, const int64_t *sizes, const int *dty
                        {have_norm ? nullptr : workspace, kGradWorkspace, "workspace"}};
   if ((st = check_grad_overlaps(c, true, more, 2)) != SSM_OK) return st;
   double *sums = have_norm ? nullptr : static_cast<double *>(workspace);
-  const int nsums = have_norm ? 0 : sums_of(c);
-  int err = have_norm ? 0 : form_squares(c, sums, nsums, stream);
-  if (err == 0)
-    err = for_tables(c, [&](const ssm::GradTable &t, const ssm::GradOuts &o, bool last) {
-      return ssm::launch_grad_scale(t, o, c.outs == nullptr, sums, nsums, max_norm, norm,
-                                    last && !have_norm, stream);
-    });
+  const Tables t(c);
+  int err = have_norm ? 0 : form_squares(t, sums, stream);
+  // the tables from the last one, too, for the last-level cache
+  for (size_t i = t.t.size(); i-- > 0 && err == 0;)
+    err = ssm::launch_grad_scale(t.t[i], t.o[i], outs == nullptr, sums, t.groups, max_norm, norm,
+                                 i == 0 && !have_norm, stream);
   return done(err);
 } catch (const std::bad_alloc &) {
   return fail(SSM_ERR_INVALID_ARG, "out of host memory");

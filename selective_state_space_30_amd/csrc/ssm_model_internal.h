@@ -63,19 +63,20 @@ int launch_layer_norm_fwd(const LayerNormArgs &a, LayerNormTypes types, void *st
 int launch_layer_norm_bwd(const LayerNormArgs &a, LayerNormTypes types, void *stream);
 
 // -------------------------------------------------------- gradients' norm --
-constexpr int kGradTensors = 128;   // tensors a launch takes, in its arguments
-constexpr int kGradGroups = 1024;   // workgroups of a launch, and partial sums
+constexpr int kGradTensors = 160;   // tensors a launch takes, in its arguments
+constexpr int kGradGroups = 1024;   // most partial sums
 constexpr int kGradChunk = 16384;   // elements that a workgroup takes at a time
+constexpr int64_t kGradPiece = int64_t(1) << 29;  // elements of an entry; longer tensors have several
 
 struct GradTable {
   const void *grad[kGradTensors];
-  uint32_t first[kGradTensors + 1];  // chunks before each tensor
+  uint32_t first[kGradTensors + 1];  // chunks before each entry
+  // elements of each entry; its gradient's and its output's types
+  uint32_t size[kGradTensors];
   int32_t n;
-  // elements of each tensor, its gradient's type in bit 62, its output's in 63
-  uint64_t size[kGradTensors];
 };
-constexpr uint64_t kGradBf16 = uint64_t(1) << 62, kGradOutBf16 = uint64_t(1) << 63;
-constexpr uint64_t kGradSize = kGradBf16 - 1;
+constexpr uint32_t kGradBf16 = 1u << 31, kGradOutBf16 = 1u << 30;
+constexpr uint32_t kGradSize = kGradOutBf16 - 1;
 
 struct GradOuts {
   void *out[kGradTensors];
