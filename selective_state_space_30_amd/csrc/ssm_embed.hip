@@ -30,39 +30,38 @@ __device__ __forceinline__ uint32_t key_of(const EmbedArgs &p, int64_t t) {
 }
 
 // ---------------------------------------------------------------- forward --
-// A workgroup takes rows_per rows at a time, their pieces flat over its lanes,
-// kAhead of them in flight.
+// A group of `lanes` (8..64) neighbouring lanes takes a row, kAhead pieces a
+// lane in flight, and then the row `step` rows behind, whose id it has asked
+// for before.
 template <typename W, typename T, int kN>
-__global__ __launch_bounds__(kThreads) void embed_fwd_kernel(EmbedArgs p, int rows_per) {
-  constexpr int kAhead = 4;
-  const uint32_t pieces = (p.dim + kN - 1) / kN;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_per; row0 < p.tokens;
-       row0 += static_cast<int64_t>(gridDim.x) * rows_per) {
-    const int64_t left = p.tokens - row0;
-    const uint32_t all = pieces * static_cast<uint32_t>(left < rows_per ? left : rows_per);
-    for (uint32_t l0 = threadIdx.x; l0 < all; l0 += kAhead * kThreads) {
-      uint32_t row[kAhead], q[kAhead], key[kAhead];
+__global__ __launch_bounds__(kThreads) void embed_fwd_kernel(EmbedArgs p, int lanes) {
+  constexpr int kAhead = 8;
+  const int pieces = (p.dim + kN - 1) / kN, per = kThreads / lanes;
+  const int at = threadIdx.x & (lanes - 1);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes;
+  if (row >= p.tokens) return;
+  uint32_t next = key_of(p, row);
+  for (; row < p.tokens; row += step) {
+    const uint32_t key = next;
+    if (row + step < p.tokens) next = key_of(p, row + step);
+    const bool there = key < p.vocab;
+    const W *from = static_cast<const W *>(p.weight) + (there ? key * p.w_stride : 0);
+    T *to = static_cast<T *>(p.out) + row * p.dim;
+    for (int q0 = at; q0 < pieces; q0 += kAhead * lanes) {
       Piece<W, kN> w[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const uint32_t l = l0 + k * kThreads;
-        row[k] = l / pieces;
-        q[k] = l - row[k] * pieces;
-        key[k] = l < all ? key_of(p, row0 + row[k]) : static_cast<uint32_t>(p.vocab);
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
         w[k].zero();
-        if (key[k] < p.vocab)
-          load_piece(w[k], static_cast<const W *>(p.weight) + key[k] * p.w_stride, q[k], p.dim);
+        if (there && q0 + k * lanes < pieces) load_piece(w[k], from, q0 + k * lanes, p.dim);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (l0 + k * kThreads >= all) break;
+        if (q0 + k * lanes >= pieces) break;
         float v[kN];
 #pragma unroll
-        for (int e = 0; e < kN; ++e) v[e] = key[k] < p.vocab ? w[k][e] * p.scale : 0.0f;
-        store_piece<T, kN>(static_cast<T *>(p.out) + (row0 + row[k]) * p.dim, q[k], p.dim, v);
+        for (int e = 0; e < kN; ++e) v[e] = there ? w[k][e] * p.scale : 0.0f;
+        store_piece<T, kN>(to, q0 + k * lanes, p.dim, v);
       }
     }
   }
@@ -665,11 +664,13 @@ int launch_bwd(const EmbedArgs &a, hipStream_t s) {
 template <typename W, typename T, int kN>
 int launch_fwd(const EmbedArgs &a, hipStream_t s) {
   const int pieces = (a.dim + kN - 1) / kN;
-  const int rows_per = pieces >= 1024 ? 1 : 1024 / pieces;
-  const int64_t groups = (a.tokens + rows_per - 1) / rows_per;
+  int lanes = 8;
+  while (lanes < 64 && lanes < pieces) lanes *= 2;
+  const int64_t per = kThreads / lanes, groups = (a.tokens + per - 1) / per;
+  const int64_t most = 4096;
   hipLaunchKernelGGL((embed_fwd_kernel<W, T, kN>),
-                     dim3(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20)),
-                     dim3(kThreads), 0, s, a, rows_per);
+                     dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(kThreads), 0,
+                     s, a, lanes);
   return static_cast<int>(hipGetLastError());
 }
 

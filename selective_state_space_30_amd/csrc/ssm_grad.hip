@@ -23,25 +23,36 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return v;
 }
 
-// Sum over the workgroup, the same in every thread.
+// Sum over the workgroup's waves, the same in every thread.
+template <int kWaves>
 __device__ __forceinline__ double block_sum64(double v, double *buf) {
   v = wave_sum64(v);
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
   __syncthreads();
   v = 0.0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) v += buf[w];
+  for (int w = 0; w < kWaves; ++w) v += buf[w];
   return v;
+}
+
+// The factor of a norm, which is also rounded to what the caller is shown.  A
+// norm that is infinite, NaN, or not above max_norm leaves the gradients.
+__device__ __forceinline__ float factor_of(double norm, float max_norm, float &shown) {
+  shown = static_cast<float>(norm);
+  const double limit = static_cast<double>(max_norm);
+  const bool clip = shown < __builtin_huge_valf() && norm > limit;
+  return clip ? static_cast<float>(limit / norm) : 1.0f;
 }
 
 __device__ __forceinline__ double sum_of_squares(const double *sums, int n, double *buf) {
   double v = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) v += sums[i];
-  return block_sum64(v, buf);
+  return block_sum64<kThreads / 64>(v, buf);
 }
 
-// Tensor of a chunk.
-__device__ __forceinline__ int tensor_of(const GradTable &t, uint32_t chunk) {
+// Entry of a chunk; `last`: that of the chunk before, which often has this one too.
+__device__ __forceinline__ int entry_of(const GradTable &t, uint32_t chunk, int last) {
+  if (t.first[last] <= chunk && chunk < t.first[last + 1]) return last;
   int lo = 0, hi = t.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -88,8 +99,9 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradTable t, dou
                                                                int first) {
   __shared__ double Buf[kThreads / 64];
   double acc = 0.0;
+  int k = 0;
   for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    const int k = tensor_of(t, c);
+    k = entry_of(t, c, k);
     const int64_t from = static_cast<int64_t>(c - t.first[k]) * kGradChunk;
     const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
     const int n = static_cast<int>(size < kGradChunk ? size : kGradChunk);
@@ -98,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradTable t, dou
     else
       acc += chunk_squares(static_cast<const float *>(t.grad[k]) + from, n);
   }
-  acc = block_sum64(acc, Buf);
+  acc = block_sum64<kThreads / 64>(acc, Buf);
   if (threadIdx.x == 0) sums[blockIdx.x] = first ? acc : sums[blockIdx.x] + acc;
 }
 
@@ -137,17 +149,15 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable t, GradO
                                                              int write_norm) {
   __shared__ double Buf[kThreads / 64];
   const double total = sums ? sqrt(sum_of_squares(sums, nsums, Buf)) : static_cast<double>(*norm);
-  const float shown = static_cast<float>(total);
+  float shown;
+  const float c = factor_of(total, max_norm, shown);
   if (sums && write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = shown;
-  // a norm that is infinite, NaN, or not above max_norm leaves the gradients
-  const bool finite = shown < __builtin_huge_valf();
-  const double limit = static_cast<double>(max_norm);
-  const float c = finite && total > limit ? static_cast<float>(limit / total) : 1.0f;
   if (in_place && c == 1.0f) return;
   // from the end, which was read last and may still be in the last-level cache
+  int k = 0;
   for (uint32_t j = blockIdx.x; j < t.first[t.n]; j += gridDim.x) {
     const uint32_t i = t.first[t.n] - 1 - j;
-    const int k = tensor_of(t, i);
+    k = entry_of(t, i, k);
     const int64_t from = static_cast<int64_t>(i - t.first[k]) * kGradChunk;
     const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
     const int n = static_cast<int>(size < kGradChunk ? size : kGradChunk);
@@ -169,7 +179,66 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable t, GradO
   }
 }
 
+// All of it in one launch, for tensors of up to kGradSmall pieces of 8 elements
+// together: the table counts pieces, a thread holds up to kHeld of them in
+// registers between the sum and the clipping.
+constexpr int kSmallThreads = 1024, kHeld = kGradSmall / kSmallThreads;
+__global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(GradTable t, GradOuts o,
+                                                                  int clip, int in_place,
+                                                                  float max_norm, float *norm) {
+  __shared__ double Buf[kSmallThreads / 64];
+  float v[kHeld][8];
+  int entry[kHeld], q[kHeld];
+  double acc = 0.0;
+  const uint32_t all = t.first[t.n];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const uint32_t at = threadIdx.x + i * kSmallThreads;
+    if (at >= all) break;
+    const int k = entry_of(t, at, 0), size = t.size[k] & kGradSize;
+    entry[i] = k;
+    q[i] = at - t.first[k];
+    if (t.size[k] & kGradBf16)
+      get_piece<uint16_t, 8>(static_cast<const uint16_t *>(t.grad[k]), q[i], size, v[i]);
+    else
+      get_piece<float, 8>(static_cast<const float *>(t.grad[k]), q[i], size, v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    if (threadIdx.x + i * kSmallThreads >= all) break;
+    const int size = t.size[entry[i]] & kGradSize;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double x = in_piece<8>(q[i], e, size) ? static_cast<double>(v[i][e]) : 0.0;
+      acc = fma(x, x, acc);
+    }
+  }
+  float shown;
+  const float c = factor_of(sqrt(block_sum64<kSmallThreads / 64>(acc, Buf)), max_norm, shown);
+  if (threadIdx.x == 0) *norm = shown;
+  if (!clip || (in_place && c == 1.0f)) return;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    if (threadIdx.x + i * kSmallThreads >= all) break;
+    const int k = entry[i], size = t.size[k] & kGradSize;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] *= c;
+    if (t.size[k] & kGradOutBf16)
+      store_piece<uint16_t, 8>(static_cast<uint16_t *>(o.out[k]), q[i], size, v[i]);
+    else
+      store_piece<float, 8>(static_cast<float *>(o.out[k]), q[i], size, v[i]);
+  }
+}
+
 }  // namespace
+
+int launch_grad_small(const GradTable &t, const GradOuts &outs, bool clip, bool in_place,
+                      float max_norm, float *norm, void *stream) {
+  hipLaunchKernelGGL(grad_small_kernel, dim3(1), dim3(kSmallThreads), 0,
+                     static_cast<hipStream_t>(stream), t, outs, clip ? 1 : 0, in_place ? 1 : 0,
+                     max_norm, norm);
+  return static_cast<int>(hipGetLastError());
+}
 
 int launch_grad_squares(const GradTable &t, double *sums, int nsums, bool first, void *stream) {
   hipLaunchKernelGGL(grad_squares_kernel, dim3(nsums), dim3(kThreads), 0,

@@ -282,7 +282,7 @@ int check_grad_overlaps(const Grads &c, bool clip, const Span *more, int nmore) 
   return SSM_OK;
 }
 
-int64_t chunks_of(int64_t size) { return (size + ssm::kGradChunk - 1) / ssm::kGradChunk; }
+int64_t chunks_of(int64_t size, int64_t chunk) { return (size + chunk - 1) / chunk; }
 
 // The tensors of a call as entries of at most kGradPiece elements, in tables of
 // equal numbers of entries.
@@ -290,11 +290,17 @@ struct Tables {
   std::vector<ssm::GradTable> t;
   std::vector<ssm::GradOuts> o;
   int groups = 1;  // workgroups, and sums, of a launch
+  bool small;      // one table, of pieces
 
-  explicit Tables(const Grads &c) {
-    int64_t entries = 0;
-    for (int64_t i = 0; i < c.n; ++i)
-      entries += (c.sizes[i] + ssm::kGradPiece - 1) / ssm::kGradPiece;
+  // form_norm: the norm is formed, by one workgroup where it can
+  Tables(const Grads &c, bool form_norm) {
+    int64_t entries = 0, pieces = 0;
+    for (int64_t i = 0; i < c.n; ++i) {
+      entries += chunks_of(c.sizes[i], ssm::kGradPiece);
+      pieces += chunks_of(c.sizes[i], 8);
+    }
+    small = form_norm && entries <= ssm::kGradTensors && pieces <= ssm::kGradSmall;
+    const int64_t chunk = small ? 8 : ssm::kGradChunk;
     const int64_t tables = std::max<int64_t>(1, (entries + ssm::kGradTensors - 1) / ssm::kGradTensors);
     const int64_t each = (entries + tables - 1) / tables;
     t.resize(tables);
@@ -314,7 +320,7 @@ struct Tables {
         table.size[table.n] = static_cast<uint32_t>(size) |
                               (in == SSM_DTYPE_BF16 ? ssm::kGradBf16 : 0u) |
                               (out == SSM_DTYPE_BF16 ? ssm::kGradOutBf16 : 0u);
-        table.first[table.n + 1] = table.first[table.n] + static_cast<uint32_t>(chunks_of(size));
+        table.first[table.n + 1] = table.first[table.n] + static_cast<uint32_t>(chunks_of(size, chunk));
         ++table.n;
       }
     }
@@ -496,7 +502,9 @@ int ssm_grad_norm(const void *const *grads, const int64_t *sizes, const int *dty
   const Span more[] = {{norm, 4, "norm"}, {workspace, kGradWorkspace, "workspace"}};
   if ((st = check_grad_overlaps(c, false, more, 2)) != SSM_OK) return st;
   double *sums = static_cast<double *>(workspace);
-  const Tables t(c);
+  const Tables t(c, true);
+  if (t.small)
+    return done(ssm::launch_grad_small(t.t[0], t.o[0], false, false, 0.0f, norm, stream));
   const int err = form_squares(t, sums, stream);
   return done(err != 0 ? err : ssm::launch_grad_norm(sums, t.groups, norm, stream));
 } catch (const std::bad_alloc &) {
@@ -519,7 +527,9 @@ int ssm_grad_clip(const void *const *grads, const int64_t *sizes, const int *dty
                        {have_norm ? nullptr : workspace, kGradWorkspace, "workspace"}};
   if ((st = check_grad_overlaps(c, true, more, 2)) != SSM_OK) return st;
   double *sums = have_norm ? nullptr : static_cast<double *>(workspace);
-  const Tables t(c);
+  const Tables t(c, !have_norm);
+  if (t.small)
+    return done(ssm::launch_grad_small(t.t[0], t.o[0], true, outs == nullptr, max_norm, norm, stream));
   int err = have_norm ? 0 : form_squares(t, sums, stream);
   // the tables from the last one, too, for the last-level cache
   for (size_t i = t.t.size(); i-- > 0 && err == 0;)

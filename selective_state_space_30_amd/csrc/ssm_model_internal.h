@@ -64,13 +64,15 @@ int launch_layer_norm_bwd(const LayerNormArgs &a, LayerNormTypes types, void *st
 
 // -------------------------------------------------------- gradients' norm --
 constexpr int kGradTensors = 160;   // tensors a launch takes, in its arguments
-constexpr int kGradGroups = 1024;   // most partial sums
+constexpr int kGradGroups = 2048;   // most partial sums
 constexpr int kGradChunk = 16384;   // elements that a workgroup takes at a time
 constexpr int64_t kGradPiece = int64_t(1) << 29;  // elements of an entry; longer tensors have several
 
+constexpr int kGradSmall = 8192;    // most pieces of 8 elements that one workgroup takes alone
+
 struct GradTable {
   const void *grad[kGradTensors];
-  uint32_t first[kGradTensors + 1];  // chunks before each entry
+  uint32_t first[kGradTensors + 1];  // chunks (or pieces) before each entry
   // elements of each entry; its gradient's and its output's types
   uint32_t size[kGradTensors];
   int32_t n;
@@ -82,6 +84,9 @@ struct GradOuts {
   void *out[kGradTensors];
 };
 
+// Norm and (with clip) clipping of a table that counts pieces.
+int launch_grad_small(const GradTable &t, const GradOuts &outs, bool clip, bool in_place,
+                      float max_norm, float *norm, void *stream);
 // Adds the squares of a table's tensors to nsums (at most kGradGroups) sums,
 // or writes them where it is the first.
 int launch_grad_squares(const GradTable &t, double *sums, int nsums, bool first, void *stream);
