@@ -50,13 +50,14 @@ __device__ __forceinline__ double sum_of_squares(const double *sums, int n, doub
   return block_sum64<kThreads / 64>(v, buf);
 }
 
-// Entry of a chunk; `last`: that of the chunk before, which often has this one too.
-__device__ __forceinline__ int entry_of(const GradTable &t, uint32_t chunk, int last) {
-  if (t.first[last] <= chunk && chunk < t.first[last + 1]) return last;
-  int lo = 0, hi = t.n;
+// Entry of n that has a chunk; `last`: that of the chunk before, which often has
+// this one too.
+__device__ __forceinline__ int entry_of(const uint32_t *first, int n, uint32_t chunk, int last) {
+  if (first[last] <= chunk && chunk < first[last + 1]) return last;
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (t.first[mid] <= chunk)
+    if (first[mid] <= chunk)
       lo = mid;
     else
       hi = mid;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradTable t, dou
   double acc = 0.0;
   int k = 0;
   for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    k = entry_of(t, c, k);
+    k = entry_of(t.first, t.n, c, k);
     const int64_t from = static_cast<int64_t>(c - t.first[k]) * kGradChunk;
     const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
     const int n = static_cast<int>(size < kGradChunk ? size : kGradChunk);
@@ -157,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable t, GradO
   int k = 0;
   for (uint32_t j = blockIdx.x; j < t.first[t.n]; j += gridDim.x) {
     const uint32_t i = t.first[t.n] - 1 - j;
-    k = entry_of(t, i, k);
+    k = entry_of(t.first, t.n, i, k);
     const int64_t from = static_cast<int64_t>(i - t.first[k]) * kGradChunk;
     const int64_t size = static_cast<int64_t>(t.size[k] & kGradSize) - from;
     const int n = static_cast<int>(size < kGradChunk ? size : kGradChunk);
@@ -187,26 +188,36 @@ __global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(GradTable t, 
                                                                   int clip, int in_place,
                                                                   float max_norm, float *norm) {
   __shared__ double Buf[kSmallThreads / 64];
+  // the table, since each lane looks for its own entry
+  __shared__ uint32_t First[kGradTensors + 1], Size[kGradTensors];
+  __shared__ const void *Grad[kGradTensors];
+  for (int i = threadIdx.x; i <= t.n; i += kSmallThreads) {
+    First[i] = t.first[i];
+    if (i == t.n) break;
+    Size[i] = t.size[i];
+    Grad[i] = t.grad[i];
+  }
+  __syncthreads();
   float v[kHeld][8];
   int entry[kHeld], q[kHeld];
   double acc = 0.0;
-  const uint32_t all = t.first[t.n];
+  const uint32_t all = First[t.n];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const uint32_t at = threadIdx.x + i * kSmallThreads;
     if (at >= all) break;
-    const int k = entry_of(t, at, 0), size = t.size[k] & kGradSize;
+    const int k = entry_of(First, t.n, at, 0), size = Size[k] & kGradSize;
     entry[i] = k;
-    q[i] = at - t.first[k];
-    if (t.size[k] & kGradBf16)
-      get_piece<uint16_t, 8>(static_cast<const uint16_t *>(t.grad[k]), q[i], size, v[i]);
+    q[i] = at - First[k];
+    if (Size[k] & kGradBf16)
+      get_piece<uint16_t, 8>(static_cast<const uint16_t *>(Grad[k]), q[i], size, v[i]);
     else
-      get_piece<float, 8>(static_cast<const float *>(t.grad[k]), q[i], size, v[i]);
+      get_piece<float, 8>(static_cast<const float *>(Grad[k]), q[i], size, v[i]);
   }
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     if (threadIdx.x + i * kSmallThreads >= all) break;
-    const int size = t.size[entry[i]] & kGradSize;
+    const int size = Size[entry[i]] & kGradSize;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const double x = in_piece<8>(q[i], e, size) ? static_cast<double>(v[i][e]) : 0.0;
@@ -220,10 +231,10 @@ __global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(GradTable t, 
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     if (threadIdx.x + i * kSmallThreads >= all) break;
-    const int k = entry[i], size = t.size[k] & kGradSize;
+    const int k = entry[i], size = Size[k] & kGradSize;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] *= c;
-    if (t.size[k] & kGradOutBf16)
+    if (Size[k] & kGradOutBf16)
       store_piece<uint16_t, 8>(static_cast<uint16_t *>(o.out[k]), q[i], size, v[i]);
     else
       store_piece<float, 8>(static_cast<float *>(o.out[k]), q[i], size, v[i]);

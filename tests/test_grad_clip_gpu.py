@@ -45,7 +45,12 @@ SETS = {
     "chunk borders": [(16383, "f"), (16384, "b"), (16385, "f"), (32768, "b"), (32777, "f")],
     "with empty ones": [(0, "f"), (5, "b"), (0, "b"), (0, "f"), (33, "f"), (0, "b")],
     "matrices": [((300, 70), "b"), ((5, 6, 7), "f"), ((1000, 999), "f")],
-    "a table and one": [(3 + i % 40, "fb"[i % 2]) for i in range(129)],
+    # 160 tensors fit a launch's arguments, 65536 elements one workgroup
+    "a table": [(3 + i % 40, "fb"[i % 2]) for i in range(160)],
+    "a table and one": [(3 + i % 40, "fb"[i % 2]) for i in range(161)],
+    "two tables and one": [(30000 + i % 40, "fb"[i % 2]) for i in range(321)],
+    "one workgroup": [(65529, "f"), (7, "b")],
+    "over one workgroup": [(65529, "f"), (8, "f"), (1, "b")],
     "many": [(1 + (i * 37) % 500, "fb"[i % 3 == 0]) for i in range(700)],
     "many chunks": [(40_000_003, "b"), (5, "f"), (20_000_001, "f")],
 }
