@@ -41,7 +41,8 @@ typedef enum {
  *  ids      required (tokens), int32 or int64 (ssm_index), device
  *  weight   required (vocab, dim), weight_dtype, rows weight_stride apart
  *  out      required output (tokens, dim) dense, dtype; overlaps no input
- *  0 <= tokens < 2^28, 1 <= vocab < 2^30, 1 <= dim <= 65536 */
+ *  0 <= tokens < 2^28, 1 <= vocab < 2^30, 1 <= dim <= 65536, tokens * dim below
+ *  2^38 - 1024 */
 int ssm_embed_fwd(const void *ids, const void *weight, int64_t weight_stride, void *out,
                   int64_t tokens, int64_t vocab, int64_t dim, float scale, int index_type,
                   int weight_dtype, int dtype, void *stream);

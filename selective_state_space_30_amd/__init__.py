@@ -1421,15 +1421,15 @@ def _tensors(ts, name, dev):
     """Host arrays of the addresses, sizes and types of a list of tensors, and
     whether all are contiguous."""
     try:
-        codes = array.array("i", map(_CODES.__getitem__, map(_dtype_of, ts)))
-        ptrs = array.array("Q", map(_data_ptr, ts))
+        codes = array.array("i", list(map(_CODES.__getitem__, map(_dtype_of, ts))))
+        ptrs = array.array("Q", list(map(_data_ptr, ts)))
         dense = all(map(_is_contiguous, ts))
         fine = set(map(_get_device, ts)) <= {dev.index}
     except (AttributeError, KeyError, TypeError):
         fine = False
     if not (fine and dense):
         dense = _check_tensors(ts, name, dev)
-    return ptrs, array.array("q", map(_numel, ts)), codes, dense
+    return ptrs, array.array("q", list(map(_numel, ts))), codes, dense
 
 
 def _check_tensors(ts, name, dev):

@@ -151,9 +151,30 @@ __device__ __forceinline__ void clear_rows(const EmbedArgs &p, int64_t row0, int
   }
 }
 
-// The short sort, by workgroup 0, and beside it, by the others, zeros in the
-// rows of ids that do not come: each finds those of its rows among the ids.
-constexpr int kClearRows = 8192;  // rows a workgroup looks for at a time
+// Zeros in the rows of ids that do not come, of the rows_per rows of one
+// workgroup (of kSortThreads), which looks for them among all ids.
+constexpr int kClearRows = 8192;  // rows it looks for at a time
+template <typename W>
+__device__ __forceinline__ void clear_group(const EmbedArgs &p, int64_t group, int64_t rows_per,
+                                            uint32_t *there) {
+  const int64_t begin = group * rows_per;
+  const int64_t stop = begin + rows_per < p.vocab ? begin + rows_per : p.vocab;
+  for (int64_t row0 = begin; row0 < stop; row0 += kClearRows) {
+    const int64_t row1 = row0 + kClearRows < stop ? row0 + kClearRows : stop;
+    for (int i = threadIdx.x; i < kClearRows / 32; i += kSortThreads) there[i] = 0u;
+    __syncthreads();
+    for (int t = threadIdx.x; t < p.tokens; t += kSortThreads) {
+      const int64_t key = key_of(p, t);
+      if (key >= row0 && key < row1)
+        atomicOr(&there[(key - row0) / 32], 1u << ((key - row0) % 32));
+    }
+    __syncthreads();
+    clear_rows<W>(p, row0, row1, there);
+    __syncthreads();
+  }
+}
+
+// The short sort, by workgroup 0; the others clear rows beside it.
 template <typename W>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedArgs p, uint32_t *keys_out,
                                                                  uint32_t *pos_out, int passes,
@@ -166,21 +187,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedArgs p, u
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int n = static_cast<int>(p.tokens);
   if (blockIdx.x > 0) {
-    const int64_t begin = (blockIdx.x - 1) * rows_per;
-    const int64_t stop = begin + rows_per < p.vocab ? begin + rows_per : p.vocab;
-    for (int64_t row0 = begin; row0 < stop; row0 += kClearRows) {
-      const int64_t row1 = row0 + kClearRows < stop ? row0 + kClearRows : stop;
-      for (int i = tid; i < kClearRows / 32; i += kSortThreads) Key[i] = 0u;
-      __syncthreads();
-      for (int t = tid; t < n; t += kSortThreads) {
-        const int64_t key = key_of(p, t);
-        if (key >= row0 && key < row1)
-          atomicOr(&Key[(key - row0) / 32], 1u << ((key - row0) % 32));
-      }
-      __syncthreads();
-      clear_rows<W>(p, row0, row1, Key);
-      __syncthreads();
-    }
+    clear_group<W>(p, blockIdx.x - 1, rows_per, Key);
     return;
   }
   // a wave holds neighbours, 64 at a time
@@ -370,6 +377,31 @@ struct Runs {
   int len;                     // sorted tokens a run has, at most 64
 };
 
+// Zeros in the rows of ids that do not come, from the sorted list: a workgroup
+// (of kThreads) takes 32 rows a wave; lane l finds where id l of them begins.
+constexpr int kSearchRows = 32 * kWavesPer;
+template <typename W>
+__device__ __forceinline__ void clear_sorted(const EmbedArgs &p, const uint32_t *keys, int64_t group,
+                                             uint32_t *there) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row0 = group * kSearchRows;
+  const int64_t want = row0 + wave * 32 + (lane < 32 ? lane : 32);
+  int64_t lo = 0, hi = p.tokens;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (keys[mid] < want)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  const int64_t next = __shfl_down(lo, 1);
+  const uint64_t come = __ballot(lane < 32 && next > lo);
+  if (lane == 0) there[wave] = static_cast<uint32_t>(come);
+  __syncthreads();
+  const int64_t row1 = row0 + kSearchRows < p.vocab ? row0 + kSearchRows : p.vocab;
+  clear_rows<W>(p, row0, row1, there);
+}
+
 template <typename W>
 __device__ __forceinline__ W *row_of(const EmbedArgs &p, uint32_t key) {
   return static_cast<W *>(p.dweight) + static_cast<int64_t>(key) * p.dim;
@@ -393,15 +425,23 @@ __device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q,
 }
 
 // A wave takes one run and 64 pieces of the columns.  kAdd: the rows to add to
-// are asked for together with those of dy.
+// are asked for together with those of dy.  The first `clears` workgroups, which
+// wait for their searches, clear rows.
 template <typename T, typename W, int kN, bool kAdd>
-__global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r) {
+__global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedArgs p, Runs r, uint32_t clears) {
+  if constexpr (!kAdd) {
+    __shared__ uint32_t There[kWavesPer];
+    if (blockIdx.x < clears) {
+      clear_sorted<W>(p, r.keys, blockIdx.x, There);
+      return;
+    }
+  }
   constexpr int kAhead = 8;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pieces = (p.dim + kN - 1) / kN;
   const int cols = (pieces + 63) / 64;
-  const uint32_t at = blockIdx.x * kWavesPer + wave;
+  const uint32_t at = (blockIdx.x - clears) * kWavesPer + wave;
   const int64_t run = at / cols;
   if (run >= r.runs) return;
   const int q = static_cast<int>(at % cols) * 64 + lane;
@@ -530,33 +570,102 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs p
   }
 }
 
-// Zeros in the rows of ids that do not come, behind the long sort.  A wave
-// looks for 32 rows; lane l finds where id l of them begins in the sorted list.
-template <typename W>
-__global__ __launch_bounds__(kThreads) void embed_clear_kernel(EmbedArgs p, const uint32_t *keys) {
-  __shared__ uint32_t There[kWavesPer];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (32 * kWavesPer);
-  const int64_t want = row0 + wave * 32 + (lane < 32 ? lane : 32);
-  int64_t lo = 0, hi = p.tokens;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (keys[mid] < want)
-      lo = mid + 1;
-    else
-      hi = mid;
+// ------------------------------------------------------------- few tokens --
+// Up to kFew tokens in one launch, without a sort: a wave takes a token and 64
+// pieces of the columns, finds the tokens of the same id among all ids, and sums
+// their rows if its own is the first of them.  Workgroups behind the first
+// `sums` clear rows.
+constexpr int kFew = 256;
+template <typename T, typename W, int kN>
+__global__ __launch_bounds__(kSortThreads) void embed_few_kernel(EmbedArgs p, uint32_t sums,
+                                                                int64_t rows_per) {
+  __shared__ uint32_t There[kClearRows / 32];
+  if (blockIdx.x >= sums) {
+    clear_group<W>(p, blockIdx.x - sums, rows_per, There);
+    return;
   }
-  const int64_t next = __shfl_down(lo, 1);
-  const uint64_t there = __ballot(lane < 32 && next > lo);
-  if (lane == 0) There[wave] = static_cast<uint32_t>(there);
-  __syncthreads();
-  const int64_t row1 = row0 + 32 * kWavesPer < p.vocab ? row0 + 32 * kWavesPer : p.vocab;
-  clear_rows<W>(p, row0, row1, There);
+  constexpr int kAhead = 8, kWords = kFew / 64;
+  const int lane = threadIdx.x & 63, n = static_cast<int>(p.tokens);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pieces = (p.dim + kN - 1) / kN, cols = (pieces + 63) / 64;
+  const uint32_t task = blockIdx.x * kSortWaves + wave;
+  const int own = task / cols;
+  if (own >= n) return;
+  const int q = static_cast<int>(task % cols) * 64 + lane, safe = q < pieces ? q : pieces - 1;
+  uint32_t keys[kWords];
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) keys[w] = key_of(p, w * 64 + lane < n ? w * 64 + lane : 0);
+  const uint32_t key = __builtin_amdgcn_readfirstlane(key_of(p, own));
+  if (key >= p.vocab) return;
+  uint64_t same[kWords];
+  int count = 0;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    same[w] = __ballot(w * 64 + lane < n && keys[w] == key);
+    count += __popcll(same[w]);
+  }
+  // the first of them
+  bool earlier = false;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const int bits = own - w * 64;
+    if (bits > 0) earlier |= (bits >= 64 ? same[w] : same[w] & ((uint64_t(1) << bits) - 1)) != 0;
+  }
+  if (earlier) return;
+  Piece<W, kN> old;
+  old.zero();
+  if (p.accumulate) load_piece(old, row_of<W>(p, key), safe, p.dim);
+  float acc[kN];
+#pragma unroll
+  for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
+  int t = 0;
+  auto next = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+      if (same[w]) {
+        t = w * 64 + __ffsll(static_cast<unsigned long long>(same[w])) - 1;
+        same[w] &= same[w] - 1;
+        return;
+      }
+  };
+  for (int j = 0; j < count; j += kAhead) {
+    Piece<T, kN> dy[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      next();  // the last one again behind it
+      load_piece(dy[k], static_cast<const T *>(p.dy) + t * p.dy_stride, safe, p.dim);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int e = 0; e < kN; ++e) acc[e] += j + k < count ? dy[k][e] : 0.0f;
+  }
+  if (q < pieces) put_sum<W, kN>(p, key, q, acc, old);
 }
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-constexpr int kRunLen = 32;
+// Columns of a lane in the sums.
+constexpr int kSumPiece = 4;
+
+// Sorted tokens a run has: short ones where there are few waves, each of which
+// waits for its rows in turn, long ones where partial rows would be many.
+// (Added to a gradient, runs of 8, 16 and 32: 8192 tokens of 768 columns 35, 36
+// and 41 us, 16384 of 768 42, 39 and 43 us, 16384 of 2560 92, 84 and 80 us.)
+int run_len(int64_t tokens, int64_t cols) {
+  return tokens * cols < 32768 ? 8 : tokens * cols < 65536 ? 16 : 32;
+}
+
+// One workgroup sorts 4096, 8192 and 16384 tokens in 14, 22 and 41 us, the
+// launches of the long sort take 24 us; but beside the short one rows are
+// cleared.  (8192 tokens of 768 columns, short and long: added 40 and 35 us, as
+// a new gradient of 32000 rows 43 and 51 us; 16384 of 2560, a new one of 50000
+// rows, 512 MB, 147 and 160 us, of 768 and 32000 rows, 98 MB, 68 and 57 us.)
+bool sort_is_short(const EmbedArgs &a, int64_t row_bytes) {
+  if (a.tokens <= 4096) return true;
+  if (a.accumulate || a.tokens > kShort) return false;
+  return a.tokens <= 8192 || a.vocab * row_bytes >= int64_t(256) << 20;
+}
 
 // Workspace: two lists of keys and positions, the counts, the partial rows.
 struct Layout {
@@ -568,10 +677,10 @@ Layout layout_of(int64_t tokens, int64_t dim) {
   Layout l;
   l.per = tokens <= kOwnTiles / 2 * kSortThreads ? 1 : 4;
   l.tiles = (tokens + l.per * kSortThreads - 1) / (l.per * kSortThreads);
-  l.len = kRunLen;
+  l.len = run_len(tokens, (dim + 64 * kSumPiece - 1) / (64 * kSumPiece));
   l.runs = (tokens + l.len - 1) / l.len;
   l.row = up(dim, 4);
-  const int lists = tokens > kShort ? 2 : 1;
+  const int lists = 2;
   int64_t at = 0;
   for (int i = 0; i < lists; ++i) {
     l.keys[i] = at;
@@ -580,7 +689,7 @@ Layout layout_of(int64_t tokens, int64_t dim) {
     at += up(tokens * 4, 256);
   }
   l.counts = at;
-  if (lists > 1) at += up(l.tiles * kBins * 4, 256);
+  at += up(l.tiles * kBins * 4, 256);
   l.parts = at;
   at += l.runs > 1 ? l.runs * 2 * l.row * 4 : 0;
   l.bytes = at;
@@ -595,12 +704,19 @@ void digits_of(int64_t vocab, int &passes, int &bits) {
   bits = (all + passes - 1) / passes;
 }
 
-template <typename T, typename W, int kN>
+template <typename T, typename W>
 int launch_bwd(const EmbedArgs &a, hipStream_t s) {
-  const unsigned clears = static_cast<unsigned>((a.vocab + 32 * kWavesPer - 1) / (32 * kWavesPer));
-  if (a.tokens == 0) {
-    if (a.accumulate) return 0;
-    hipLaunchKernelGGL(embed_clear_kernel<W>, dim3(clears), dim3(kThreads), 0, s, a, nullptr);
+  constexpr int kN = kSumPiece;
+  const unsigned cols = static_cast<unsigned>(((a.dim + kN - 1) / kN + 63) / 64);
+  // workgroups that clear rows, and the rows of each, beside few tokens or the
+  // short sort
+  const unsigned clears = a.accumulate ? 0u : static_cast<unsigned>(a.vocab < 255 ? a.vocab : 255);
+  const int64_t rows_per = a.accumulate ? 1 : (a.vocab + clears - 1) / clears;
+  if (a.tokens <= kFew) {
+    const unsigned sums = static_cast<unsigned>((a.tokens * cols + kSortWaves - 1) / kSortWaves);
+    if (sums + clears == 0) return 0;
+    hipLaunchKernelGGL((embed_few_kernel<T, W, kN>), dim3(sums + clears), dim3(kSortThreads), 0, s,
+                       a, sums, rows_per);
     return static_cast<int>(hipGetLastError());
   }
   const Layout l = layout_of(a.tokens, a.dim);
@@ -608,15 +724,10 @@ int launch_bwd(const EmbedArgs &a, hipStream_t s) {
   auto words = [&](int64_t at) { return reinterpret_cast<uint32_t *>(ws + at); };
   int passes, bits, to = 0;
   digits_of(a.vocab, passes, bits);
-  if (a.tokens <= kShort) {
-    int64_t groups = 0, rows_per = 1;
-    if (!a.accumulate) {
-      groups = a.vocab < 255 ? a.vocab : 255;
-      rows_per = (a.vocab + groups - 1) / groups;
-    }
-    hipLaunchKernelGGL(embed_sort_kernel<W>, dim3(static_cast<unsigned>(1 + groups)),
-                       dim3(kSortThreads), 0, s, a, words(l.keys[0]), words(l.pos[0]), passes, bits,
-                       rows_per);
+  const bool brief = sort_is_short(a, a.dim * static_cast<int64_t>(sizeof(W)));
+  if (brief) {
+    hipLaunchKernelGGL(embed_sort_kernel<W>, dim3(1 + clears), dim3(kSortThreads), 0, s, a,
+                       words(l.keys[0]), words(l.pos[0]), passes, bits, rows_per);
   } else {
     SortPass sort{nullptr, nullptr, nullptr, nullptr, words(l.counts), l.tiles, 0, bits};
     const unsigned grid = static_cast<unsigned>(l.tiles < 65536 ? l.tiles : 65536);
@@ -646,18 +757,21 @@ int launch_bwd(const EmbedArgs &a, hipStream_t s) {
   }
   const Runs r{words(l.keys[to]), words(l.pos[to]), reinterpret_cast<float *>(ws + l.parts), l.runs,
                l.row, l.len};
-  const unsigned cols = static_cast<unsigned>(((a.dim + kN - 1) / kN + 63) / 64);
-  const dim3 waves(static_cast<unsigned>((l.runs * cols + kWavesPer - 1) / kWavesPer));
+  const unsigned sums = static_cast<unsigned>((l.runs * cols + kWavesPer - 1) / kWavesPer);
+  const unsigned searches =
+      a.accumulate || brief ? 0u
+                            : static_cast<unsigned>((a.vocab + kSearchRows - 1) / kSearchRows);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(searches + sums), dim3(kThreads), 0, s, a, r, searches);
+  };
   if (a.accumulate)
-    hipLaunchKernelGGL((embed_sum_kernel<T, W, kN, true>), waves, dim3(kThreads), 0, s, a, r);
+    go(embed_sum_kernel<T, W, kN, true>);
   else
-    hipLaunchKernelGGL((embed_sum_kernel<T, W, kN, false>), waves, dim3(kThreads), 0, s, a, r);
+    go(embed_sum_kernel<T, W, kN, false>);
   if (l.runs > 1)
     hipLaunchKernelGGL((embed_join_kernel<W, kN>),
                        dim3(static_cast<unsigned>((l.runs + kJoinWaves - 1) / kJoinWaves), cols),
                        dim3(64 * kJoinWaves), 0, s, a, r);
-  if (!a.accumulate && a.tokens > kShort)
-    hipLaunchKernelGGL(embed_clear_kernel<W>, dim3(clears), dim3(kThreads), 0, s, a, r.keys);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -677,7 +791,7 @@ int launch_fwd(const EmbedArgs &a, hipStream_t s) {
 }  // namespace
 
 int64_t embed_bwd_workspace(int64_t tokens, int64_t, int64_t dim) {
-  return tokens == 0 ? 0 : layout_of(tokens, dim).bytes;
+  return tokens <= kFew ? 0 : layout_of(tokens, dim).bytes;
 }
 
 int launch_embed_fwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream) {
@@ -690,8 +804,8 @@ int launch_embed_fwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream) {
 int launch_embed_bwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (bf16)
-    return w_bf16 ? launch_bwd<uint16_t, uint16_t, 4>(a, s) : launch_bwd<uint16_t, float, 4>(a, s);
-  return w_bf16 ? launch_bwd<float, uint16_t, 4>(a, s) : launch_bwd<float, float, 4>(a, s);
+    return w_bf16 ? launch_bwd<uint16_t, uint16_t>(a, s) : launch_bwd<uint16_t, float>(a, s);
+  return w_bf16 ? launch_bwd<float, uint16_t>(a, s) : launch_bwd<float, float>(a, s);
 }
 
 }  // namespace ssm

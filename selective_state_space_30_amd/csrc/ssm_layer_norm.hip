@@ -378,12 +378,17 @@ Shape shape_of(int dim, LayerNormTypes types, bool backward) {
   return shape_of(dim, 8, 4, backward && types != kLnBf16 ? 2 : 3);
 }
 
-// Workgroups of a pass over the rows: at most `most` for each CU and 256 threads.
+// Workgroups that take the rows, at most `most`.
 int groups_of(int64_t rows, const Shape &sh, int most) {
   const int per = sh.threads / sh.lanes;
   const int64_t groups = (rows + per - 1) / per;
-  most = most * kCus * 256 / (sh.threads < 256 ? sh.threads : 256);
   return static_cast<int>(groups < most ? groups : most);
+}
+
+// Of the forward pass: what 4 waves a SIMD make (twice as many workgroups of 512
+// threads: 4096 x 8192 in bf16 53 instead of 51 us).
+int forward_groups(int64_t rows, const Shape &sh) {
+  return groups_of(rows, sh, kCus * 1024 / sh.threads);
 }
 
 // Workgroups a CU of the backward pass: one that asks for its rows ahead keeps
@@ -395,7 +400,8 @@ int groups_of(int64_t rows, const Shape &sh, int most) {
 int back_groups(int64_t rows, const Shape &sh, LayerNormTypes types) {
   const int held = sh.per * (types == kLnF32 ? 4 : 8);
   const bool fit = held <= (types == kLnBf16 ? 24 : 16) && sh.threads <= 256;
-  return groups_of(rows, sh, fit && (!sh.whole || sh.lanes > 64) ? 2 : 1);
+  const int each = fit && (!sh.whole || sh.lanes > 64) ? 2 : 1;
+  return groups_of(rows, sh, each * kCus * 256 / (sh.threads < 256 ? sh.threads : 256));
 }
 
 template <typename T, typename R, typename Y, int kN, int kP, bool kWhole, bool kBack>
@@ -413,7 +419,7 @@ int launch_p(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
       go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 512>);
   } else {
     hipLaunchKernelGGL((layer_norm_fwd_kernel<T, R, Y, kN, kP, kWhole>),
-                       dim3(groups_of(a.rows, sh, 4)),
+                       dim3(forward_groups(a.rows, sh)),
                        dim3(sh.threads), 0, s, a, sh.lanes);
   }
   return static_cast<int>(hipGetLastError());

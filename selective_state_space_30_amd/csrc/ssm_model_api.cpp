@@ -103,6 +103,9 @@ int check_embed_sizes(int64_t tokens, int64_t vocab, int64_t dim) {
     return fail(SSM_ERR_UNSUPPORTED, "tokens=%lld vocab=%lld dim=%lld: this build supports %lld, "
                 "%lld and %d", (long long)tokens, (long long)vocab, (long long)dim,
                 (long long)kMaxTokens, (long long)kMaxVocab, ssm::kEmbedMaxDim);
+  if (tokens * dim > kMaxTokens * 1024)
+    return fail(SSM_ERR_UNSUPPORTED, "tokens=%lld dim=%lld: this build supports %lld elements",
+                (long long)tokens, (long long)dim, (long long)(kMaxTokens * 1024));
   return SSM_OK;
 }
 

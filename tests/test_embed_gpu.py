@@ -67,7 +67,11 @@ CASES = [
     (64, 3, 8, "skewed", BF16, BF16),
     (65, 300, 513, "padded", BF16, BF16),      # a piece over 64 pieces
     (100, 300, 257, "padded", F32, F32),
-    (257, 50, 7, "skewed", F32, BF16),         # rows shorter than a piece
+    (255, 50, 7, "skewed", F32, BF16),         # rows shorter than a piece
+    (256, 3, 300, "skewed", BF16, F32),        # the most tokens that are not sorted
+    (256, 9, 90, "one", F32, BF16),
+    (257, 50, 7, "skewed", F32, BF16),
+    (257, 3, 300, "padded", F32, F32),
     (1000, 255, 129, "skewed", BF16, BF16),
     (1000, 256, 130, "even", BF16, BF16),      # the last id over one pass's 8 bits
     (4095, 257, 40, "even", F32, BF16),
@@ -75,10 +79,16 @@ CASES = [
     (4097, 5000, 24, "padded", F32, F32),
     (5000, 65536, 16, "even", F32, BF16),      # three passes
     (9000, 70000, 12, "skewed", F32, BF16),
+    (8192, 300, 1030, "skewed", BF16, BF16),   # the short sort beside the clearing
+    (8193, 300, 1030, "even", F32, F32),
+    (4100, 40, 4000, "skewed", F32, BF16),     # runs of 16 and of 32
+    (6000, 40, 4000, "one", F32, BF16),
     (16384, 600, 20, "skewed", F32, BF16),
     (16385, 600, 20, "skewed", F32, BF16),
     (40000, 20, 16, "one", F32, BF16),         # a thousand runs of one id
     (70000, 3000, 24, "skewed", BF16, BF16),
+    (262145, 3000, 9, "skewed", F32, BF16),    # 4 keys a thread of the long sort
+    (1048577, 70000, 8, "padded", F32, BF16),  # places in a launch of their own
     (300, 40, 96, "none", BF16, BF16),         # padding alone
     (20, 5, 9001, "even", BF16, BF16),
 ]
@@ -176,6 +186,18 @@ def test_deterministic_whatever_the_workspace_holds(n):
     for fill in (0, 255):
         ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV)
         assert torch.equal(ssm.ssm_embed_bwd(ids, dy, 400, workspace=ws), a)
+
+
+def test_short_sort_beside_a_large_weight():
+    """16384 tokens and a weight of 256 MB, as one workgroup sorts them."""
+    ids = make(16384, 66000, "skewed", seed=8)
+    dy = torch.randn(16384, 1024, generator=torch.Generator().manual_seed(8))
+    got = ssm.ssm_embed_bwd(ids.to(DEV), dy.to(DEV), 66000)
+    rows = torch.unique(ids)
+    want = ref.embed_gradient(torch.searchsorted(rows, ids), dy, rows.numel(), 1.0)
+    check_gradient(got[rows.to(DEV)], want)
+    got[rows.to(DEV)] = 0
+    assert not got.any()
 
 
 @pytest.mark.slow

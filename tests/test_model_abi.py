@@ -27,7 +27,7 @@ def at(i, off=0):
 
 EFWD = dict(ids=at(1), w=at(2), ws=256, out=at(3), tokens=100, vocab=50, dim=256, scale=1.0,
             index=1, wdtype=F32, dtype=BF16, stream=None)
-EBWD = dict(ids=at(1), dy=at(2), dys=256, dw=at(3), tokens=100, vocab=50, dim=256, scale=1.0,
+EBWD = dict(ids=at(1), dy=at(2), dys=256, dw=at(3), tokens=1000, vocab=50, dim=256, scale=1.0,
             flags=0, index=1, dtype=BF16, wdtype=F32, ws=at(4), wsb=1 << 24, stream=None)
 NFWD = dict(x=at(1), xs=256, res=at(2), rs=256, w=at(3), b=at(4), r=at(5), y=at(6), rows=8,
             dim=256, eps=1e-5, xdtype=BF16, rdtype=F32, dtype=BF16, stream=None)
@@ -38,7 +38,7 @@ NBWD = dict(x=at(1), xs=256, res=at(2), rs=256, w=at(3), dr=at(5), dy=at(6), dx=
 EMBED = [
     (dict(ids=None), INVALID), (dict(ids=at(1, 4)), INVALID), (dict(tokens=-1), INVALID),
     (dict(vocab=0), INVALID), (dict(dim=0), INVALID), (dict(tokens=1 << 28), UNSUPPORTED),
-    (dict(vocab=1 << 30), UNSUPPORTED), (dict(index=2), INVALID), (dict(index=-1), INVALID),
+    (dict(vocab=1 << 30), UNSUPPORTED), (dict(tokens=(1 << 28) - 1, dim=1025), UNSUPPORTED), (dict(index=2), INVALID), (dict(index=-1), INVALID),
     (dict(dtype=2), INVALID), (dict(wdtype=7), INVALID), (dict(scale=NAN), INVALID),
     (dict(scale=INF), INVALID), (dict(ids=at(1, 2), index=0), INVALID),
 ]
@@ -165,6 +165,8 @@ def test_sizes(lib):
     assert lib.ssm_layer_norm_bwd_workspace_size(8, 16385, ctypes.byref(size)) == UNSUPPORTED
     assert lib.ssm_grad_workspace_size(None) == INVALID
     assert ssm.ssm_embed_bwd_workspace_size(0, 10, 64) == 0
+    assert ssm.ssm_embed_bwd_workspace_size(256, 10, 64) == 0  # no sort
+    assert ssm.ssm_embed_bwd_workspace_size(257, 10, 64) > 0
     assert ssm.ssm_layer_norm_bwd_workspace_size(0, 64) == 0
     assert ssm.ssm_grad_workspace_size() % 256 == 0
     # the partial sums stay a fraction of what is summed
