@@ -22,11 +22,13 @@ using namespace dev;
 constexpr int kThreads = 256;
 constexpr int kWavesPer = kThreads / 64;
 
-// The id of a token as a sort key: vocab for ids outside.
+// The id of a token as a sort key: vocab for ids outside.  Both words of a wide
+// id are read as words, the only one of a narrow id twice: without a branch, at
+// whose end the compiler would wait for each load.
 __device__ __forceinline__ uint32_t key_of(const EmbedArgs &p, int64_t t) {
-  const int64_t id = p.wide_ids ? static_cast<const int64_t *>(p.ids)[t]
-                                : static_cast<const int32_t *>(p.ids)[t];
-  return id >= 0 && id < p.vocab ? static_cast<uint32_t>(id) : static_cast<uint32_t>(p.vocab);
+  const uint32_t *word = static_cast<const uint32_t *>(p.ids) + (t << p.wide_ids);
+  const uint32_t low = word[0], high = word[p.wide_ids] & (0u - p.wide_ids);
+  return high == 0u && low < static_cast<uint32_t>(p.vocab) ? low : static_cast<uint32_t>(p.vocab);
 }
 
 // ---------------------------------------------------------------- forward --
@@ -415,15 +417,6 @@ __device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q,
   for (int e = 0; e < kN; ++e) v[e] = fmaf(sum[e], p.scale, old[e]);
   store_piece<W, kN>(row_of<W>(p, key), q, p.dim, v);
 }
-template <typename W, int kN>
-__device__ __forceinline__ void put_sum(const EmbedArgs &p, uint32_t key, int q,
-                                        const float (&sum)[kN]) {
-  Piece<W, kN> old;
-  old.zero();
-  if (p.accumulate) load_piece(old, row_of<W>(p, key), q, p.dim);
-  put_sum<W, kN>(p, key, q, sum, old);
-}
-
 // A wave takes one run and 64 pieces of the columns.  kAdd: the rows to add to
 // are asked for together with those of dy.  The first `clears` workgroups, which
 // wait for their searches, clear rows.
@@ -511,6 +504,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs p
   float acc[kN];
   // the first partial row of the id that begins in a run, and every `step`-th
   // behind it
+  Piece<W, kN> old;
   auto sum = [&](int64_t of, int64_t first, int64_t n, int64_t step) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
@@ -530,6 +524,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs p
         for (int e = 0; e < kN; ++e) acc[e] += c + k * step < n ? v[k][e] : 0.0f;
     }
   };
+  // asks for the row that a sum is added to
+  auto add_to = [&](uint32_t key) __attribute__((always_inline)) {
+    old.zero();
+    if (p.accumulate) load_piece(old, row_of<W>(p, key), q < pieces ? q : pieces - 1, p.dim);
+  };
   const int64_t from = run * r.len, last = from + r.len - 1;
   int64_t behind = 0;
   if (last < p.tokens - 1) {
@@ -545,8 +544,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs p
         if (more < 64) break;
       }
       if (behind <= kAlone) {
+        add_to(key);
         sum(run, 0, behind, 1);
-        if (q < pieces) put_sum<W, kN>(p, key, q, acc);
+        if (q < pieces) put_sum<W, kN>(p, key, q, acc, old);
         behind = 0;
       }
     }
@@ -556,6 +556,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs p
   for (int w = 0; w < kJoinWaves; ++w) {
     const int64_t n = Behind[w];
     if (n == 0) continue;
+    const uint32_t key = r.keys[(run0 + w + 1) * r.len - 1];
+    if (wave == 0) add_to(key);
     sum(run0 + w, wave, n, kJoinWaves);
 #pragma unroll
     for (int e = 0; e < kN; ++e) Sums[wave][e][lane] = acc[e];
@@ -564,7 +566,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs p
       for (int k = 1; k < kJoinWaves; ++k)
 #pragma unroll
         for (int e = 0; e < kN; ++e) acc[e] += Sums[k][e][lane];
-      put_sum<W, kN>(p, r.keys[(run0 + w + 1) * r.len - 1], q, acc);
+      put_sum<W, kN>(p, key, q, acc, old);
     }
     __syncthreads();
   }
@@ -619,20 +621,23 @@ __global__ __launch_bounds__(kSortThreads) void embed_few_kernel(EmbedArgs p, ui
 #pragma unroll
   for (int e = 0; e < kN; ++e) acc[e] = 0.0f;
   int t = 0;
+  // the next of them, or the last one again (no indexing by a variable, which
+  // would put the masks into memory)
   auto next = [&]() __attribute__((always_inline)) {
+    bool found = false;
 #pragma unroll
-    for (int w = 0; w < kWords; ++w)
-      if (same[w]) {
-        t = w * 64 + __ffsll(static_cast<unsigned long long>(same[w])) - 1;
-        same[w] &= same[w] - 1;
-        return;
-      }
+    for (int w = 0; w < kWords; ++w) {
+      const bool here = !found && same[w] != 0;
+      t = here ? w * 64 + __ffsll(static_cast<unsigned long long>(same[w])) - 1 : t;
+      same[w] &= here ? same[w] - 1 : ~uint64_t(0);
+      found |= here;
+    }
   };
   for (int j = 0; j < count; j += kAhead) {
     Piece<T, kN> dy[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      next();  // the last one again behind it
+      next();
       load_piece(dy[k], static_cast<const T *>(p.dy) + t * p.dy_stride, safe, p.dim);
     }
 #pragma unroll
