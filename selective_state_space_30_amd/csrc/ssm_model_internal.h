@@ -64,7 +64,7 @@ int launch_layer_norm_bwd(const LayerNormArgs &a, LayerNormTypes types, void *st
 
 // -------------------------------------------------------- gradients' norm --
 constexpr int kGradTensors = 160;   // tensors a launch takes, in its arguments
-constexpr int kGradGroups = 2048;   // most partial sums
+constexpr int kGradGroups = 2048;   // most workgroups that sum squares, and their sums
 constexpr int kGradChunk = 16384;   // elements that a workgroup takes at a time
 constexpr int64_t kGradPiece = int64_t(1) << 29;  // elements of an entry; longer tensors have several
 
