@@ -102,8 +102,8 @@ __device__ __forceinline__ double chunk_squares(const T *g, int n) {
   return acc[0] + acc[1];
 }
 
-// Bound by memory: 267 gradients of 24 layers, 771 MB in fp32, 150 us in two
-// launches (5.1 TB/s; one tensor of 800 MB 5.6).  A square in 64 bits costs two
+// Bound by memory: 267 gradients of 24 layers, 771 MB in fp32, 160 us in two
+// launches (4.8 TB/s; one tensor of 800 MB 5.6).  A square in 64 bits costs two
 // instructions an element, a tenth of the time.
 __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradTable t, double *sums,
                                                                int first) {
@@ -153,7 +153,7 @@ __device__ __forceinline__ void scale_chunk(const T *g, W *out, int n, float c) 
   }
 }
 
-// Bound by memory.  The gradients above into other tensors: 290 us (1542 MB, 5.3
+// Bound by memory.  The gradients above into other tensors: 276 us (1542 MB, 5.6
 // TB/s), the whole call 443 us.  Taken from the end, so that what the squares'
 // launch read last comes from the last-level cache: 476 -> 461 us, 1.6 GB in
 // bf16 905 -> 884.
