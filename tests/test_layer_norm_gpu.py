@@ -104,6 +104,24 @@ def test_rows_of_one_value_and_far_means():
             assert scaled_max_err(g[i], w[i]) <= 2e-5 + far, "row %d" % i
 
 
+@pytest.mark.parametrize("dim", [7, 320, 1000, 1537, 5000, 16384])
+def test_rows_of_one_value_are_their_bias(dim):
+    """Whatever the value.  A sum takes at most 32 additions in a lane, 9 over
+    lanes and waves and a division, each off by 2^-24: the mean is off by
+    42 * 2^-24 of the value, what is left of that after its own mean by 42 * 2^-24
+    of it, over at least sqrt(eps) and at least 2^-10 of what was taken away."""
+    values = torch.tensor([0.1, 1.0 / 3, -777.7, 3e4, 1e-30, 123456.7, 1e20, -3e25])
+    x = values.unsqueeze(1).expand(len(values), dim).contiguous()
+    w, b = torch.full((dim,), 1.5), torch.linspace(-1, 1, dim)
+    _, y = ssm.ssm_layer_norm_fwd(x.to(DEV), w.to(DEV), b.to(DEV))
+    far = (values.abs().unsqueeze(1) * 42 ** 2 * 2.0 ** -48 / 1e-5 ** 0.5).clamp(max=42 * 2.0 ** -14)
+    assert ((y.cpu() - b).abs() <= 1.5 * far + 2.0 ** -23).all()
+    # dy of ones: 1.5 less its mean is what the sum's rounding leaves
+    got = ssm.ssm_layer_norm_bwd(torch.ones(1, dim, device=DEV), w.to(DEV),
+                                 dy=torch.ones(1, dim, device=DEV))
+    assert got["dx"].abs().max() <= 1.5 / 1e-5 ** 0.5 * 64 * 2.0 ** -24
+
+
 def test_not_finite_stays_in_its_row():
     inp, dr, dy = make("bf16", 40, 200, "wbrd", seed=6)
     inp["x"][3, 5], inp["residual"][9, 0] = float("nan"), float("inf")
