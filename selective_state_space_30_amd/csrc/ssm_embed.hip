@@ -86,7 +86,7 @@ constexpr int kOwnTiles = 256;      // tiles up to which the scatter sums the co
 struct SortPass {
   const uint32_t *keys, *pos;  // null in the first pass: the ids themselves
   uint32_t *keys_out, *pos_out;
-  uint32_t *counts;            // (bins, tiles): of each tile, or the places before it
+  uint32_t *counts;            // (tiles, bins): of each tile, or the places before it
   int64_t tiles;
   int shift, bits;
 };
@@ -286,7 +286,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedArgs p, 
 }
 
 // Places before each (tile, bin), in the order of the bins and in each that of
-// the tiles: a workgroup's threads take a bin each, two for every other tile.
+// the tiles.  Two threads have a bin, one the even tiles, one the odd ones; the
+// first of them returns the sum.
 constexpr int kHalves = kSortThreads / kBins;
 __device__ __forceinline__ uint32_t places_before(const SortPass &s, int64_t tile,
                                                   uint32_t (*half)[kBins], uint32_t *buf) {
@@ -324,10 +325,16 @@ __global__ __launch_bounds__(kSortThreads) void embed_offsets_kernel(SortPass s)
   __shared__ uint32_t Buf[kSortWaves];
   uint32_t at = places_before(s, 0, Half, Buf);
   if (threadIdx.x >= kBins) return;
-  for (int64_t t = 0; t < s.tiles; ++t) {
-    const uint32_t c = s.counts[t * kBins + threadIdx.x];
-    s.counts[t * kBins + threadIdx.x] = at;
-    at += c;
+  uint32_t *count = s.counts + threadIdx.x;
+  for (int64_t t0 = 0; t0 < s.tiles; t0 += 16) {
+    uint32_t c[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) c[k] = t0 + k < s.tiles ? count[(t0 + k) * kBins] : 0u;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (t0 + k < s.tiles) count[(t0 + k) * kBins] = at;
+      at += c[k];
+    }
   }
 }
 
