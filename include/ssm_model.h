@@ -51,9 +51,9 @@ int ssm_embed_fwd(const void *ids, const void *weight, int64_t weight_stride, vo
 int ssm_embed_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t dim, size_t *bytes);
 
 /* The gradient of the weight: dweight_v = scale * sum of dy_t over the tokens t
- * with ids_t = v, in the tokens' order as it is cut into runs of a fixed
- * length, in fp32; with SSM_FLAG_ACCUMULATE that sum is added to dweight_v
- * before the rounding.
+ * with ids_t = v, in fp32, in the order of the tokens, cut into runs whose
+ * length and borders follow from the sizes and the ids; with
+ * SSM_FLAG_ACCUMULATE that sum is added to dweight_v before the rounding.
  *  dy         required (tokens, dim), dtype, rows dy_stride apart
  *  dweight    required output (vocab, dim) dense, weight_dtype; every row is
  *             written (0 where no token has the id) unless it is added to;

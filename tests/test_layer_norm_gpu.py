@@ -157,6 +157,20 @@ def test_slices_in_place_and_leading_dimensions(types):
         assert all(torch.equal(a[n], c[n]) for n in a)
 
 
+@pytest.mark.parametrize("types", ["bf16", "wide", "f32"])
+@pytest.mark.parametrize("dim", [1, 3, 37, 1001, 5003, 16383])
+def test_in_place_where_pieces_overlap(types, dim):
+    """A row's last piece begins inside the one before, which another lane or
+    wave may have written already."""
+    inp, _, _ = make(types, 700, dim, "wbr", seed=9)
+    x, res, w, b = (inp[n].to(DEV) for n in ("x", "residual", "weight", "bias"))
+    r, y = ssm.ssm_layer_norm_fwd(x, w, b, residual=res)
+    for _ in range(3):
+        inplace = res.clone()
+        r2, y2 = ssm.ssm_layer_norm_fwd(x, w, b, residual=inplace, r=inplace)
+        assert r2 is inplace and torch.equal(r2, r) and torch.equal(y2, y)
+
+
 def test_from_r_alone():
     """A caller that kept the sum in fp32 gives it as x: the same gradient."""
     inp, dr, dy = make("wide", 50, 640, "wbrd", seed=12)
