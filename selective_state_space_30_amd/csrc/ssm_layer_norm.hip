@@ -205,7 +205,6 @@ __global__ __launch_bounds__(kBound) void layer_norm_bwd_kernel(LayerNormArgs p,
   const int pieces = kP * lanes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * per;
   const float n = static_cast<float>(p.dim);
-  stage_weight<kWhole, kN>(p, Dyn, pieces);
   float gw[kP][kN], gb[kP][kN];
 #pragma unroll
   for (int i = 0; i < kP; ++i)
@@ -245,6 +244,7 @@ __global__ __launch_bounds__(kBound) void layer_norm_bwd_kernel(LayerNormArgs p,
   }
   int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes;
   if (kAhead && row < p.rows) load(row);
+  stage_weight<kWhole, kN>(p, Dyn, pieces);
   for (; row < p.rows; row += step) {
     if (!kAhead) load(row);
     float v[kP][kN];
@@ -338,17 +338,20 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(LayerNormArgs p)
   float *out = blockIdx.y == 0 ? p.dweight : p.dbias;
   if (!out) return;
   const int c = blockIdx.x * 32 + lane;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int kAhead = 8;
+  float acc = 0.0f;
   if (c < p.dim) {
     const float *s = p.parts + static_cast<int64_t>(blockIdx.y) * p.dim + c;
     const int64_t row = 2 * static_cast<int64_t>(p.dim);
-    int w = grp;
-    for (; w + 96 < p.nparts; w += 128)
+    for (int w = grp; w < p.nparts; w += 32 * kAhead) {
+      float v[kAhead];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] += s[(w + 32 * k) * row];
-    for (; w < p.nparts; w += 32) acc[0] += s[w * row];
+      for (int k = 0; k < kAhead; ++k) v[k] = s[(w + 32 * k < p.nparts ? w + 32 * k : w) * row];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) acc += w + 32 * k < p.nparts ? v[k] : 0.0f;
+    }
   }
-  Sums[grp][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  Sums[grp][lane] = acc;
   __syncthreads();
   if (grp == 0 && c < p.dim) {
     float s = 0.0f;
