@@ -50,11 +50,9 @@ Names follow the C ABI:
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import functools
 import inspect
-import operator
 import os
 import threading
 
@@ -1412,29 +1410,30 @@ def _fills_its_memory(t):
     return True
 
 
-_data_ptr, _numel, _is_contiguous, _get_device = (
-    torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.get_device)
-_dtype_of = operator.attrgetter("dtype")
+@functools.lru_cache(maxsize=1)
+def _read_list():
+    """The compiled walk over a list of tensors.  Raises if it is missing: there is
+    no fallback."""
+    try:
+        from . import _ssmtensors
+    except ImportError as e:
+        raise RuntimeError(
+            "_ssmtensors.so cannot be loaded; build it first "
+            "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    return _ssmtensors.tensors
 
 
 def _tensors(ts, name, dev):
-    """Host arrays of the addresses, sizes and types of a list of tensors, and
-    whether all are contiguous."""
-    try:
-        codes = array.array("i", list(map(_CODES.__getitem__, map(_dtype_of, ts))))
-        ptrs = array.array("Q", list(map(_data_ptr, ts)))
-        dense = all(map(_is_contiguous, ts))
-        fine = set(map(_get_device, ts)) <= {dev.index}
-    except (AttributeError, KeyError, TypeError):
-        fine = False
-    if not (fine and dense):
-        dense = _check_tensors(ts, name, dev)
-    return ptrs, array.array("q", list(map(_numel, ts))), codes, dense
+    """Host arrays (bytes) of the addresses, sizes and types of a list of tensors,
+    and whether all are contiguous."""
+    ptrs, sizes, codes, kind = _read_list()(ts, dev.index)
+    if kind != 2:
+        _check_tensors(ts, name, dev)
+    return ptrs, sizes, codes, kind == 2
 
 
 def _check_tensors(ts, name, dev):
-    """Says what is wrong with a list of tensors, or whether all are contiguous."""
-    dense = True
+    """Says what is wrong with a list of tensors that are not all contiguous."""
     for i, t in enumerate(ts):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s[%d] must be a torch.Tensor" % (name, i))
@@ -1442,15 +1441,10 @@ def _check_tensors(ts, name, dev):
             raise TypeError("%s[%d] must be float32 or bfloat16, got %s" % (name, i, t.dtype))
         if t.device != dev:
             raise ValueError("%s[%d] is on %s, expected %s" % (name, i, t.device, dev))
-        if not t.is_contiguous():
-            dense = False
-            if not _fills_its_memory(t):
-                raise ValueError("%s[%d] has gaps between its elements" % (name, i))
-    return dense
-
-
-def _at(a):
-    return a.buffer_info()[0]
+        if t.layout is not torch.strided:
+            raise TypeError("%s[%d] must be strided, got %s" % (name, i, t.layout))
+        if not t.is_contiguous() and not _fills_its_memory(t):
+            raise ValueError("%s[%d] has gaps between its elements" % (name, i))
 
 
 def _grad_device(grads):
@@ -1476,7 +1470,7 @@ def ssm_grad_norm(grads, norm=None, workspace=None, stream=None):
         norm = torch.empty((), dtype=torch.float32, device=dev)
     keep, ws, ws_bytes = _scratch(workspace, ssm_grad_workspace_size(), dev)
     _check(load_library().ssm_grad_norm(
-        _at(ptrs), _at(sizes), _at(codes), len(grads),
+        ptrs, sizes, codes, len(grads),
         _dense(norm, "norm", torch.float32, (), dev), ws, ws_bytes, _raw_stream(dev, stream)))
     return norm
 
@@ -1495,7 +1489,9 @@ def ssm_grad_clip(grads, max_norm, norm=None, out=None, workspace=None,
     ptrs, sizes, codes, dense = _tensors(grads, "grads", dev)
     p_out = p_out_codes = None
     if out is not None:
-        outs, out_sizes, out_codes, out_dense = _tensors(out, "out", dev)
+        if not isinstance(out, (list, tuple)):
+            out = list(out)
+        p_out, out_sizes, p_out_codes, out_dense = _tensors(out, "out", dev)
         if out_sizes != sizes:
             raise ValueError("out must have a tensor of its size for each gradient")
         if not (dense and out_dense):
@@ -1503,7 +1499,6 @@ def ssm_grad_clip(grads, max_norm, norm=None, out=None, workspace=None,
                 if not (g.is_contiguous() and o.is_contiguous()) and (
                         o.shape != g.shape or o.stride() != g.stride()):
                     raise ValueError("out[%d] must have the strides of its gradient" % i)
-        p_out, p_out_codes = _at(outs), _at(out_codes)
     have = norm is not None
     keep, ws, ws_bytes = None, None, 0
     if have:
@@ -1513,6 +1508,6 @@ def ssm_grad_clip(grads, max_norm, norm=None, out=None, workspace=None,
         p_norm = norm.data_ptr()
         keep, ws, ws_bytes = _scratch(workspace, ssm_grad_workspace_size(), dev)
     _check(load_library().ssm_grad_clip(
-        _at(ptrs), _at(sizes), _at(codes), p_out, p_out_codes, len(grads), max_norm, have, p_norm,
-        ws, ws_bytes, _raw_stream(dev, stream)))
+        ptrs, sizes, codes, p_out, p_out_codes, len(grads), max_norm, have, p_norm, ws, ws_bytes,
+        _raw_stream(dev, stream)))
     return norm
