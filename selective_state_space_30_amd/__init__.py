@@ -1263,13 +1263,13 @@ def ssm_embed_fwd(ids, weight, scale=1.0, out=None, dtype=None, stream=None):
 
 @_on_device
 def ssm_embed_bwd(ids, dy, vocab, scale=1.0, dweight=None, accumulate=False,
-                  dtype=torch.float32, workspace=None, stream=None):
+                  dtype=None, workspace=None, stream=None):
     """Gradient of :func:`ssm_embed_fwd`'s weight for a gradient ``dy`` of its
     result (ids.shape + (dim,), float32 or bfloat16, rows may be slices of
     wider ones): dweight[v] = scale * sum of dy[t] where ids[t] = v, in fp32 in
     a fixed order.  ``accumulate`` adds it to the given ``dweight`` (vocab, dim)
-    in place, whose rows without a token are not touched.  ``dtype``: of a new
-    dweight, float32 or bfloat16.  Returns dweight."""
+    in place, whose rows without a token are not touched.  ``dtype``: of
+    dweight, float32 (a new one's by default) or bfloat16.  Returns dweight."""
     p_ids, index = _ids(ids)
     dev, tokens = ids.device, ids.numel()
     if not isinstance(dy, torch.Tensor) or dy.dim() < 1:
@@ -1280,7 +1280,9 @@ def ssm_embed_bwd(ids, dy, vocab, scale=1.0, dweight=None, accumulate=False,
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate needs dweight")
-        dweight = torch.empty((vocab, dim), dtype=dtype, device=dev)
+        dweight = torch.empty((vocab, dim), dtype=dtype or torch.float32, device=dev)
+    elif dtype is not None and dweight.dtype != dtype:
+        raise TypeError("dweight must be %s, got %s" % (dtype, dweight.dtype))
     p_dw = _dense(dweight, "dweight", dweight.dtype, (vocab, dim), dev)
     keep, ws, ws_bytes = _scratch(workspace, ssm_embed_bwd_workspace_size(tokens, vocab, dim), dev)
     _check(load_library().ssm_embed_bwd(
