@@ -433,17 +433,22 @@ int launch_p(const LayerNormArgs &a, const Shape &sh, hipStream_t s) {
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(a.nparts), dim3(sh.threads), weight > sums ? weight : sums, s,
                          a, sh.lanes);
+      return static_cast<int>(hipGetLastError());
     };
-    if (sh.threads <= 256)
-      go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 256>);
-    else
-      go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 512>);
+    // 512 lanes take what 256 hold in no `shared` pieces each (5 of 4 elements, 2
+    // or 3 of 8), so more than half as many; up to 256 take at most `alone` (7 of 4
+    // elements).  No kernel is built for the others.
+    if constexpr (kP <= (kN == 4 ? 7 : 4))
+      if (sh.threads <= 256) return go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 256>);
+    if constexpr (kP > (kN == 4 ? 2 : 1))
+      if (sh.threads > 256) return go(layer_norm_bwd_kernel<T, R, Y, kN, kP, kWhole, 512>);
+    return static_cast<int>(hipErrorInvalidValue);
   } else {
     hipLaunchKernelGGL((layer_norm_fwd_kernel<T, R, Y, kN, kP, kWhole>),
                        dim3(forward_groups(a.rows, sh)),
                        dim3(sh.threads), 0, s, a, sh.lanes);
+    return static_cast<int>(hipGetLastError());
   }
-  return static_cast<int>(hipGetLastError());
 }
 
 template <typename T, typename R, typename Y, int kN, bool kWhole, bool kBack>
