@@ -573,7 +573,8 @@ int ssm_conv_scan_fwd(const void *x, const float *conv_w, const float *conv_b,
                       int64_t requested_chunk, void *workspace,
                       size_t workspace_bytes, void *stream) {
   if (!x) return fail(SSM_ERR_INVALID_ARG, "x is NULL");
-  // More states than one register of lanes holds are not offered here.
+  // No instance with the prologue is built over more states than one register a
+  // lane holds: u formed before and ssm_scan_fwd serve those.
   if (dstate > 64)
     return fail(SSM_ERR_UNSUPPORTED, "the conv prologue supports dstate <= 64 (got %lld)",
                 (long long)dstate);

@@ -676,6 +676,18 @@ __global__ __launch_bounds__(256) void ckpt_fix_kernel(ScanArgs p) {
   *q = fmaf(fast_exp2(Aq * p.ckpt_s[bd * nblk + k]), hin, *q);
 }
 
+using ScanKernel = void (*)(ScanArgs);
+
+// The instance with the conv prologue: none over more states than one register
+// a lane holds, which ssm_conv_scan_fwd refuses.
+template <typename T, bool kVec, bool kSoftplus, bool kZoh, int kN>
+constexpr ScanKernel conv_kernel() {
+  if constexpr (kN == kMaxStates)
+    return nullptr;
+  else
+    return scan_kernel<T, kVec, kSoftplus, true, kZoh, false, kN>;
+}
+
 template <typename T, bool kVec, int kN>
 hipError_t launch_scan_t(const ScanArgs &a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.dim + kChannelsPerGroup - 1) /
@@ -683,27 +695,27 @@ hipError_t launch_scan_t(const ScanArgs &a, hipStream_t s) {
                   static_cast<unsigned>(a.batch),
                   static_cast<unsigned>(a.n_chunks));
   // (conv prologue, softplus, ZOH) -> kernel instance
-  using KernelFn = void (*)(ScanArgs);
-  static constexpr KernelFn kernels[8] = {
+  static constexpr ScanKernel kernels[8] = {
       scan_kernel<T, kVec, false, false, false, false, kN>,
       scan_kernel<T, kVec, true, false, false, false, kN>,
-      scan_kernel<T, kVec, false, true, false, false, kN>,
-      scan_kernel<T, kVec, true, true, false, false, kN>,
+      conv_kernel<T, kVec, false, false, kN>(),
+      conv_kernel<T, kVec, true, false, kN>(),
       scan_kernel<T, kVec, false, false, true, false, kN>,
       scan_kernel<T, kVec, true, false, true, false, kN>,
-      scan_kernel<T, kVec, false, true, true, false, kN>,
-      scan_kernel<T, kVec, true, true, true, false, kN>};
+      conv_kernel<T, kVec, false, true, kN>(),
+      conv_kernel<T, kVec, true, true, kN>()};
   const int which = (a.softplus ? 1 : 0) | (a.x ? 2 : 0) | (a.zoh ? 4 : 0);
   // the backward's checkpoint pass (no conv prologue) has instances of its
   // own, so the forward instances carry none of its code
-  static constexpr KernelFn ckpt_kernels[4] = {
+  static constexpr ScanKernel ckpt_kernels[4] = {
       scan_kernel<T, kVec, false, false, false, true, kN>,
       scan_kernel<T, kVec, true, false, false, true, kN>,
       scan_kernel<T, kVec, false, false, true, true, kN>,
       scan_kernel<T, kVec, true, false, true, true, kN>};
-  hipLaunchKernelGGL(a.ckpt ? ckpt_kernels[(a.softplus ? 1 : 0) | (a.zoh ? 2 : 0)]
-                            : kernels[which], grid,
-                     dim3(kWaveLanes * kWavesPerGroup), 0, s, a);
+  const ScanKernel kernel =
+      a.ckpt ? ckpt_kernels[(a.softplus ? 1 : 0) | (a.zoh ? 2 : 0)] : kernels[which];
+  if (!kernel) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kernel, grid, dim3(kWaveLanes * kWavesPerGroup), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_chunks == 1) return e;
   const int64_t nthreads = a.batch * a.dim * a.N;
