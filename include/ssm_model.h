@@ -47,7 +47,8 @@ int ssm_embed_fwd(const void *ids, const void *weight, int64_t weight_stride, vo
                   int64_t tokens, int64_t vocab, int64_t dim, float scale, int index_type,
                   int weight_dtype, int dtype, void *stream);
 
-/* Bytes of device workspace for ssm_embed_bwd. */
+/* Bytes of device workspace for ssm_embed_bwd.  vocab is checked; the size does
+ * not depend on it in this build. */
 int ssm_embed_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t dim, size_t *bytes);
 
 /* The gradient of the weight: dweight_v = scale * sum of dy_t over the tokens t
@@ -72,7 +73,9 @@ int ssm_embed_bwd(const void *ids, const void *dy, int64_t dy_stride, void *dwei
  *   r = x + residual                       (without a residual: r = x)
  *   y = (r - mean(r)) / sqrt(var(r) + eps) * weight + bias
  * with var the mean of the squared differences from the mean, formed from the
- * differences themselves.  y is formed from r before r is rounded.
+ * differences themselves.  y is formed from r before r is rounded.  Where the
+ * squares pass fp32's largest number (differences over about 1.8e19) the variance
+ * is infinite, and y the bias.
  * (ssm_block_norm_fwd, ssm_linattn.h, has the norm without mean and bias.)
  *  x         required, x_dtype (rows, dim), rows x_stride apart
  *  residual  nullable, residual_dtype (rows, dim), rows residual_stride apart

@@ -4,7 +4,7 @@
 //   dweight_v (+)= scale sum_{t: ids_t = v} dy_t
 //
 // The gradient sorts the tokens by their id (a stable radix sort of (id,
-// token) pairs, 8 bits a pass, so that tokens of one id stay in order) and
+// token) pairs, digits of up to 9 bits, so that tokens of one id stay in order) and
 // cuts the sorted list into runs of equal length.  A wave sums one run's rows
 // of dy, for the columns that its lanes hold, and writes the sum of every id
 // that begins and ends in the run; the sums of ids that go on over a run's end
@@ -820,7 +820,7 @@ int launch_fwd(const EmbedArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int64_t embed_bwd_workspace(int64_t tokens, int64_t, int64_t dim) {
+int64_t embed_bwd_workspace(int64_t tokens, int64_t dim) {
   return tokens <= kFew ? 0 : layout_of(tokens, dim).bytes;
 }
 

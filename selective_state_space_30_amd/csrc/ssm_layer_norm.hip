@@ -12,7 +12,7 @@
 // elements each: 8 to 64 lanes of a wave, whose sums need no barrier, or a
 // workgroup of up to 8 waves, whose sums meet in LDS.  The mean is formed
 // first and the squares from the differences, so that a mean far from 0 costs
-// no digits.
+// only the digits that fp32 does not hold beside it.
 #include "ssm_model_internal.h"
 #include "ssm_pieces.h"
 
@@ -73,10 +73,13 @@ __device__ __forceinline__ void store_at(bool whole, T *row, int q, int dim, con
 
 // r - mean in v (0 behind the row's end), and s.  The mean of the differences,
 // which is what the first mean's rounding left, is taken from both.  In a row of
-// one value nothing else is left, and the difference of two sums that is the
-// variance could come out below 0: it is at least 2^-20 of the first of them,
-// which is more than it rounds by, and leaves (the differences round to 42 * 2^-24
-// of what was taken from them) at most 42 * 2^-14 of any such row.  (A third sum,
+// one value nothing else is left, and the difference of two equal sums that is the
+// variance comes out as their roundings, below 0 as well (up to 42 additions each,
+// 2^-24 an addition).  It is held at 2^-20 of the first sum, which is not more than
+// they can round by, but is positive and leaves (the differences round to 42 *
+// 2^-24 of what was taken from them) at most 42 * 2^-14 of any such row.  It matters
+// where a row spreads by less than 2^-10 of what the first mean was off by, which
+// is less than 42 * 2^-34 of that mean.  (A third sum,
 // over the differences of the differences, cost the backward pass 10 % at rows of
 // 2560 in bf16 and 19 % at rows of 8192: its registers.)
 template <int kP, int kN, bool kWhole>
@@ -113,8 +116,9 @@ __device__ __forceinline__ float centre(float (&v)[kP][kN], const LayerNormArgs 
 
 // Bound by memory, the weights in registers over the group's rows.  16384 rows
 // of 2560, bf16 with an fp32 residual, 97 us (503 MB, 5.2 TB/s, as a large
-// copy); 65536 of 768, all bf16, 75 us (5.4 TB/s); with the weights read for each
-// row 113 us.  8 rows of 2560: 4 us, a call 9.3 us on the host.
+// copy); 65536 of 768, all bf16, 66 us in a training step (403 MB, 6.1 TB/s: some of
+// it is in the last-level cache; 75 us by itself).  With the weights read for each
+// row the first took 113 us.  8 rows of 2560: 4 us, a call 9.3 us on the host.
 template <typename T, typename R, typename Y, int kN, int kP, bool kWhole>
 __global__ __launch_bounds__(512) void layer_norm_fwd_kernel(LayerNormArgs p, int lanes) {
   __shared__ float Buf[2][8][2];
@@ -191,8 +195,8 @@ __device__ __forceinline__ void stage_weight(const LayerNormArgs &p, float *W, i
 // from LDS for each row: in registers it does not fit beside them.  8192 rows of
 // 2560, bf16 with an fp32 residual, 83 us (377 MB, 4.6 TB/s; 107 us without the
 // next row asked for ahead, 143 us with the weight in registers, which spilled);
-// vector instructions are issued 42 % of the time.  65536 of 768, all bf16, 106
-// us (503 MB, 4.7 TB/s).  Rows over 8192 elements find no registers for the next
+// vector instructions are issued 42 % of the time.  65536 of 768, all bf16, 118
+// us in a training step (503 MB, 4.3 TB/s; 106 us by itself).  Rows over 8192 elements find no registers for the next
 // row, nor in part for their own: 2048 of 16384, bf16, 111 us (336 MB, 3.0 TB/s;
 // with 1024 threads, which spill more, the same).
 template <typename T, typename R, typename Y, int kN, int kP, bool kWhole, int kBound>
@@ -377,7 +381,9 @@ struct Shape {
 // (forward, bf16: 8192 x 5120 with 128 and 256 lanes 77 and 65 us, 4096 x 8192
 // with 256 and 512 lanes 57 and 52 us; backward: 8192 x 4096 with 128 and 256
 // lanes 85 and 78 us, 8192 x 2560 with an fp32 residual with 64, 128 and 256
-// lanes 86, 87 and 82 us).
+// lanes 86, 87 and 82 us).  The limits of fp32 rows (pieces of 4) are about the same
+// elements a lane, and were held against others at one size only (2003 x 1537,
+// backward, with 1 to 4 pieces 24 to 28 us, with 7 24 us).
 Shape shape_of(int dim, int n, int alone, int shared) {
   const int pieces = (dim + n - 1) / n;
   auto per = [&](int lanes) { return (pieces + lanes - 1) / lanes; };
@@ -417,7 +423,8 @@ int forward_groups(int64_t rows, const Shape &sh) {
 // wave; two where they fit into the registers and it does not.  (bf16, one and
 // two: 32768 x 1024 69 and 73 us, 65536 x 768 105 and 109; 8192 x 4096 94 and
 // 78, 30000 x 1100 95 and 76, 8192 x 2560 76 and 58; with an fp32 residual 8192
-// x 2560 103 and 83.)
+// x 2560 103 and 83.  fp32 rows take the limit of those with an fp32 residual,
+// not measured by themselves.)
 int back_groups(int64_t rows, const Shape &sh, LayerNormTypes types) {
   const int held = sh.per * (types == kLnF32 ? 4 : 8);
   const bool fit = held <= (types == kLnBf16 ? 24 : 16) && sh.threads <= 256;

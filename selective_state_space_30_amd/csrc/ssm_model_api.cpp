@@ -376,7 +376,7 @@ int ssm_embed_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t dim, siz
   if (!bytes) return fail(SSM_ERR_INVALID_ARG, "bytes is NULL");
   const int st = check_embed_sizes(tokens, vocab, dim);
   if (st != SSM_OK) return st;
-  *bytes = static_cast<size_t>(ssm::embed_bwd_workspace(tokens, vocab, dim));
+  *bytes = static_cast<size_t>(ssm::embed_bwd_workspace(tokens, dim));
   return ok();
 }
 
@@ -391,7 +391,7 @@ int ssm_embed_bwd(const void *ids, const void *dy, int64_t dy_stride, void *dwei
   if ((tokens > 0 && !dy) || !dweight) return fail(SSM_ERR_INVALID_ARG, "dy or dweight is NULL");
   if (!aligned(dweight, size_of(weight_dtype)))
     return fail(SSM_ERR_INVALID_ARG, "dweight=%p not aligned", dweight);
-  const int64_t need = ssm::embed_bwd_workspace(tokens, vocab, dim);
+  const int64_t need = ssm::embed_bwd_workspace(tokens, dim);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != SSM_OK) return st;
   const Span ins[] = {{ids, tokens * (index_type == SSM_INDEX_I64 ? 8 : 4), "ids"},
                       {dy, span_of(tokens, dy_stride, dim, dtype), "dy"}};

@@ -29,8 +29,8 @@ struct EmbedArgs {
   void *workspace;
 };
 
-int64_t embed_bwd_workspace(int64_t tokens, int64_t vocab, int64_t dim);
-// wdtype_bf16: of weight or dweight; bf16: of out or dy
+int64_t embed_bwd_workspace(int64_t tokens, int64_t dim);
+// w_bf16: of weight or dweight; bf16: of out or dy
 int launch_embed_fwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream);
 int launch_embed_bwd(const EmbedArgs &a, bool w_bf16, bool bf16, void *stream);
 
